@@ -112,6 +112,20 @@ typedef struct moe_expert_weights {
     const uint8_t *w_down; const float *s_down;
 } moe_expert_weights;
 
+/* element types of the calls that take a dtype */
+#define MOE_DTYPE_F32  0
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F16  2
+
+/* Expert weights in MXFP4 (see moe_quantize_mxfp4), row major over all experts:
+ *   w_gate, w_up [E][F][H/2] u8    s_gate, s_up [E][F][H/32] u8
+ *   w_down       [E][H][F/2] u8    s_down       [E][H][F/32] u8 */
+typedef struct moe_expert_mxfp4 {
+    const uint8_t *w_gate, *s_gate;
+    const uint8_t *w_up, *s_up;
+    const uint8_t *w_down, *s_down;
+} moe_expert_mxfp4;
+
 /* Optional probes of moe_expert_ffn (device pointers, each nullable), indexed
  * by pair p in permuted order (p < offsets[E]):
  *   acc_gate, acc_up [P][F][H/64] int32: per-group sum (u - 8) * xq
@@ -187,6 +201,90 @@ int moe_quantize_int4_gs64(const float *w, int rows, int K, uint8_t *packed, flo
  * MOE_ERR_SHAPE for rows < 0 or a bad K.  Asynchronous on stream. */
 int moe_quantize_int3_g64(const float *w, int rows, int K, uint8_t *packed, float *scales,
                           void *stream);
+
+/* Rows to MXFP4, the microscaled 4-bit floating point of the OCP Microscaling
+ * Formats specification 1.0 that some checkpoints hold their experts in
+ * ["colibri 开发演进实录": the DeepSeek V4 and Kimi K3 engines' fp4 weights].
+ *   x [rows][K], dtype fp32, bf16 or fp16, ldx elements between rows (ldx >= K,
+ *   rows 16-byte aligned), K a multiple of 32 in [32, 65536], rows <= 2^27.
+ *   codes [rows][K/2] u8 and scales [rows][K/32] u8 (16-byte aligned), written
+ *   in full.  Per block of 32 values: e = floor(log2(amax)) - 2, no less than
+ *   -127; scale byte e + 127; code = the e2m1 value (sign in bit 3; 0, .5, 1,
+ *   1.5, 2, 3, 4, 6) nearest to x / 2^e, ties to the even code, magnitudes above
+ *   6 held as 6.  Byte j = element 2j (low nibble) | element 2j+1 (high).  A
+ *   block of zeros: scale 0, codes 0.  A block with a NaN or an infinity: scale
+ *   255 (NaN), codes 0.  Inputs need not be finite here.
+ * Asynchronous on stream, no workspace. */
+int moe_quantize_mxfp4(const void *x, int dtype, long long ldx, long long rows, int K,
+                       uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values that MXFP4 rows stand for: y [rows][K] (dense) of `dtype`, the exact
+ * value rounded once to that type (fp32 and bf16 hold every value from 2^-126 up
+ * exactly; fp16 overflows to infinity).  A block with scale 255 becomes NaN. */
+int moe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K,
+                         void *y, int dtype, void *stream);
+
+/* Product of MXFP4 rows with MXFP4 weights, by group (expert):
+ *   y[p][n] = sum_k x[p][k] * w[g][n][k]  for offsets[g] <= p < offsets[g+1]
+ *   x, x_scales: `rows` rows of K; w, w_scales: `groups` x N rows of K, both as
+ *   moe_quantize_mxfp4 writes them.  y [rows][N] of `dtype`, fp32 sums rounded
+ *   once; rows outside every group are left untouched.
+ *   offsets [groups+1] int32 (device), in order within [0, rows], as moe_permute
+ *   writes it; NULL (one group only) means all rows.  A group whose offsets are
+ *   out of order or past the rows is skipped and recorded (moe_check_errors).
+ *   1 <= groups <= 512, 1 <= N <= 2^20, groups * N <= 2^27.
+ *   workspace: 256 bytes (the error word), zeroed once before its first use.
+ * A NaN block (scale 255) makes the outputs that read it NaN and no others. */
+int moe_mxfp4_matmul(const uint8_t *x, const uint8_t *x_scales, int rows, const uint8_t *w,
+                     const uint8_t *w_scales, int groups, const int32_t *offsets, int N, int K,
+                     void *y, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Routed expert FFN on MXFP4 weights over a permutation: moe_expert_ffn's
+ * counterpart for such checkpoints.  Every pair p of expert e and token t = tok[p]:
+ *   h = q(silu(q(x_t) Wg[e]^T) * (q(x_t) Wu[e]^T)),  y_pairs[p] = h Wd[e]^T
+ * q: moe_quantize_mxfp4; sums and silu in fp32.
+ *   x [T][H] of x_dtype; y_pairs [T*K][H] of y_dtype (fp32 for moe_combine); rows
+ *   >= offsets[E] are left untouched.  cfg gives hidden, n_experts, top_k, d_ff.
+ *   offsets, tok as moe_permute writes them; both NULL (n_experts = top_k = 1)
+ *   runs every token through the one expert: a shared expert or a dense layer.
+ *   A token index outside [0, T) makes its pair NaN and is recorded.
+ *   workspace: moe_mxfp4_workspace_size(cfg, T) bytes, first 256 zeroed once. */
+int moe_mxfp4_expert_ffn(const moe_config *cfg, const void *x, int x_dtype, int T,
+                         const moe_expert_mxfp4 *w, const int32_t *offsets, const int32_t *tok,
+                         void *y_pairs, int y_dtype, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* Bytes of workspace moe_mxfp4_expert_ffn needs for up to max_tokens tokens; 0
+ * for an invalid config or count. */
+size_t moe_mxfp4_workspace_size(const moe_config *cfg, int max_tokens);
+
+/* Dense gated block in 16 bits, the trainable form of a dense layer or a shared
+ * expert ["MoE 路由与专家流式加载" §1.4, §2: dense layers before the sparse ones]:
+ *   g = x w_gate^T, u = x w_up^T, h = silu(g) * u      (sums and silu in fp32)
+ *   x [T][H] with ldx elements between rows, w_gate, w_up [F][H], h [T][F], all
+ *   bf16 or all fp16 (dtype).  g, u [T][F]: kept for moe_gated_backward, rounded
+ *   to dtype; both NULL when no gradient is wanted.
+ *   H, F multiples of 8 in [8, 65536], T in [0, 2^24], rows of x 16-byte aligned.
+ *   workspace: moe_gated_workspace_size(T, H, F, 0) bytes, first 256 zeroed once. */
+int moe_gated_forward(const void *x, long long ldx, const void *w_gate, const void *w_up, int dtype,
+                      int T, int H, int F, void *h, void *g, void *u, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Gradients of the gated block from dh [T][F] and the g, u that the forward pass
+ * kept: with s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s (rounded to
+ * dtype as the products' operands),
+ *   dx = dg w_gate + du w_up [T][H],  dw_gate = dg^T x, dw_up = du^T x [F][H]
+ * written in full (not accumulated).  dx, or both weight gradients, may be NULL.
+ * T = 0 zeroes the weight gradients.  workspace: moe_gated_workspace_size(T, H,
+ * F, 1) bytes, first 256 zeroed once. */
+int moe_gated_backward(const void *dh, const void *x, long long ldx, const void *w_gate,
+                       const void *w_up, const void *g, const void *u, int dtype, int T, int H,
+                       int F, void *dx, void *dw_gate, void *dw_up, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of the gated block's calls (train = 0: forward alone); 0
+ * for sizes outside the limits. */
+size_t moe_gated_workspace_size(int T, int H, int F, int train);
 
 /* Diagnostic of the error path of the kernels' bounded device-side waits:
  * one CTA polls, `polls` times (1 .. 2^24), an mbarrier that nothing arrives

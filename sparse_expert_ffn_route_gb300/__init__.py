@@ -14,4 +14,8 @@ from .binding import (EXPORTS, LIBRARY_PATH, MOE_ERR_ALIGN, MOE_ERR_ARG, MOE_ERR
                       moe_workspace_size, moe_ffn_uses_tensor_cores,
                       moe_route_lookahead, moe_topk_hits, moe_quantize_int4_gs64, moe_quantize_int3_g64,
                       moe_selftest_wait_timeout, moe_layer_forward_host, moe_ffn_path,
-                      moe_ffn_path_down)
+                      moe_ffn_path_down, MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, ExpertMxfp4,
+                      alloc_gated_workspace, alloc_mxfp4_matmul_workspace, alloc_mxfp4_workspace,
+                      moe_dequantize_mxfp4, moe_gated_backward, moe_gated_forward,
+                      moe_gated_workspace_size, moe_mxfp4_expert_ffn, moe_mxfp4_matmul,
+                      moe_mxfp4_workspace_size, moe_quantize_mxfp4)

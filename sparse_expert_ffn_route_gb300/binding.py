@@ -31,6 +31,9 @@ MOE_FLAG_STAGE_EVENTS = 2
 MOE_FFN_WARP_GEMV = 0
 MOE_FFN_TENSOR = 1
 MOE_FFN_ROW_GEMV = 2
+MOE_DTYPE_F32 = 0
+MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F16 = 2
 STAGES = ("router", "select", "permute", "plan", "quant", "gate_up", "quant_h", "down", "combine")
 
 # every symbol include/moe.h declares
@@ -39,7 +42,10 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_expert_ffn", "
            "moe_route_noalloc", "moe_ffn_uses_tensor_cores", "moe_route_lookahead",
            "moe_topk_hits", "moe_quantize_int4_gs64", "moe_quantize_int3_g64",
            "moe_selftest_wait_timeout",
-           "moe_layer_forward_host", "moe_ffn_path", "moe_ffn_path_down")
+           "moe_layer_forward_host", "moe_ffn_path", "moe_ffn_path_down",
+           "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_mxfp4_matmul", "moe_mxfp4_expert_ffn",
+           "moe_mxfp4_workspace_size", "moe_gated_forward", "moe_gated_backward",
+           "moe_gated_workspace_size")
 
 
 class MoeError(RuntimeError):
@@ -70,6 +76,12 @@ class ExpertWeights(ctypes.Structure):
     @classmethod
     def of(cls, d: Dict[str, torch.Tensor]) -> "ExpertWeights":
         return cls(*[_ptr(d[k]) for k in ("w_gate", "s_gate", "w_up", "s_up", "w_down", "s_down")])
+
+
+class ExpertMxfp4(ctypes.Structure):
+    _fields_ = [("w_gate", ctypes.c_void_p), ("s_gate", ctypes.c_void_p),
+                ("w_up", ctypes.c_void_p), ("s_up", ctypes.c_void_p),
+                ("w_down", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
 
 
 class FfnProbe(ctypes.Structure):
@@ -117,6 +129,18 @@ def load_library():
     L.moe_check_errors.argtypes = [vp, sz, vp]
     L.moe_stage_times.argtypes = [vp, vp, i32]
     L.moe_route_noalloc.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp]
+    i64 = ctypes.c_longlong
+    L.moe_quantize_mxfp4.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+    L.moe_dequantize_mxfp4.argtypes = [vp, vp, i64, i32, vp, i32, vp]
+    L.moe_mxfp4_matmul.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, i32, vp, i32, vp, sz, vp]
+    L.moe_mxfp4_expert_ffn.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.moe_mxfp4_workspace_size.argtypes = [vp, i32]
+    L.moe_mxfp4_workspace_size.restype = sz
+    L.moe_gated_forward.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.moe_gated_backward.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp,
+                                     sz, vp]
+    L.moe_gated_workspace_size.argtypes = [i32, i32, i32, i32]
+    L.moe_gated_workspace_size.restype = sz
     L.moe_last_error_string.argtypes = []
     L.moe_last_error_string.restype = ctypes.c_char_p
     _lib = L
@@ -314,3 +338,148 @@ def moe_stage_times(reset: bool = True):
     n = (ctypes.c_longlong * len(STAGES))()
     _check(load_library().moe_stage_times(ms, n, 1 if reset else 0), "moe_stage_times")
     return {name: (ms[i], int(n[i])) for i, name in enumerate(STAGES)}
+
+
+# --- MXFP4 and the 16-bit gated block ----------------------------------------------------
+# These check what the C entry points cannot see: types, shapes and strides of the tensors.
+_DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32, bfloat16 or float16 (got %s)" % (name, t.dtype))
+    return code
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype) -> int:
+    """Device pointer of a contiguous CUDA tensor of the given shape and type."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s must be a contiguous CUDA tensor %s of %s (got %s of %s%s)" % (
+            name, shape, dtype, tuple(t.shape), t.dtype, "" if t.is_contiguous() else ", strided"))
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, width, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError("%s must be a 2-D CUDA tensor" % name)
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError("rows of %s must be contiguous" % name)
+    return rows, width, (t.stride(0) if rows > 1 else width)
+
+
+def moe_quantize_mxfp4(x, codes, scales, stream=None):
+    """Rows x [rows][K] (float32, bfloat16 or float16; K a multiple of 32, rows may be strided)
+    -> MXFP4: codes [rows][K/2] uint8 and scales [rows][K/32] uint8.  A contiguous x of more
+    dimensions is taken as its rows laid end to end."""
+    if x.dim() != 2 and x.is_contiguous() and x.dim() > 0:
+        K = x.shape[-1]
+        x = x.view(-1, K)
+        codes, scales = codes.view(-1, codes.shape[-1]), scales.view(-1, scales.shape[-1])
+    rows, K, ld = _rows(x, "x")
+    _check(load_library().moe_quantize_mxfp4(
+        x.data_ptr(), _dtype(x, "x"), ld, rows, K, _dense(codes, "codes", (rows, K // 2), torch.uint8),
+        _dense(scales, "scales", (rows, K // 32), torch.uint8), _stream(stream)), "moe_quantize_mxfp4")
+
+
+def moe_dequantize_mxfp4(codes, scales, y, stream=None):
+    """The values that MXFP4 codes [..][K/2] and scales [..][K/32] stand for, into y [..][K]."""
+    K = y.shape[-1]
+    rows, lead = (y.numel() // K if K else 0), tuple(y.shape[:-1])
+    _check(load_library().moe_dequantize_mxfp4(
+        _dense(codes, "codes", lead + (K // 2,), torch.uint8),
+        _dense(scales, "scales", lead + (K // 32,), torch.uint8), rows, K,
+        _dense(y, "y", lead + (K,), y.dtype), _dtype(y, "y"), _stream(stream)), "moe_dequantize_mxfp4")
+
+
+def alloc_mxfp4_matmul_workspace(device="cuda") -> torch.Tensor:
+    """Zeroed workspace of moe_mxfp4_matmul (the error word)."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def moe_mxfp4_matmul(x, x_scales, w, w_scales, y, workspace, offsets=None, stream=None):
+    """y [rows][N] = x w^T by group: x [rows][K/2], x_scales [rows][K/32]; w [groups][N][K/2] (or
+    [N][K/2]), w_scales alike; offsets [groups + 1] int32 (None: one group, all rows)."""
+    rows, half = x.shape
+    groups, N = (1, w.shape[0]) if w.dim() == 2 else w.shape[:2]
+    K, u8, lead = 2 * half, torch.uint8, tuple(w.shape[:-1])
+    _check(load_library().moe_mxfp4_matmul(
+        _dense(x, "x", (rows, half), u8), _dense(x_scales, "x_scales", (rows, K // 32), u8), rows,
+        _dense(w, "w", lead + (half,), u8), _dense(w_scales, "w_scales", lead + (K // 32,), u8), groups,
+        None if offsets is None else _dense(offsets, "offsets", (groups + 1,), torch.int32), N, K,
+        _dense(y, "y", (rows, N), y.dtype), _dtype(y, "y"), _ptr(workspace), workspace.numel(),
+        _stream(stream)), "moe_mxfp4_matmul")
+
+
+def moe_mxfp4_workspace_size(cfg: MoeConfig, max_tokens: int) -> int:
+    return int(load_library().moe_mxfp4_workspace_size(ctypes.byref(cfg), max_tokens))
+
+
+def alloc_mxfp4_workspace(cfg: MoeConfig, max_tokens: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_mxfp4_expert_ffn for up to ``max_tokens`` tokens, its head zeroed."""
+    n = moe_mxfp4_workspace_size(cfg, max_tokens)
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_mxfp4_workspace_size", "invalid config or token count")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_mxfp4_expert_ffn(cfg, x, weights: Dict[str, torch.Tensor], y_pairs, workspace, offsets=None,
+                         tok=None, stream=None):
+    """Routed expert FFN on MXFP4 weights: x [T][H] -> y_pairs [T * top_k][H] in the order of
+    offsets / tok (as moe_permute writes them; both None: one expert, every token).  weights:
+    w_gate, w_up [E][F][H/2], w_down [E][H][F/2] and s_gate, s_up [E][F][H/32],
+    s_down [E][H][F/32], uint8."""
+    T, H, F, E, u8 = x.shape[0], cfg.hidden, cfg.d_ff, cfg.n_experts, torch.uint8
+    shapes = {"w_gate": (E, F, H // 2), "s_gate": (E, F, H // 32), "w_up": (E, F, H // 2),
+              "s_up": (E, F, H // 32), "w_down": (E, H, F // 2), "s_down": (E, H, F // 32)}
+    w = ExpertMxfp4(*[_dense(weights[k], k, s, u8) for k, s in shapes.items()])
+    _check(load_library().moe_mxfp4_expert_ffn(
+        ctypes.byref(cfg), _dense(x, "x", (T, H), x.dtype), _dtype(x, "x"), T, ctypes.byref(w),
+        None if offsets is None else _dense(offsets, "offsets", (E + 1,), torch.int32),
+        None if tok is None else _dense(tok, "tok", (T * cfg.top_k,), torch.int32),
+        _dense(y_pairs, "y_pairs", (T * cfg.top_k, H), y_pairs.dtype), _dtype(y_pairs, "y_pairs"),
+        _ptr(workspace), workspace.numel(), _stream(stream)), "moe_mxfp4_expert_ffn")
+
+
+def moe_gated_workspace_size(T: int, H: int, F: int, train: bool) -> int:
+    return int(load_library().moe_gated_workspace_size(T, H, F, 1 if train else 0))
+
+
+def alloc_gated_workspace(T: int, H: int, F: int, train: bool, device="cuda") -> torch.Tensor:
+    """Workspace of the gated block's calls for T tokens, its head zeroed."""
+    n = moe_gated_workspace_size(T, H, F, train)
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_gated_workspace_size", "sizes outside the limits")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_gated_forward(x, w_gate, w_up, h, workspace, g=None, u=None, stream=None):
+    """h [T][F] = silu(x w_gate^T) * (x w_up^T), all bfloat16 or all float16; g, u [T][F] keep the
+    two products for moe_gated_backward.  Rows of x [T][H] may be strided."""
+    T, H, ld = _rows(x, "x")
+    F, dt = w_gate.shape[0], x.dtype
+    _check(load_library().moe_gated_forward(
+        x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt), _dense(w_up, "w_up", (F, H), dt),
+        _dtype(x, "x"), T, H, F, _dense(h, "h", (T, F), dt),
+        None if g is None else _dense(g, "g", (T, F), dt), None if u is None else _dense(u, "u", (T, F), dt),
+        _ptr(workspace), workspace.numel(), _stream(stream)), "moe_gated_forward")
+
+
+def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace, stream=None):
+    """Gradients of moe_gated_forward from dh [T][F] and the kept g, u: dx [T][H] (or None) and
+    dw_gate, dw_up [F][H] (or both None), written in full."""
+    T, H, ld = _rows(x, "x")
+    F, dt = w_gate.shape[0], x.dtype
+    opt = lambda t, name, shape: None if t is None else _dense(t, name, shape, dt)  # noqa: E731
+    _check(load_library().moe_gated_backward(
+        _dense(dh, "dh", (T, F), dt), x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt),
+        _dense(w_up, "w_up", (F, H), dt), _dense(g, "g", (T, F), dt), _dense(u, "u", (T, F), dt),
+        _dtype(x, "x"), T, H, F, opt(dx, "dx", (T, H)), opt(dw_gate, "dw_gate", (F, H)),
+        opt(dw_up, "dw_up", (F, H)), _ptr(workspace), workspace.numel(), _stream(stream)),
+        "moe_gated_backward")

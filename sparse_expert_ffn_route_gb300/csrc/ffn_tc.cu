@@ -46,6 +46,7 @@
 #include "launch.cuh"
 #include "moe_internal.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace moe {
 
@@ -536,8 +537,6 @@ bool ffn_tc_supported(const FfnArgs &a)
 
 size_t ffn_tc_smem_bytes() { return kSmemBytes; }
 
-namespace {
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static std::once_flag once;
@@ -552,6 +551,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     });
     return fn;
 }
+
+namespace {
 
 // Tensor map of a [rows][ld] bf16 matrix of which the first `cols` columns are read: boxes of
 // 64 columns (128 bytes) x box_rows rows, 128-byte swizzle, rows past the end read as zero.

@@ -1,0 +1,281 @@
+// gated.cu -- the dense gated block in 16 bits, h = silu(x Wg^T) * (x Wu^T), and its gradients:
+// launches of the products (kernel: gemm_tc.cuh), the elementwise pass between them, and the
+// entry points.
+//
+// With s = sigmoid(g):  dg = dh u s (1 + g (1 - s)),  du = dh g s,
+//   dx = dg Wg + du Wu,   dWg = dg^T x,   dWu = du^T x.
+//
+// Roundings to 16 bits besides the outputs': g and u, kept by the forward pass for the
+// backward one (their half step is the outputs' own; keeping fp32 would double what both
+// passes move), and dg and du, the operands of the tensor-core products.  Everything else is
+// fp32.
+#include <algorithm>
+
+#include "gemm_tc.cuh"
+#include "tensor_map.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace gemm;
+
+// fp32 sums, operands bf16 or fp16, 128 lanes
+uint32_t idesc16(int dtype, bool a_mn, bool b_mn)
+{
+    const uint32_t f = dtype == MOE_DTYPE_BF16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(kM >> 4) << 24);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v)
+{
+    return __bfloat162float(v);
+}
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v)
+{
+    return __half2float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v)
+{
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v)
+{
+    return __float2half_rn(v);
+}
+
+// dg, du from dh, g, u, 8 values a thread (F is a multiple of 8, so the rows laid end to end are)
+template <typename T>
+__global__ void __launch_bounds__(256)
+    gated_grad_kernel(const T *__restrict__ dh, const T *__restrict__ g, const T *__restrict__ u, long long units,
+                      T *__restrict__ dg, T *__restrict__ du)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= units) return;
+    union Pack {
+        uint4 v;
+        T t[8];
+    } a, b, c, p, q;
+    a.v = ld_stream_v4(reinterpret_cast<const uint4 *>(dh) + i);
+    b.v = ld_stream_v4(reinterpret_cast<const uint4 *>(g) + i);
+    c.v = ld_stream_v4(reinterpret_cast<const uint4 *>(u) + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float d = to_f(a.t[j]), gg = to_f(b.t[j]), uu = to_f(c.t[j]);
+        const float s = 1.0f / (1.0f + expf(-gg));
+        p.t[j] = from_f<T>(d * uu * s * (1.0f + gg * (1.0f - s)));
+        q.t[j] = from_f<T>(d * gg * s);
+    }
+    reinterpret_cast<uint4 *>(dg)[i] = p.v;
+    reinterpret_cast<uint4 *>(du)[i] = q.v;
+}
+
+cudaError_t box_maps(CUtensorMap (&m)[kBoxMaps], const void *b, int cols, long long ld, int rows)
+{
+    cudaError_t e = cudaSuccess;
+    for (int k = 0; k < kBoxMaps && e == cudaSuccess; ++k) e = rows_map(&m[k], b, 16, cols, ld, rows, 16 << k);
+    return e;
+}
+
+cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,
+                    void *h, void *g, void *u, int32_t *err, cudaStream_t st)
+{
+    Maps m;
+    cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, kM);
+    if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, kM);
+    if (e == cudaSuccess) e = box_maps(m.b[0], x, H, ldx, T);
+    if (e != cudaSuccess) return e;
+    Args a = {};
+    a.E = 1;
+    a.rows = T;
+    a.M = F;
+    a.ksteps = a.kphase = (H + 63) / 64;
+    a.out[0] = h;
+    a.out[1] = g;
+    a.out[2] = u;
+    a.ld = F;
+    a.dtype = dtype;
+    a.idesc = idesc16(dtype, false, false);
+    a.err = err;
+    const int sms = num_sms(), mtiles = (F + kM - 1) / kM;
+    if (T <= 32) {
+        // one column chunk: a cluster a tile while tiles are fewer than SMs
+        a.split = std::max(1, std::min({8, sms / mtiles, a.ksteps}));
+        return launch<kGate, 32>(a, m, std::min(mtiles, sms / a.split) * a.split, st);
+    }
+    a.split = 1;
+    return launch<kGate, 256>(a, m, (int)std::min<long long>((long long)mtiles * ((T + 255) / 256), sms), st);
+}
+
+cudaError_t grad_x(const void *dg, const void *du, const void *wg, const void *wu, int dtype, int T, int H, int F,
+                   void *dx, int32_t *err, cudaStream_t st)
+{
+    Maps m;
+    cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, 64);
+    if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, 64);
+    if (e == cudaSuccess) e = box_maps(m.b[0], dg, F, F, T);
+    if (e == cudaSuccess) e = box_maps(m.b[1], du, F, F, T);
+    if (e != cudaSuccess) return e;
+    Args a = {};
+    a.E = 1;
+    a.rows = T;
+    a.M = H;
+    a.kphase = (F + 63) / 64;
+    a.ksteps = 2 * a.kphase;
+    a.split = 1;
+    a.out[0] = dx;
+    a.ld = H;
+    a.dtype = dtype;
+    a.idesc = idesc16(dtype, true, false);
+    a.err = err;
+    const long long tiles = (long long)((H + kM - 1) / kM) * ((T + 255) / 256);
+    return launch<kDx, 256>(a, m, (int)std::min<long long>(tiles, num_sms()), st);
+}
+
+cudaError_t grad_w(const void *dg, const void *du, const void *x, long long ldx, int dtype, int T, int H, int F,
+                   void *dwg, void *dwu, int32_t *err, cudaStream_t st)
+{
+    Maps m;
+    cudaError_t e = rows_map(&m.a[0], x, 16, H, ldx, T, 64);
+    if (e == cudaSuccess) e = rows_map(&m.b[0][0], dg, 16, F, F, T, 64);
+    if (e == cudaSuccess) e = rows_map(&m.b[1][0], du, 16, F, F, T, 64);
+    if (e != cudaSuccess) return e;
+    Args a = {};
+    a.E = 2;
+    a.rows = F;
+    a.M = H;
+    a.ksteps = a.kphase = (T + 63) / 64;
+    a.split = 1;
+    a.out[0] = dwg;
+    a.out[1] = dwu;
+    a.ld = H;
+    a.dtype = dtype;
+    a.idesc = idesc16(dtype, true, true);
+    a.err = err;
+    const long long tiles = 2ll * ((H + kM - 1) / kM) * ((F + 255) / 256);
+    return launch<kDw, 256>(a, m, (int)std::min<long long>(tiles, num_sms()), st);
+}
+
+constexpr int kMaxGatedDim = 65536, kMaxGatedT = 1 << 24;
+
+bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
+
+int check_shape(int dtype, int T, int H, int F, long long ldx)
+{
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16)
+        return set_error(MOE_ERR_ARG, "dtype must be bf16 or fp16 (got %d)", dtype);
+    if (T < 0 || T > kMaxGatedT) return set_error(MOE_ERR_SHAPE, "T must be in [0, 2^24] (got %d)", T);
+    if (H < 8 || H > kMaxGatedDim || H % 8)
+        return set_error(MOE_ERR_SHAPE, "H must be a multiple of 8 in [8, %d] (got %d)", kMaxGatedDim, H);
+    if (F < 8 || F > kMaxGatedDim || F % 8)
+        return set_error(MOE_ERR_SHAPE, "F must be a multiple of 8 in [8, %d] (got %d)", kMaxGatedDim, F);
+    if (ldx < H) return set_error(MOE_ERR_SHAPE, "ldx must be at least H (got %lld)", ldx);
+    if (ldx % 8) return set_error(MOE_ERR_ALIGN, "rows of x are not 16-byte aligned (ldx %lld)", ldx);
+    return MOE_OK;
+}
+
+#define GATED_PTR(p)                                                                             \
+    do {                                                                                         \
+        if (!(p)) return set_error(MOE_ERR_ARG, "%s is NULL", #p);                               \
+        if (off((p), 16)) return set_error(MOE_ERR_ALIGN, "%s is not 16-byte aligned", #p);      \
+    } while (0)
+
+int check_workspace(void *ws, size_t bytes, size_t need)
+{
+    if (!ws) return set_error(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (off(ws, 256)) return set_error(MOE_ERR_ALIGN, "workspace is not 256-byte aligned");
+    if (bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace has %zu bytes; %zu needed", bytes, need);
+    return MOE_OK;
+}
+
+size_t grad_bytes(int T, int F) { return ((size_t)T * F * 2 + 255) / 256 * 256; }
+
+int done(cudaError_t e, const char *what)
+{
+    if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return set_error(MOE_OK, "%s", "");
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_gated_workspace_size(int T, int H, int F, int train)
+{
+    if (T < 0 || T > kMaxGatedT || H < 8 || H > kMaxGatedDim || H % 8 || F < 8 || F > kMaxGatedDim || F % 8) return 0;
+    return 256 + (train ? 2 * grad_bytes(T, F) : 0);
+}
+
+int moe_gated_forward(const void *x, long long ldx, const void *w_gate, const void *w_up, int dtype, int T, int H, int F,
+                      void *h, void *g, void *u, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if ((rc = check_shape(dtype, T, H, F, ldx))) return rc;
+    if (T == 0) return done(cudaSuccess, "");
+    GATED_PTR(x);
+    GATED_PTR(w_gate);
+    GATED_PTR(w_up);
+    GATED_PTR(h);
+    if (!g != !u) return set_error(MOE_ERR_ARG, "g and u go together");
+    if (off(g, 16) || off(u, 16)) return set_error(MOE_ERR_ALIGN, "g or u is not 16-byte aligned");
+    if ((rc = check_workspace(workspace, workspace_bytes, 256)) || (rc = require_device())) return rc;
+    return done(forward(x, ldx, w_gate, w_up, dtype, T, H, F, h, g, u, static_cast<int32_t *>(workspace),
+                        (cudaStream_t)stream),
+                "gated forward launch");
+}
+
+int moe_gated_backward(const void *dh, const void *x, long long ldx, const void *w_gate, const void *w_up, const void *g,
+                       const void *u, int dtype, int T, int H, int F, void *dx, void *dw_gate, void *dw_up,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if ((rc = check_shape(dtype, T, H, F, ldx))) return rc;
+    if (!dw_gate != !dw_up) return set_error(MOE_ERR_ARG, "dw_gate and dw_up go together");
+    if (off(dx, 16) || off(dw_gate, 16) || off(dw_up, 16)) return set_error(MOE_ERR_ALIGN, "a gradient is not 16-byte aligned");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {   // no rows: the weights' gradients are zero
+        if (!dw_gate) return done(cudaSuccess, "");
+        if ((rc = require_device())) return rc;
+        cudaError_t e = cudaMemsetAsync(dw_gate, 0, (size_t)F * H * 2, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dw_up, 0, (size_t)F * H * 2, st);
+        return done(e, "gated backward");
+    }
+    GATED_PTR(dh);
+    GATED_PTR(x);
+    GATED_PTR(w_gate);
+    GATED_PTR(w_up);
+    GATED_PTR(g);
+    GATED_PTR(u);
+    if ((rc = check_workspace(workspace, workspace_bytes, moe_gated_workspace_size(T, H, F, 1))) || (rc = require_device()))
+        return rc;
+    if (!dx && !dw_gate) return done(cudaSuccess, "");
+    int32_t *err = static_cast<int32_t *>(workspace);
+    char *dg = static_cast<char *>(workspace) + 256, *du = dg + grad_bytes(T, F);
+    const long long units = (long long)T * F / 8;
+    const dim3 grid((unsigned)((units + 255) / 256));
+    cudaError_t e =
+        dtype == MOE_DTYPE_BF16
+            ? launch_kernel(gated_grad_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, 1, (const __nv_bfloat16 *)dh,
+                            (const __nv_bfloat16 *)g, (const __nv_bfloat16 *)u, units, (__nv_bfloat16 *)dg, (__nv_bfloat16 *)du)
+            : launch_kernel(gated_grad_kernel<__half>, grid, dim3(256), 0, st, 1, (const __half *)dh, (const __half *)g,
+                            (const __half *)u, units, (__half *)dg, (__half *)du);
+    if (e == cudaSuccess && dx) e = grad_x(dg, du, w_gate, w_up, dtype, T, H, F, dx, err, st);
+    if (e == cudaSuccess && dw_gate) e = grad_w(dg, du, x, ldx, dtype, T, H, F, dw_gate, dw_up, err, st);
+    return done(e, "gated backward launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,674 @@
+// gemm_tc.cuh -- the tcgen05 matrix-product kernel behind the MXFP4 operators and the 16-bit
+// gated block.  One kernel template, five uses:
+//   kMxGate   h = q(silu(x Wg^T) * (x Wu^T)), x and W in MXFP4, h requantised to MXFP4
+//   kMxMul    y = x W^T, x and W in MXFP4
+//   kGate     h = silu(x Wg^T) * (x Wu^T) in 16 bits (g and u kept on request)
+//   kDx       dx = dg Wg + du Wu in 16 bits
+//   kDw       dWg = dg^T x, dWu = du^T x in 16 bits
+//
+// Orientation.  The accumulator's 128 lanes are the output's contiguous dimension (weight rows;
+// for dx and dW the model width) and its columns the other one (tokens; for dW the rows of the
+// weight).  A weight tile is then always a full 128-lane operand, however few tokens there
+// are, and a warp's lanes write consecutive output elements.  The MMA's column count follows the
+// tile's token count in steps of 16, so one token costs 16 columns.
+//
+// Work.  A tile is 128 lanes x up to BN columns over the whole reduction; groups (experts) are
+// cut into equal column chunks of at most BN.  CTAs run tiles blockIdx, blockIdx + grid, ...
+// With few tiles a cluster of S CTAs shares one: each takes a slice of the reduction, sends its
+// partial sums to the owner of each column through distributed shared memory, and the owner
+// adds them in rank order (the sums do not depend on timing).
+//
+// A reduction step (stage) is 128 bytes of each operand row: 64 16-bit or 256 4-bit inputs, in
+// 128-byte-swizzled tiles fed by TMA.  Rows and inputs past a tensor's end are read as zero.
+//
+// Warps: 0 feeds the stages by TMA; 1 issues the MMAs; 4-7 are the epilogue (TMEM lanes
+// 32 * (warp - 4) ..); 8-11 (MXFP4 only) bring the scales, one operand of 128 rows each: global
+// rows of scale bytes -> shared memory blocks of 512 bytes (row r, block k of 4 at
+// 16 * (r % 32) + 4 * (r / 32) + k) that tcgen05.cp copies to TMEM.
+//
+// Every wait is bounded: one that gives up sets the workspace's error word and ends the CTA's
+// loops; its copies in flight and MMAs are waited for and TMEM is freed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device_util.cuh"
+#include "launch.cuh"
+#include "moe_internal.cuh"
+#include "mx_util.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace gemm {
+
+enum Mode { kMxGate, kMxMul, kGate, kDx, kDw };
+
+constexpr int kM = 128;          // lanes of a tile
+constexpr int kBoxMaps = 5;      // column-operand maps with boxes of 16 << k rows
+constexpr int kMaxGroups = 512;
+
+constexpr bool is_mx(Mode m) { return m == kMxGate || m == kMxMul; }
+constexpr bool is_gated(Mode m) { return m == kMxGate || m == kGate; }
+constexpr bool a_mn(Mode m) { return m == kDx || m == kDw; }   // lanes operand stored reduction-major
+constexpr bool b_mn(Mode m) { return m == kDw; }
+
+// the kernel's parameters (tensor maps apart)
+struct Args {
+    const int32_t *offsets;    // [E + 1] rows of each group (null: every group is rows 0 .. rows)
+    int E;                     // groups
+    int rows;                  // columns of the output (tokens) in all
+    int M;                     // lanes dimension of one group
+    int ksteps;                // stages of the whole reduction
+    int kphase;                // kDx: stages of the first phase (gate); else == ksteps
+    int split;                 // CTAs that share a tile (the cluster size)
+    // scale bytes [rows][sf_ld] of the lanes operands (groups * M rows) and the columns operand
+    const uint8_t *sfa[2], *sfb;
+    int sf_ld;                 // K / 32
+    long long sfa_rows;        // E * M
+    void *out[3];              // y | (h, g, u) | (dWg, dWu) | (codes, scales)
+    int ld;                    // row stride of out, in elements (codes: of M)
+    int dtype;                 // MOE_DTYPE_* of out
+    uint32_t idesc;            // instruction descriptor without N and the scale ids
+    int32_t *err;
+};
+
+struct Maps {
+    CUtensorMap a[2];
+    CUtensorMap b[2][kBoxMaps];   // [0]: boxes 16 << k rows (reduction contiguous); kDw: [g][0], 64 x 64 boxes
+};
+
+template <Mode MODE, int BN>
+struct Cfg {
+    static constexpr bool MX = is_mx(MODE), GATED = is_gated(MODE);
+    static constexpr int NA = GATED ? 2 : 1;               // lanes operands (accumulators) of a tile
+    static constexpr int NBUF = NA * BN <= 192 ? 2 : 512 / (NA * BN) >= 2 && !MX ? 2 : 1;
+    static constexpr int A_BYTES = kM * 128;
+    static constexpr int B_BYTES = BN * 128;
+    static constexpr int SFB_UNITS = MX ? (BN + 127) / 128 : 0;
+    static constexpr int SF_UNITS = MX ? NA + SFB_UNITS : 0;   // 128-row scale blocks of a stage (2 x 512 B each)
+    static constexpr int SF_BYTES = SF_UNITS * 1024;
+    static constexpr bool SPLIT = BN <= 32;
+    static constexpr int RED_COLS = 40;                    // >= S * ceil(32 / S) for S <= 8
+    static constexpr int RED_BYTES = SPLIT ? NA * RED_COLS * kM * 4 : 0;
+    static constexpr int CTRL_BYTES = 8192;                // control block and the groups' prefix
+    static constexpr int STAGE = NA * A_BYTES + B_BYTES + SF_BYTES;
+    static constexpr int BUDGET = 232448 - 1024 - CTRL_BYTES - RED_BYTES;
+    static constexpr int STAGES = BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + CTRL_BYTES;
+    static constexpr int THREADS = MX ? 384 : 256;
+    static constexpr int SF_COL = 448;                     // first TMEM column of the scales: 2 buffers
+    static constexpr int SF_BUF = 32;                      // columns of one buffer
+    static_assert(STAGES >= 3, "shared memory budget");
+    static_assert(NBUF * NA * BN <= (MX ? SF_COL : 512), "TMEM budget");
+};
+
+struct Ctrl {
+    uint64_t full[8], empty[8], dfull[2], dempty[2], rfull, rempty, fin;
+    uint32_t tmem;
+    int abort;
+    int tiles;
+    int32_t prefix[kMaxGroups + 1], off[kMaxGroups + 1];
+};
+
+__device__ __forceinline__ bool stopped(const Ctrl *c) { return *(volatile const int *)&c->abort != 0; }
+
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
+{
+    bool ok = mbar_wait(bar, parity);
+    if (!ok) {
+        atomicOr(err, kErrTimeout);
+        atomicExch(&c->abort, 1);
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// the same on a barrier that other CTAs of the cluster arrive at (their writes become visible)
+__device__ __forceinline__ bool wait_warp_cluster(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
+{
+    uint32_t ok = 0;
+    for (int n = 0; n < kWaitLimit && !ok; ++n)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    if (!ok) {
+        atomicOr(err, kErrTimeout);
+        atomicExch(&c->abort, 1);
+    }
+    return __all_sync(0xffffffffu, ok != 0);
+}
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+        : "memory");
+}
+
+// descriptor of an operand tile stored reduction-major (64 lanes or columns of 128 bytes per
+// reduction index, 128-byte swizzle): 64-wide chunks 8192 bytes apart, 8 reduction indices 1024
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(8192u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// descriptor of a 512-byte scale block: 32 rows of 16 bytes, no swizzle, 8-row groups 128 apart
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(128u >> 4) << 32 |
+           (uint64_t)1 << 46;
+}
+
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc)
+        : "memory");
+}
+
+// --- cluster ----------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, int rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// --- tiles ------------------------------------------------------------------------------
+struct Tile {
+    int e, m0, row0, n, np;
+};
+
+// columns of a group of c rows in nt chunks of equal size (a multiple of 16)
+__device__ __forceinline__ int chunk_cols(int c, int nt) { return ((c + nt - 1) / nt + 15) & ~15; }
+
+template <int BN>
+__device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
+{
+    int lo = 0, hi = a.E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c->prefix[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int first = a.offsets ? c->off[lo] : 0;
+    const int rows = a.offsets ? c->off[lo + 1] - first : a.rows;
+    const int nt = (rows + BN - 1) / BN;
+    const int w = chunk_cols(rows, nt);
+    const int local = t - c->prefix[lo];
+    const int mi = local / nt, ni = local - mi * nt;   // a weight tile's chunks run next to one another
+    Tile r;
+    r.e = lo;
+    r.m0 = mi * kM;
+    r.row0 = first + ni * w;
+    r.n = max(0, min(w, rows - ni * w));
+    r.np = max(16, (r.n + 15) & ~15);
+    return r;
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+__device__ __forceinline__ void store(void *p, int dtype, size_t i, float v)
+{
+    if (dtype == MOE_DTYPE_F32) reinterpret_cast<float *>(p)[i] = v;
+    else if (dtype == MOE_DTYPE_BF16) reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else reinterpret_cast<__half *>(p)[i] = __float2half_rn(v);
+}
+
+// 8 columns of h of this lane's row -> MXFP4.  A block is the warp's 32 rows of one column.
+// col(j) gives column j's output row, or -1.
+template <class Col>
+__device__ __forceinline__ void emit_mx8(const Args &a, const float (&v)[8], int m, int lane, Col col)
+{
+    uint32_t w = 0, mine = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        float s[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t bits = __float_as_uint(v[j + k]) & 0x7fffffffu;
+            float f;
+            const uint32_t sb = mx_scale(__reduce_max_sync(0xffffffffu, bits), f);
+            s[k] = f == 0.0f ? 0.0f : v[j + k] * f;
+            if ((lane & 7) == j + k) mine = sb;
+        }
+        w |= e2m1x2(s[0], s[1]) << (4 * j);
+    }
+    // lane 8a + i holds column j's nibble of row 8a + i at nibble j: transpose within 8 lanes,
+    // so that lane 8a + j holds rows 8a .. 8a + 7 of column j
+#pragma unroll
+    for (int d = 4; d; d >>= 1) {
+        const uint32_t mask = d == 4 ? 0x0000ffffu : d == 2 ? 0x00ff00ffu : 0x0f0f0f0fu;
+        const bool up = lane & d;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? (w & mask) : ((w >> (4 * d)) & mask), d);
+        w = up ? ((w & ~mask) | got) : ((w & mask) | (got << (4 * d)));
+    }
+    const int r = col(lane & 7);
+    if (r >= 0 && m < a.M) {
+        const size_t at = (size_t)r * a.ld + (m & ~7);   // first of the 8 rows that this word holds
+        *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.out[0]) + (at >> 1)) = w;
+        if (lane < 8) static_cast<uint8_t *>(a.out[1])[(size_t)r * (a.ld >> 5) + (m >> 5)] = (uint8_t)mine;
+    }
+}
+
+// NC columns of a tile (acc[0..NA-1][j]) -> the outputs; col(j): column j's output row, or -1
+template <Mode MODE, int NC, class Col>
+__device__ __forceinline__ void emit(const Args &a, const float (&g)[NC], const float (&u)[NC], int e, int m, int lane,
+                                     Col col)
+{
+    if constexpr (MODE == kMxGate) {
+#pragma unroll
+        for (int j0 = 0; j0 < NC; j0 += 8) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = silu(g[j0 + j]) * u[j0 + j];
+            emit_mx8(a, v, m, lane, [&](int j) { return col(j0 + j); });
+        }
+    } else {
+        if (m >= a.M) return;
+        void *out = MODE == kDw ? a.out[e] : a.out[0];
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int r = col(j);
+            if (r < 0) continue;
+            const size_t at = (size_t)r * a.ld + m;
+            if constexpr (MODE == kGate) {
+                store(out, a.dtype, at, silu(g[j]) * u[j]);
+                if (a.out[1]) {
+                    store(a.out[1], a.dtype, at, g[j]);
+                    store(a.out[2], a.dtype, at, u[j]);
+                }
+            } else {
+                store(out, a.dtype, at, g[j]);
+            }
+        }
+    }
+}
+
+// 16 scale bytes (blocks 16 kc .. 16 kc + 15) of a row of K / 32; past the end: 0 (2^-127, on
+// codes that are zero there)
+__device__ __forceinline__ uint4 load_scales(const uint8_t *base, long long row, long long rows, int ld, int kc)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row >= rows) return v;
+    const uint8_t *p = base + row * ld + 16 * kc;
+    if ((ld & 15) == 0) return __ldg(reinterpret_cast<const uint4 *>(p));
+    const int left = min(16, ld - 16 * kc);
+    uint32_t w[4] = {0, 0, 0, 0};
+    if ((ld & 3) == 0) {   // K a multiple of 128: whole words
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * i < left) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < left) w[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <Mode MODE, int BN>
+__global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
+    gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
+{
+    using C = Cfg<MODE, BN>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    pdl_wait();
+    pdl_launch_dependents();
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sfring = ring + C::STAGES * (C::NA * C::A_BYTES + C::B_BYTES);
+    float *red = reinterpret_cast<float *>(sfring + C::STAGES * C::SF_BYTES);
+    Ctrl *c = reinterpret_cast<Ctrl *>(reinterpret_cast<uint8_t *>(red) + C::RED_BYTES);
+    static_assert(sizeof(Ctrl) <= C::CTRL_BYTES, "control block");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int mtiles = (a.M + kM - 1) / kM;
+    const int S = C::SPLIT ? a.split : 1;
+    const int rank = C::SPLIT ? (int)(blockIdx.x % S) : 0;
+    const int tile0 = C::SPLIT ? (int)(blockIdx.x / S) : (int)blockIdx.x;
+    const int tstep = C::SPLIT ? (int)(gridDim.x / S) : (int)gridDim.x;
+    const int ks0 = (int)((long long)a.ksteps * rank / S), ks1 = (int)((long long)a.ksteps * (rank + 1) / S);
+
+    if (a.offsets)
+        for (int e = tid; e <= a.E; e += C::THREADS) c->off[e] = a.offsets[e];
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&c->full[i], 1 + C::SF_UNITS);
+            mbar_init(&c->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->dfull[i], 1);
+            mbar_init(&c->dempty[i], 4);
+        }
+        mbar_init(&c->rfull, 4 * S);
+        mbar_init(&c->rempty, 4 * S);
+        mbar_init(&c->fin, 1);
+        c->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&c->tmem, 512);
+        tc::tmem_relinquish();
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // tiles before each group; a group whose offsets do not lie in order within the rows is
+        // recorded and left out
+        int carry = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < a.E) {
+                int rows = a.rows;
+                if (a.offsets) {
+                    const int lo = c->off[e], hi = c->off[e + 1];
+                    rows = hi - lo;
+                    if (lo < 0 || hi > a.rows || hi < lo) {
+                        atomicOr(a.err, kErrBadOffsets);
+                        rows = 0;
+                    }
+                }
+                n = mtiles * ((rows + BN - 1) / BN);
+            }
+            int s = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, s, d);
+                if (lane >= d) s += o;
+            }
+            if (e < a.E) c->prefix[e] = carry + s - n;
+            carry += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) {
+            c->prefix[a.E] = carry;
+            c->tiles = carry;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (C::SPLIT && S > 1) cluster_sync();   // every rank's barriers are ready
+    const uint32_t tmem = c->tmem;
+    const int total = c->tiles;
+
+    if (warp == 0) {
+        // ---------------- operands by TMA ---------------------------------------------------
+        const uint32_t r0 = smem_u32(ring);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
+            const Tile q = get_tile<BN>(a, c, t);
+            const int boxes = (q.np + 63) >> 6;
+            const uint32_t bytes = C::NA * C::A_BYTES + (b_mn(MODE) ? boxes * 8192u : (uint32_t)q.np * 128u);
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                const uint32_t s = it % C::STAGES;
+                if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
+                const uint32_t bar = smem_u32(&c->full[s]);
+                const uint32_t as = r0 + s * (C::NA * C::A_BYTES + C::B_BYTES), bs = as + C::NA * C::A_BYTES;
+                expect_tx(bar, bytes);
+                const int ph = MODE == kDx && ks >= a.kphase;
+                const int kk = MODE == kDx && ph ? ks - a.kphase : ks;
+                if constexpr (a_mn(MODE)) {
+                    tma_2d(as, &maps.a[ph], q.m0, kk * 64, bar);
+                    tma_2d(as + 8192, &maps.a[ph], q.m0 + 64, kk * 64, bar);
+                } else {
+#pragma unroll
+                    for (int o = 0; o < C::NA; ++o)
+                        tma_2d(as + o * C::A_BYTES, &maps.a[o], kk * (C::MX ? 128 : 64), q.e * a.M + q.m0, bar);
+                }
+                if constexpr (b_mn(MODE)) {
+                    for (int i = 0; i < boxes; ++i) tma_2d(bs + i * 8192, &maps.b[q.e][0], q.row0 + 64 * i, kk * 64, bar);
+                } else {
+                    int r = 0;
+#pragma unroll
+                    for (int k = kBoxMaps - 1; k >= 0; --k)
+                        if (q.np - r >= (16 << k)) {
+                            tma_2d(bs + r * 128, &maps.b[ph][k], kk * (C::MX ? 128 : 64), q.row0 + r, bar);
+                            r += 16 << k;
+                        }
+                }
+            }
+        }
+        // copies still in flight (after a wait that gave up) land before the CTA ends
+        for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+            mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issue ---------------------------------------------------------
+        const uint32_t r0 = smem_u32(ring), sf0 = smem_u32(sfring);
+        uint32_t it = 0, nt = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
+            const Tile q = get_tile<BN>(a, c, t);
+            const uint32_t idesc = a.idesc | (uint32_t)(q.np >> 3) << 17;
+            const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
+            const uint32_t d0 = tmem + buf * (C::NA * BN);
+            if (use >= 1 && !(ok = wait_warp(&c->dempty[buf], (use - 1) & 1, c, a.err))) break;
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                const uint32_t s = it % C::STAGES;
+                if (!(ok = wait_warp(&c->full[s], (it / C::STAGES) & 1, c, a.err))) break;
+                const uint32_t as = r0 + s * (C::NA * C::A_BYTES + C::B_BYTES), bs = as + C::NA * C::A_BYTES;
+                uint32_t sfc = 0;
+                if constexpr (C::MX) {
+                    // the scales' TMEM buffer was last read by the MMAs of two stages ago
+                    if (it >= 2 && !(ok = wait_warp(&c->empty[(it - 2) % C::STAGES], ((it - 2) / C::STAGES) & 1, c, a.err)))
+                        break;
+                    tc::fence_after_sync();
+                    sfc = tmem + C::SF_COL + (it & 1) * C::SF_BUF;
+                    const uint64_t sd = sdesc_scales(sf0 + s * C::SF_BYTES);
+                    // columns: [block of 128 inputs][lanes operand 0, 1: 4 each, columns: 8]
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int u = 0; u < C::SF_UNITS; ++u)
+                            cp_scales(sfc + b * 16 + (u < C::NA ? u * 4 : 8 + (u - C::NA) * 4), sd + (uint64_t)((u * 1024 + b * 512) >> 4));
+                    }
+                } else {
+                    tc::fence_after_sync();
+                }
+                const uint64_t bd = b_mn(MODE) ? sdesc_mn_sw128(bs) : tc::sdesc_kmajor_sw128(bs);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int o = 0; o < C::NA; ++o) {
+                        const uint64_t ad = a_mn(MODE) ? sdesc_mn_sw128(as) : tc::sdesc_kmajor_sw128(as + o * C::A_BYTES);
+                        const uint64_t ka = ad + (a_mn(MODE) ? k * 128 : k * 2), kb = bd + (b_mn(MODE) ? k * 128 : k * 2);
+                        if constexpr (C::MX) {
+                            const uint32_t id = idesc | (uint32_t)((k & 1) * 2) << 29 | (uint32_t)((k & 1) * 2) << 4;
+                            mma_mx4(d0 + o * BN, ka, kb, id, sfc + (k >> 1) * 16 + o * 4, sfc + (k >> 1) * 16 + 8, ks > ks0 || k > 0);
+                        } else {
+                            mma_f16(d0 + o * BN, ka, kb, idesc, ks > ks0 || k > 0);
+                        }
+                    }
+                }
+                tc::commit_elect(&c->empty[s]);
+            }
+            tc::commit_elect(&c->dfull[buf]);
+        }
+        tc::commit_elect(&c->fin);   // every MMA issued here is done before TMEM is freed
+        wait_warp(&c->fin, 0, c, a.err);
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------- epilogue ----------------------------------------------------------
+        const int qd = warp - 4;
+        const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
+        uint32_t nt = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
+            const Tile q = get_tile<BN>(a, c, t);
+            const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
+            const int m = q.m0 + qd * 32 + lane;
+            if (!(ok = wait_warp(&c->dfull[buf], use & 1, c, a.err))) break;
+            tc::fence_after_sync();
+            if (C::SPLIT && S > 1) {
+                // send the partial sums to their columns' owners (column k to rank k % S), then
+                // add up the own columns in rank order
+                if (nt >= 1 && !(ok = wait_warp_cluster(&c->rempty, (nt - 1) & 1, c, a.err))) break;
+                const uint32_t rb = smem_u32(red);
+#pragma unroll
+                for (int o = 0; o < C::NA; ++o)
+                    for (int c0 = 0; c0 < q.np; c0 += 16) {
+                        uint32_t v[16];
+                        tc::ld16(tl + buf * (C::NA * BN) + o * BN + c0, v);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int k = c0 + j;
+                            if (k < q.n)
+                                st_cluster(map_rank(rb + (uint32_t)(((o * C::RED_COLS + rank * ((BN + S - 1) / S) + k / S) * kM + qd * 32 + lane) * 4), k % S),
+                                           __uint_as_float(v[j]));
+                        }
+                    }
+                tc::fence_before_sync();
+                fence_cluster();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->dempty[buf]);
+                if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rfull), lane));
+                if (!(ok = wait_warp_cluster(&c->rfull, nt & 1, c, a.err))) break;
+                const int per = (BN + S - 1) / S;
+                for (int i0 = 0; i0 * S + rank < q.n; i0 += 8) {
+                    float v[2][8];
+#pragma unroll
+                    for (int o = 0; o < C::NA; ++o)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float x = 0.0f;
+                            if ((i0 + j) * S + rank < q.n)
+                                for (int r = 0; r < S; ++r) x += red[(o * C::RED_COLS + r * per + i0 + j) * kM + qd * 32 + lane];
+                            v[o][j] = x;
+                        }
+                    emit<MODE, 8>(a, v[0], v[C::NA - 1], q.e, m, lane, [&](int j) {
+                        const int k = (i0 + j) * S + rank;
+                        return k < q.n ? q.row0 + k : -1;
+                    });
+                }
+                fence_cluster();
+                __syncwarp();
+                if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rempty), lane));
+            } else {
+                for (int c0 = 0; c0 < q.np; c0 += 16) {
+                    uint32_t v[2][16];
+#pragma unroll
+                    for (int o = 0; o < C::NA; ++o) tc::ld16(tl + buf * (C::NA * BN) + o * BN + c0, v[o]);
+                    tc::wait_ld();
+                    if (c0 + 16 >= q.np) {   // the accumulator is in registers
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c->dempty[buf]);
+                    }
+                    float f[2][16];
+#pragma unroll
+                    for (int o = 0; o < C::NA; ++o)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[o][j] = __uint_as_float(v[o][j]);
+                    emit<MODE, 16>(a, f[0], f[C::NA - 1], q.e, m, lane,
+                                   [&](int j) { return c0 + j < q.n ? q.row0 + c0 + j : -1; });
+                }
+            }
+        }
+    } else if (C::MX && warp >= 8 && warp - 8 < C::SF_UNITS) {
+        // ---------------- scales: this warp's operand, 128 rows -----------------------------
+        const int u = warp - 8;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
+            const Tile q = get_tile<BN>(a, c, t);
+            const uint8_t *base = u < C::NA ? a.sfa[u] : a.sfb;
+            const long long row0 = u < C::NA ? (long long)q.e * a.M + q.m0 : (long long)q.row0 + (u - C::NA) * 128;
+            const long long rows = u < C::NA ? a.sfa_rows : a.rows;
+            // chunks of 512 inputs (16 scale bytes of a row), one chunk ahead in registers
+            uint4 cur[4], nxt[4];
+            int kc = ks0 >> 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nxt[i] = load_scales(base, row0 + lane + 32 * i, rows, a.sf_ld, kc);
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                if (ks == ks0 || (ks & 1) == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                    ++kc;
+                    if (2 * kc < ks1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) nxt[i] = load_scales(base, row0 + lane + 32 * i, rows, a.sf_ld, kc);
+                    }
+                }
+                const uint32_t s = it % C::STAGES;
+                if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
+                uint4 *dst = reinterpret_cast<uint4 *>(sfring + s * C::SF_BYTES + u * 1024) + lane;
+                const bool odd = ks & 1;
+                dst[0] = make_uint4(odd ? cur[0].z : cur[0].x, odd ? cur[1].z : cur[1].x, odd ? cur[2].z : cur[2].x, odd ? cur[3].z : cur[3].x);
+                dst[32] = make_uint4(odd ? cur[0].w : cur[0].y, odd ? cur[1].w : cur[1].y, odd ? cur[2].w : cur[2].y, odd ? cur[3].w : cur[3].y);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->full[s]);
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+    if (C::SPLIT && S > 1) cluster_sync();   // no rank leaves while another may still write to it
+}
+
+template <Mode MODE, int BN>
+cudaError_t launch(const Args &a, const Maps &m, int grid, cudaStream_t st)
+{
+    using C = Cfg<MODE, BN>;
+    return launch_kernel(gemm_kernel<MODE, BN>, dim3(grid), dim3(C::THREADS), C::SMEM, st, a.split, a, m);
+}
+
+}  // namespace gemm
+}  // namespace moe

@@ -311,6 +311,12 @@ int set_error(int code, const char *fmt, ...)
 
 int require_device() { return check_device(); }
 
+int validate_config(const moe_config *cfg, int T)
+{
+    const int rc = check_config(cfg);
+    return rc ? rc : check_tokens(T);
+}
+
 cudaError_t ensure_dynamic_smem(const void *kernel, size_t bytes)
 {
     static std::mutex mu;
@@ -684,6 +690,8 @@ int moe_check_errors(void *workspace, size_t workspace_bytes, void *stream)
     if (flag & kErrBadExpertId) return fail(MOE_ERR_DEVICE, "an expert id outside [0, n_experts) was skipped");
     if (flag & kErrBadKeff) return fail(MOE_ERR_DEVICE, "a keff outside [0, top_k] was clamped");
     if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a bounded device-side wait gave up; the kernel stopped early and its outputs are incomplete");
+    if (flag & kErrBadOffsets) return fail(MOE_ERR_DEVICE, "a group whose offsets are out of order or past the rows was skipped");
+    if (flag & kErrBadToken) return fail(MOE_ERR_DEVICE, "a token index outside [0, T) was skipped");
     if (flag) return fail(MOE_ERR_DEVICE, "device error word 0x%x", flag);
     return ok();
 }

@@ -34,6 +34,8 @@ constexpr size_t kRouteScratchFloats = size_t(2) << 20;
 constexpr int kErrBadExpertId = 1;
 constexpr int kErrBadKeff = 2;
 constexpr int kErrTimeout = 4;     // a bounded device-side wait gave up
+constexpr int kErrBadOffsets = 8;  // a group's offsets are out of order or past the rows
+constexpr int kErrBadToken = 16;   // a token index outside [0, T)
 
 // ---------------------------------------------------------------------------
 // Work plan of the grouped expert FFN.  A "slot" is one expert applied to its
@@ -204,12 +206,30 @@ cudaError_t launch_quantize_int4(const float *w, int rows, int K, uint8_t *packe
 cudaError_t launch_quantize_int3(const float *w, int rows, int K, uint8_t *packed, float *scales,
                                  cudaStream_t st);
 
+// MXFP4 rows (mxfp4.cu).  launch_quantize_mxfp4: with `tok`, row r is x's row tok[r] (of T) for
+// r < *limit (rows after it are left alone, an index outside [0, T) is recorded in err)
+cudaError_t launch_quantize_mxfp4(const void *x, int dtype, long long ldx, long long rows, int K, const int32_t *tok,
+                                  const int32_t *limit, int T, uint8_t *codes, uint8_t *scales, int32_t *err,
+                                  cudaStream_t st);
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K, void *y,
+                                    int dtype, cudaStream_t st);
+
+// MXFP4 products (mxfp4_gemm.cu): y [rows][N] = x W^T over `E` groups of rows, and
+// codes/scales [rows][F] = q(silu(x Wg^T) * (x Wu^T))
+cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *w, const uint8_t *ws,
+                                int E, const int32_t *offsets, int N, int K, void *y, int dtype, int32_t *err,
+                                cudaStream_t st);
+cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *wg, const uint8_t *sg,
+                                 const uint8_t *wu, const uint8_t *su, int E, const int32_t *offsets, int F, int K,
+                                 uint8_t *codes, uint8_t *scales, int32_t *err, cudaStream_t st);
+
 // diagnostic: one bounded wait on an mbarrier nothing arrives at (selftest.cu)
 cudaError_t launch_selftest_wait(int32_t *err, int polls, cudaStream_t st);
 
 // host helpers shared with the entry points outside moe_api.cu
 int set_error(int code, const char *fmt, ...);   // records the thread's last error message
 int require_device();                            // MOE_OK on a compute capability 10.3 device
+int validate_config(const moe_config *cfg, int T);
 int validate_route_args(const moe_config *cfg, const float *x, const float *w_router,
                         const float *bias, int T, const int32_t *ids, const float *w,
                         const int32_t *keff);

@@ -1,0 +1,94 @@
+// mxfp4_gemm.cu -- launches of the MXFP4 products (kernel: gemm_tc.cuh) and their entry points.
+#include <algorithm>
+
+#include "gemm_tc.cuh"
+#include "tensor_map.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace gemm;
+
+// e2m1 x e2m1 with ue8m0 scales, fp32 sums, both operands reduction-major, 128 lanes
+constexpr uint32_t kIdescMx = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(kM >> 4) << 24);
+
+cudaError_t code_maps(Maps &m, const uint8_t *a0, const uint8_t *a1, long long arows, const uint8_t *b, int rows, int K)
+{
+    cudaError_t e = rows_map(&m.a[0], a0, 8, K / 2, K / 2, arows, kM);
+    if (e == cudaSuccess && a1) e = rows_map(&m.a[1], a1, 8, K / 2, K / 2, arows, kM);
+    for (int k = 0; k < kBoxMaps && e == cudaSuccess; ++k) e = rows_map(&m.b[0][k], b, 8, K / 2, K / 2, rows, 16 << k);
+    return e;
+}
+
+template <Mode MODE>
+cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
+{
+    const int sms = num_sms();
+    const int mtiles = (a.M + kM - 1) / kM, used = std::min(a.E, a.rows);
+    if (a.rows <= 24 * used) {
+        // few rows a group: 32 columns, and a cluster a tile while tiles are fewer than SMs
+        const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + 31) / 32 + used);
+        a.split = (int)std::max<long long>(1, std::min<long long>({8, sms / std::max<long long>(1, (long long)mtiles * used), a.ksteps}));
+        const long long clusters = std::min<long long>(tiles, sms / a.split);
+        return launch<MODE, 32>(a, m, (int)clusters * a.split, st);
+    }
+    const long long tiles = (long long)mtiles * ((a.rows + 191) / 192 + used);
+    a.split = 1;
+    return launch<MODE, 192>(a, m, (int)std::min<long long>(tiles, sms), st);
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *w, const uint8_t *ws,
+                                int E, const int32_t *offsets, int N, int K, void *y, int dtype, int32_t *err,
+                                cudaStream_t st)
+{
+    Maps m;
+    const cudaError_t e = code_maps(m, w, nullptr, (long long)E * N, x, rows, K);
+    if (e != cudaSuccess) return e;
+    Args a = {};
+    a.offsets = offsets;
+    a.E = E;
+    a.rows = rows;
+    a.M = N;
+    a.ksteps = a.kphase = (K + 255) / 256;
+    a.sfa[0] = ws;
+    a.sfb = xs;
+    a.sf_ld = K / 32;
+    a.sfa_rows = (long long)E * N;
+    a.out[0] = y;
+    a.ld = N;
+    a.dtype = dtype;
+    a.idesc = kIdescMx;
+    a.err = err;
+    return run<kMxMul>(a, m, st);
+}
+
+cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *wg, const uint8_t *sg,
+                                 const uint8_t *wu, const uint8_t *su, int E, const int32_t *offsets, int F, int K,
+                                 uint8_t *codes, uint8_t *scales, int32_t *err, cudaStream_t st)
+{
+    Maps m;
+    const cudaError_t e = code_maps(m, wg, wu, (long long)E * F, x, rows, K);
+    if (e != cudaSuccess) return e;
+    Args a = {};
+    a.offsets = offsets;
+    a.E = E;
+    a.rows = rows;
+    a.M = F;
+    a.ksteps = a.kphase = (K + 255) / 256;
+    a.sfa[0] = sg;
+    a.sfa[1] = su;
+    a.sfb = xs;
+    a.sf_ld = K / 32;
+    a.sfa_rows = (long long)E * F;
+    a.out[0] = codes;
+    a.out[1] = scales;
+    a.ld = F;
+    a.idesc = kIdescMx;
+    a.err = err;
+    return run<kMxGate>(a, m, st);
+}
+
+}  // namespace moe
