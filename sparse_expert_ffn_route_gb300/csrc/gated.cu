@@ -110,7 +110,7 @@ cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu
     const int sms = num_sms(), mtiles = (F + kM - 1) / kM;
     if (T <= 32) {
         // one column chunk: a cluster a tile while tiles are fewer than SMs
-        a.split = std::max(1, std::min({8, sms / mtiles, a.ksteps}));
+        a.split = choose_split<kGate, 32>(mtiles, a.ksteps);
         return launch<kGate, 32>(a, m, std::min(mtiles, sms / a.split) * a.split, st);
     }
     a.split = 1;

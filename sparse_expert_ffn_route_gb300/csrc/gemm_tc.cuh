@@ -34,6 +34,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "device_util.cuh"
 #include "launch.cuh"
 #include "moe_internal.cuh"
@@ -661,6 +663,51 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
         tc::tmem_dealloc(tmem, 512);
     }
     if (C::SPLIT && S > 1) cluster_sync();   // no rank leaves while another may still write to it
+}
+
+// Clusters of `size` CTAs of this kernel that the current device holds at once (0 if unknown); a
+// cluster lies within one of the device's processor groups, so this is less than SMs / size
+// (measured on GB300: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
+template <Mode MODE, int BN>
+int max_clusters(int size)
+{
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][size].load();
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size * num_sms());
+        cfg.blockDim = dim3(Cfg<MODE, BN>::THREADS);
+        cfg.dynamicSmemBytes = Cfg<MODE, BN>::SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)size;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        const void *k = reinterpret_cast<const void *>(gemm_kernel<MODE, BN>);
+        if (ensure_dynamic_smem(k, Cfg<MODE, BN>::SMEM) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        known[dev][size].store(n);
+    }
+    return n;
+}
+
+// CTAs that share a tile when `tiles` of them would leave SMs idle: the largest cluster of
+// which the device holds as many as there are tiles (a second wave would cost more than the
+// finer split gains)
+template <Mode MODE, int BN>
+int choose_split(long long tiles, int ksteps)
+{
+    int best = 1;
+    if (Cfg<MODE, BN>::SPLIT)
+        for (int s = 2; s <= 8 && s <= ksteps && s * tiles <= num_sms(); ++s)
+            if (max_clusters<MODE, BN>(s) >= tiles) best = s;
+    return best;
 }
 
 template <Mode MODE, int BN>

@@ -11,6 +11,8 @@
 // Bound by memory.  A warp takes 1024 consecutive values of a row, 8 a lane in each of 4 steps:
 // one or two 16-byte loads a step, all issued before the first use; the 4 lanes of a block
 // meet in two shuffles; a step's codes go out as 128 consecutive bytes.
+#include <type_traits>
+
 #include "device_util.cuh"
 #include "launch.cuh"
 #include "moe_internal.cuh"
@@ -22,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSteps = 4;              // 256 values a warp and step
+constexpr int kDeqSteps = 4;           // units a lane writes in the dequantiser
 constexpr int kSeg = 256 * kSteps;     // values of a row that a warp takes
 
 template <typename T>
@@ -130,18 +133,15 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void put8(T *p, const float (&v)[8]);
-
-template <>
-__device__ __forceinline__ void put8<float>(float *p, const float (&v)[8])
+// A lane writes 16 consecutive bytes a step, so that a warp's stores are 512 consecutive bytes:
+// 4 values in fp32 (8, as two stores 32 bytes apart over the warp, wrote 403 MB at 4.9 TB/s; this
+// way at DEQ32 TB/s), 8 in 16 bits.
+__device__ __forceinline__ void put(float *p, const float (&v)[4])
 {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-template <>
-__device__ __forceinline__ void put8<__nv_bfloat16>(__nv_bfloat16 *p, const float (&v)[8])
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[8])
 {
     __nv_bfloat162 o[4];
 #pragma unroll
@@ -149,8 +149,7 @@ __device__ __forceinline__ void put8<__nv_bfloat16>(__nv_bfloat16 *p, const floa
     *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(o);
 }
 
-template <>
-__device__ __forceinline__ void put8<__half>(__half *p, const float (&v)[8])
+__device__ __forceinline__ void put(__half *p, const float (&v)[8])
 {
     __half2 o[4];
 #pragma unroll
@@ -163,30 +162,32 @@ __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, long long units,
                       T *__restrict__ y)
 {
+    constexpr int V = 16 / sizeof(T);   // values of a unit: 16 bytes of y, 2 or 4 bytes of codes
+    using Codes = typename std::conditional<V == 4, uint16_t, uint32_t>::type;
     pdl_wait();
     pdl_launch_dependents();
-    // unit u: values 8u .. 8u + 7 of the rows laid end to end (K is a multiple of 32)
+    // unit u: values V u .. of the rows laid end to end (K is a multiple of 32)
     const int lane = threadIdx.x & 31;
-    const long long u0 = (((long long)blockIdx.x * kThreads + threadIdx.x) >> 5) * (32 * kSteps) + lane;
-    uint32_t w[kSteps], sb[kSteps];
+    const long long u0 = (((long long)blockIdx.x * kThreads + threadIdx.x) >> 5) * (32 * kDeqSteps) + lane;
+    uint32_t w[kDeqSteps], sb[kDeqSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < kDeqSteps; ++i)
         if (u0 + 32 * i < units) {
-            w[i] = __ldg(reinterpret_cast<const uint32_t *>(codes) + u0 + 32 * i);
-            sb[i] = __ldg(scales + ((u0 + 32 * i) >> 2));
+            w[i] = __ldg(reinterpret_cast<const Codes *>(codes) + u0 + 32 * i);
+            sb[i] = __ldg(scales + (u0 + 32 * i) / (32 / V));
         }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < kDeqSteps; ++i) {
         if (u0 + 32 * i >= units) return;
         const float s = mx_scale_value(sb[i]);
-        float v[8];
+        float v[V];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < V / 2; ++j) {
             const float2 p = e2m1x2_values(w[i] >> (8 * j));
             v[2 * j] = p.x * s;
             v[2 * j + 1] = p.y * s;
         }
-        put8(y + (u0 + 32 * i) * 8, v);
+        put(y + (u0 + 32 * i) * V, v);
     }
 }
 
@@ -217,8 +218,8 @@ cudaError_t launch_quantize_mxfp4(const void *x, int dtype, long long ldx, long 
 cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K, void *y,
                                     int dtype, cudaStream_t st)
 {
-    const long long units = rows * K / 8;
-    const dim3 grid((unsigned)((units + kThreads * kSteps - 1) / (kThreads * kSteps)));
+    const long long units = rows * K / (dtype == MOE_DTYPE_F32 ? 4 : 8);
+    const dim3 grid((unsigned)((units + kThreads * kDeqSteps - 1) / (kThreads * kDeqSteps)));
     if (dtype == MOE_DTYPE_F32)
         return launch_kernel(dequantize_kernel<float>, grid, dim3(kThreads), 0, st, 1, codes, scales, units, (float *)y);
     if (dtype == MOE_DTYPE_BF16)

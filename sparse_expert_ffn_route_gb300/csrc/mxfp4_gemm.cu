@@ -29,7 +29,7 @@ cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
     if (a.rows <= 24 * used) {
         // few rows a group: 32 columns, and a cluster a tile while tiles are fewer than SMs
         const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + 31) / 32 + used);
-        a.split = (int)std::max<long long>(1, std::min<long long>({8, sms / std::max<long long>(1, (long long)mtiles * used), a.ksteps}));
+        a.split = choose_split<MODE, 32>((long long)mtiles * used, a.ksteps);
         const long long clusters = std::min<long long>(tiles, sms / a.split);
         return launch<MODE, 32>(a, m, (int)clusters * a.split, st);
     }
