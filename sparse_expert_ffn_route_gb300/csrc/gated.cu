@@ -1,5 +1,5 @@
 // gated.cu -- the dense gated block in 16 bits, h = silu(x Wg^T) * (x Wu^T), and its gradients:
-// launches of the products (kernel: gemm_tc.cuh), the elementwise pass between them, and the
+// launches of the products (kernels: gemm16.cuh, for few tokens gemm_tc.cuh), the elementwise pass between them, and the
 // entry points.
 //
 // With s = sigmoid(g):  dg = dh u s (1 + g (1 - s)),  du = dh g s,
@@ -11,20 +11,18 @@
 // fp32.
 #include <algorithm>
 
-#include "gemm_tc.cuh"
+#include "gemm16.cuh"
 #include "tensor_map.cuh"
 
 namespace moe {
 
 namespace {
 
-using namespace gemm;
-
-// fp32 sums, operands bf16 or fp16, 128 lanes
-uint32_t idesc16(int dtype, bool a_mn, bool b_mn)
+// fp32 sums, operands bf16 or fp16, `lanes` rows of which `a` is the rows' operand
+uint32_t idesc16(int dtype, int lanes, bool a_mn, bool b_mn)
 {
     const uint32_t f = dtype == MOE_DTYPE_BF16 ? 1u : 0u;
-    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(kM >> 4) << 24);
+    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(lanes >> 4) << 24);
 }
 
 template <typename T>
@@ -80,90 +78,106 @@ __global__ void __launch_bounds__(256)
     reinterpret_cast<uint4 *>(du)[i] = q.v;
 }
 
-cudaError_t box_maps(CUtensorMap (&m)[kBoxMaps], const void *b, int cols, long long ld, int rows)
+template <int N>
+cudaError_t box_maps(CUtensorMap (&m)[N], const void *b, int cols, long long ld, int rows)
 {
     cudaError_t e = cudaSuccess;
-    for (int k = 0; k < kBoxMaps && e == cudaSuccess; ++k) e = rows_map(&m[k], b, 16, cols, ld, rows, 16 << k);
+    for (int k = 0; k < N && e == cudaSuccess; ++k) e = rows_map(&m[k], b, 16, cols, ld, rows, 16 << k);
     return e;
 }
 
-cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,
-                    void *h, void *g, void *u, int32_t *err, cudaStream_t st)
+// T <= kFewTokens: the weights' rows on the lanes, the tokens on the columns
+constexpr int kFewTokens = 32;
+
+cudaError_t forward_few(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,
+                        void *h, void *g, void *u, int32_t *err, cudaStream_t st)
 {
-    Maps m;
-    cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, kM);
-    if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, kM);
-    if (e == cudaSuccess) e = box_maps(m.b[0], x, H, ldx, T);
+    gemm::Maps m;
+    cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, gemm::kM);
+    if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, gemm::kM);
+    if (e == cudaSuccess) e = box_maps(m.b, x, H, ldx, T);
     if (e != cudaSuccess) return e;
-    Args a = {};
+    gemm::Args a = {};
     a.E = 1;
     a.rows = T;
     a.M = F;
-    a.ksteps = a.kphase = (H + 63) / 64;
+    a.ksteps = (H + 63) / 64;
     a.out[0] = h;
     a.out[1] = g;
     a.out[2] = u;
     a.ld = F;
     a.dtype = dtype;
-    a.idesc = idesc16(dtype, false, false);
+    a.idesc = idesc16(dtype, gemm::kM, false, false);
     a.err = err;
-    const int sms = num_sms(), mtiles = (F + kM - 1) / kM;
-    if (T <= 32) {
-        // one column chunk: a cluster a tile while tiles are fewer than SMs
-        a.split = choose_split<kGate, 32>(mtiles, a.ksteps);
-        return launch<kGate, 32>(a, m, std::min(mtiles, sms / a.split) * a.split, st);
-    }
-    a.split = 1;
-    return launch<kGate, 256>(a, m, (int)std::min<long long>((long long)mtiles * ((T + 255) / 256), sms), st);
+    const int mtiles = (F + gemm::kM - 1) / gemm::kM;
+    a.split = gemm::choose_split<gemm::kGate, kFewTokens>(mtiles, a.ksteps);
+    return gemm::launch<gemm::kGate, kFewTokens>(a, m, std::min(mtiles, num_sms() / a.split) * a.split, st);
+}
+
+cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,
+                    void *h, void *g, void *u, int32_t *err, cudaStream_t st)
+{
+    if (T <= kFewTokens) return forward_few(x, ldx, wg, wu, dtype, T, H, F, h, g, u, err, st);
+    gemm16::Maps m;
+    cudaError_t e = rows_map(&m.r[0], x, 16, H, ldx, T, gemm16::kLanes);
+    if (e == cudaSuccess) e = box_maps(m.c[0], wg, H, H, F);
+    if (e == cudaSuccess) e = box_maps(m.c[1], wu, H, H, F);
+    if (e != cudaSuccess) return e;
+    gemm16::Args a = {};
+    a.rows = T;
+    a.cols = F;
+    a.groups = 1;
+    a.ksteps = a.kphase = (H + 63) / 64;
+    a.out[0] = h;
+    a.out[1] = g;
+    a.out[2] = u;
+    a.dtype = dtype;
+    a.idesc = idesc16(dtype, 2 * gemm16::kLanes, false, false);
+    a.err = err;
+    return gemm16::launch<gemm16::kGate2>(a, m, st);
 }
 
 cudaError_t grad_x(const void *dg, const void *du, const void *wg, const void *wu, int dtype, int T, int H, int F,
                    void *dx, int32_t *err, cudaStream_t st)
 {
-    Maps m;
-    cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, 64);
-    if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, 64);
-    if (e == cudaSuccess) e = box_maps(m.b[0], dg, F, F, T);
-    if (e == cudaSuccess) e = box_maps(m.b[1], du, F, F, T);
+    gemm16::Maps m;
+    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, gemm16::kLanes);
+    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, gemm16::kLanes);
+    if (e == cudaSuccess) e = rows_map(&m.c[0][0], wg, 16, H, H, F, 64);
+    if (e == cudaSuccess) e = rows_map(&m.c[1][0], wu, 16, H, H, F, 64);
     if (e != cudaSuccess) return e;
-    Args a = {};
-    a.E = 1;
+    gemm16::Args a = {};
     a.rows = T;
-    a.M = H;
+    a.cols = H;
+    a.groups = 1;
     a.kphase = (F + 63) / 64;
     a.ksteps = 2 * a.kphase;
-    a.split = 1;
     a.out[0] = dx;
-    a.ld = H;
     a.dtype = dtype;
-    a.idesc = idesc16(dtype, true, false);
+    a.idesc = idesc16(dtype, 2 * gemm16::kLanes, false, true);
     a.err = err;
-    const long long tiles = (long long)((H + kM - 1) / kM) * ((T + 255) / 256);
-    return launch<kDx, 256>(a, m, (int)std::min<long long>(tiles, num_sms()), st);
+    return gemm16::launch<gemm16::kDx>(a, m, st);
 }
 
 cudaError_t grad_w(const void *dg, const void *du, const void *x, long long ldx, int dtype, int T, int H, int F,
                    void *dwg, void *dwu, int32_t *err, cudaStream_t st)
 {
-    Maps m;
-    cudaError_t e = rows_map(&m.a[0], x, 16, H, ldx, T, 64);
-    if (e == cudaSuccess) e = rows_map(&m.b[0][0], dg, 16, F, F, T, 64);
-    if (e == cudaSuccess) e = rows_map(&m.b[1][0], du, 16, F, F, T, 64);
+    gemm16::Maps m;
+    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, 64);
+    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, 64);
+    if (e == cudaSuccess) e = rows_map(&m.c[0][0], x, 16, H, ldx, T, 64);
     if (e != cudaSuccess) return e;
-    Args a = {};
-    a.E = 2;
+    gemm16::Args a = {};
     a.rows = F;
-    a.M = H;
+    a.cols = H;
+    a.groups = 2;
     a.ksteps = a.kphase = (T + 63) / 64;
-    a.split = 1;
     a.out[0] = dwg;
     a.out[1] = dwu;
-    a.ld = H;
     a.dtype = dtype;
-    a.idesc = idesc16(dtype, true, true);
+    a.idesc = idesc16(dtype, 2 * gemm16::kLanes, true, true);
     a.err = err;
-    const long long tiles = 2ll * ((H + kM - 1) / kM) * ((F + 255) / 256);
-    return launch<kDw, 256>(a, m, (int)std::min<long long>(tiles, num_sms()), st);
+    return gemm16::launch<gemm16::kDw>(a, m, st);
 }
 
 constexpr int kMaxGatedDim = 65536, kMaxGatedT = 1 << 24;

@@ -1,0 +1,360 @@
+// gemm16.cuh -- the 16-bit matrix products of the gated block on pairs of SMs (tcgen05
+// cta_group::2): output rows on the accumulator's lanes, output columns on its columns.
+//   kGate2   h = silu(x Wg^T) * (x Wu^T)     rows T, columns F; two column operands, two sums
+//   kDx      dx = dg Wg + du Wu              rows T, columns H; two phases of the reduction
+//   kDw      dWg = dg^T x, dWu = du^T x      rows F, columns H; two groups of tiles
+//
+// Why pairs: a 128 x 256 tile of one SM moves 48 KB into shared memory and 48 KB out of it for
+// 512 cycles of the tensor pipe, 192 bytes a cycle where shared memory gives 128 and L2 about 64
+// into an SM; that form stood at 1.28 PFLOP/s.  A pair works on 256 x 256, each SM holding its
+// 128 rows and half of the columns' operand: 32 KB in and out.
+//
+// A thread of the epilogue holds consecutive columns of one output row, so that it writes 16
+// bytes at a time with no exchange between lanes.
+//
+// Tiles: 256 rows x `width` columns (a multiple of 32, chosen by the host so that the tiles
+// fill whole waves of SM pairs).  Warps of each CTA: 0 its operand loads (TMA), 1 of the leader
+// the MMAs, 4-11 the epilogue, two for each quarter of the lanes.  Barriers: `full` lives in
+// the leader (both CTAs' copies complete on it); `empty` and `dfull` are in both (multicast
+// commits); `dempty` in the leader (both epilogues arrive).  Waits are bounded as in gemm_tc.cuh.
+#pragma once
+
+#include "gemm_tc.cuh"
+
+namespace moe {
+namespace gemm16 {
+
+using gemm::cluster_sync;
+using gemm::expect_tx;
+using gemm::map_rank;
+
+enum Mode { kGate2, kDx, kDw };
+
+constexpr int kLanes = 128;   // rows of a CTA (a pair: 256)
+constexpr int kMaxCols = 256;
+constexpr int kBoxMaps = 4;   // column-operand maps with boxes of 16 << k rows
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+
+constexpr bool rows_mn(Mode m) { return m == kDw; }    // rows operand stored reduction-major
+constexpr bool cols_mn(Mode m) { return m != kGate2; }
+
+struct Args {
+    int rows, cols;          // of the output (one group)
+    int mtiles, ntiles;      // 256-row tiles, column chunks
+    int width;               // columns of a chunk, a multiple of 32, at most 256
+    int groups;              // kDw: 2 (gate, up)
+    int ksteps, kphase;      // stages of 64; kDx: stages of the first phase
+    void *out[3];            // (h, g, u) | dx | (dWg, dWu)
+    int dtype;
+    uint32_t idesc;          // without N
+    int32_t *err;
+};
+
+struct Maps {
+    CUtensorMap r[2];                 // rows operand, by phase (kDx) or group (kDw)
+    CUtensorMap c[2][kBoxMaps];       // columns operand: gate, up (kGate2) or by phase; reduction-major: [i][0] alone
+};
+
+template <Mode MODE>
+struct Cfg {
+    static constexpr int NB = MODE == kGate2 ? 2 : 1;
+    static constexpr int NBUF = MODE == kGate2 ? 1 : 2;
+    static constexpr int OP = kLanes * 128;                 // bytes of one operand's part in a CTA
+    static constexpr int STAGE = (1 + NB) * OP;
+    static constexpr int STAGES = MODE == kGate2 ? 4 : 6;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 512;
+};
+
+struct Ctrl {
+    uint64_t full[6], empty[6], dfull[2], dempty[2], fin;
+    uint32_t tmem;
+    int abort;
+};
+
+// descriptor of an operand tile stored reduction-major (64 lanes or columns of 128 bytes per
+// reduction index, 128-byte swizzle): 64-wide chunks 8192 bytes apart, 8 reduction indices 1024
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(8192u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ bool stopped(const Ctrl *c) { return *(volatile const int *)&c->abort != 0; }
+
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
+{
+    uint32_t ok = 0;
+    for (int n = 0; n < kWaitLimit && !ok; ++n)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    if (!ok) {
+        atomicOr(err, kErrTimeout);
+        atomicExch(&c->abort, 1);
+    }
+    return __all_sync(0xffffffffu, ok != 0);
+}
+
+// TMA into this CTA's shared memory, completing on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// one arrival on this barrier of both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_remote(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 8 consecutive columns -> 16 bytes
+__device__ __forceinline__ uint4 pack8(const float *v, int dtype)
+{
+    uint4 o;
+    uint32_t *w = &o.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (dtype == MOE_DTYPE_BF16) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        } else {
+            const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+    }
+    return o;
+}
+
+__device__ __forceinline__ void put8(void *out, size_t at, const float *v, int dtype)
+{
+    *reinterpret_cast<uint4 *>(static_cast<char *>(out) + at * 2) = pack8(v, dtype);
+}
+
+template <Mode MODE>
+__global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
+{
+    using C = Cfg<MODE>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Ctrl *c = reinterpret_cast<Ctrl *>(ring + C::STAGES * C::STAGE);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&c->full[i], 1);
+            mbar_init(&c->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->dfull[i], 1);
+            mbar_init(&c->dempty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&c->fin, 1);
+        c->abort = 0;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();   // the pair's barriers and TMEM are ready
+    tc::fence_after_sync();
+    const uint32_t tmem = c->tmem;
+    const int per_group = a.mtiles * a.ntiles, total = a.groups * per_group;
+
+    if (warp == 0) {
+        // ---------------- operands by TMA ---------------------------------------------------
+        const uint32_t r0 = smem_u32(ring);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = pair; t < total && ok && !stopped(c); t += pairs) {
+            const int g = t / per_group, mi = (t - g * per_group) / a.ntiles, ni = t - g * per_group - mi * a.ntiles;
+            const int m0 = mi * 2 * kLanes + rank * kLanes, n0 = ni * a.width;
+            const int half = ((min(a.width, a.cols - n0) + 31) & ~31) >> 1;   // this CTA's columns
+            const int boxes = (half + 63) >> 6;
+            const uint32_t bytes = 2u * (C::OP + C::NB * (cols_mn(MODE) ? boxes * 8192u : half * 128u));
+            for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
+                const uint32_t s = it % C::STAGES;
+                if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
+                if (rank == 0) expect_tx(smem_u32(&c->full[s]), bytes);
+                const uint32_t bar = map_rank(smem_u32(&c->full[s]), 0);
+                const uint32_t rs = r0 + s * C::STAGE, cs = rs + C::OP;
+                const int ph = MODE == kDx && ks >= a.kphase;
+                const int k = 64 * (ph ? ks - a.kphase : ks), sel = MODE == kDw ? g : ph;
+                if constexpr (rows_mn(MODE)) {
+                    tma_2d_pair(rs, &maps.r[sel], m0, k, bar);
+                    tma_2d_pair(rs + 8192, &maps.r[sel], m0 + 64, k, bar);
+                } else {
+                    tma_2d_pair(rs, &maps.r[sel], k, m0, bar);
+                }
+                const int cfirst = n0 + rank * half;
+#pragma unroll
+                for (int o = 0; o < C::NB; ++o) {
+                    if constexpr (cols_mn(MODE)) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_2d_pair(cs + i * 8192, &maps.c[MODE == kDx ? ph : 0][0], cfirst + 64 * i, k, bar);
+                    } else {
+                        int r = 0;
+#pragma unroll
+                        for (int b = kBoxMaps - 1; b >= 0; --b)
+                            if (half - r >= (16 << b)) {
+                                tma_2d_pair(cs + o * C::OP + r * 128, &maps.c[o][b], k, cfirst + r, bar);
+                                r += 16 << b;
+                            }
+                    }
+                }
+            }
+        }
+        // copies still in flight (after a wait that gave up) land before the pair ends
+        if (rank == 0)
+            for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- MMA issue, for both CTAs ------------------------------------------
+        const uint32_t r0 = smem_u32(ring);
+        uint32_t it = 0, nt = 0;
+        bool ok = true;
+        for (int t = pair; t < total && ok && !stopped(c); t += pairs, ++nt) {
+            const int ni = t % per_group % a.ntiles;
+            const int np = (min(a.width, a.cols - ni * a.width) + 31) & ~31;
+            const uint32_t idesc = a.idesc | (uint32_t)(np >> 3) << 17;
+            const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
+            if (use >= 1 && !(ok = wait_warp(&c->dempty[buf], (use - 1) & 1, c, a.err))) break;
+            for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
+                const uint32_t s = it % C::STAGES;
+                if (!(ok = wait_warp(&c->full[s], (it / C::STAGES) & 1, c, a.err))) break;
+                tc::fence_after_sync();
+                const uint32_t rs = r0 + s * C::STAGE, cs = rs + C::OP;
+                const uint64_t rd = rows_mn(MODE) ? sdesc_mn_sw128(rs) : tc::sdesc_kmajor_sw128(rs);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int o = 0; o < C::NB; ++o) {
+                        const uint64_t cd = cols_mn(MODE) ? sdesc_mn_sw128(cs) : tc::sdesc_kmajor_sw128(cs + o * C::OP);
+                        mma_pair(tmem + buf * kMaxCols + o * kMaxCols, rd + (rows_mn(MODE) ? k * 128 : k * 2),
+                                 cd + (cols_mn(MODE) ? k * 128 : k * 2), idesc, ks > 0 || k > 0);
+                    }
+                commit_pair(&c->empty[s]);
+            }
+            commit_pair(&c->dfull[buf]);
+        }
+        commit_pair(&c->fin);   // every MMA is done before TMEM is freed
+        wait_warp(&c->fin, 0, c, a.err);
+    } else if (warp >= 4) {
+        // ---------------- epilogue ----------------------------------------------------------
+        const int qd = warp & 3, part = (warp - 4) >> 2;
+        const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
+        uint32_t nt = 0;
+        bool ok = true;
+        for (int t = pair; t < total && ok && !stopped(c); t += pairs, ++nt) {
+            const int g = t / per_group, mi = (t - g * per_group) / a.ntiles, ni = t - g * per_group - mi * a.ntiles;
+            const int row = mi * 2 * kLanes + rank * kLanes + qd * 32 + lane, n0 = ni * a.width;
+            const int n = min(a.width, a.cols - n0);
+            const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
+            if (!(ok = wait_warp(&c->dfull[buf], use & 1, c, a.err))) break;
+            tc::fence_after_sync();
+            const size_t at = (size_t)row * a.cols + n0;
+            void *out = MODE == kDw ? a.out[g] : a.out[0];
+            // 32 columns at a time, alternately to the two warps of these lanes; the width is a
+            // multiple of 32, the columns of 8
+            for (int c0 = part * 32; c0 < n; c0 += 64) {
+                uint32_t v[2][32];
+#pragma unroll
+                for (int o = 0; o < C::NB; ++o) tc::ld32(tl + buf * kMaxCols + o * kMaxCols + c0, v[o]);
+                tc::wait_ld();
+                if (row < a.rows) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (c0 + j >= n) break;
+                        float x[8], y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[0][j + i]);
+                        if constexpr (MODE == kGate2) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(v[1][j + i]);
+                            if (a.out[1]) {
+                                put8(a.out[1], at + c0 + j, x, a.dtype);
+                                put8(a.out[2], at + c0 + j, y, a.dtype);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = gemm::silu(x[i]) * y[i];
+                        }
+                        put8(out, at + c0 + j, x, a.dtype);
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_remote(map_rank(smem_u32(&c->dempty[buf]), 0));
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
+    if (warp == 1) {
+        tc::fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <Mode MODE>
+cudaError_t launch(Args a, const Maps &m, cudaStream_t st)
+{
+    // Column chunks: the count whose waves of SM pairs take least, by what a tile costs in
+    // cycles: its reduction at the tensor pipe's rate or what L2 feeds an SM, whichever is more,
+    // and a fixed start and end.
+    const int pairs = num_sms() / 2;
+    a.mtiles = (a.rows + 2 * kLanes - 1) / (2 * kLanes);
+    double best = 0;
+    for (int nt = (a.cols + kMaxCols - 1) / kMaxCols; nt <= (a.cols + 31) / 32; ++nt) {
+        const int w = ((a.cols + nt - 1) / nt + 31) & ~31;
+        const long long tiles = (long long)a.groups * a.mtiles * ((a.cols + w - 1) / w);
+        if (best > 0 && tiles > 8 * pairs) break;
+        const double stage = std::max(2.0 * w * Cfg<MODE>::NB, (16384.0 + 64.0 * w * Cfg<MODE>::NB) / 64);
+        const double cost = (double)((tiles + pairs - 1) / pairs) * (a.ksteps * stage + 3000.0 + 4.0 * w * Cfg<MODE>::NB);
+        if (best == 0 || cost < best) {
+            best = cost;
+            a.width = w;
+        }
+    }
+    a.ntiles = (a.cols + a.width - 1) / a.width;
+    const long long tiles = (long long)a.groups * a.mtiles * a.ntiles;
+    const int grid = 2 * (int)std::min<long long>(tiles, pairs);
+    return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(kThreads), Cfg<MODE>::SMEM, st, 2, a, m);
+}
+
+}  // namespace gemm16
+}  // namespace moe

@@ -1,14 +1,11 @@
 // gemm_tc.cuh -- the tcgen05 matrix-product kernel behind the MXFP4 operators and the 16-bit
-// gated block.  One kernel template, five uses:
+// gated block for few tokens.  One kernel template, three uses:
 //   kMxGate   h = q(silu(x Wg^T) * (x Wu^T)), x and W in MXFP4, h requantised to MXFP4
 //   kMxMul    y = x W^T, x and W in MXFP4
 //   kGate     h = silu(x Wg^T) * (x Wu^T) in 16 bits (g and u kept on request)
-//   kDx       dx = dg Wg + du Wu in 16 bits
-//   kDw       dWg = dg^T x, dWu = du^T x in 16 bits
 //
-// Orientation.  The accumulator's 128 lanes are the output's contiguous dimension (weight rows;
-// for dx and dW the model width) and its columns the other one (tokens; for dW the rows of the
-// weight).  A weight tile is then always a full 128-lane operand, however few tokens there
+// Orientation.  The accumulator's 128 lanes are weight rows (the output's contiguous dimension)
+// and its columns tokens.  A weight tile is then always a full 128-lane operand, however few tokens there
 // are, and a warp's lanes write consecutive output elements.  The MMA's column count follows the
 // tile's token count in steps of 16, so one token costs 16 columns.
 //
@@ -45,31 +42,28 @@
 namespace moe {
 namespace gemm {
 
-enum Mode { kMxGate, kMxMul, kGate, kDx, kDw };
+enum Mode { kMxGate, kMxMul, kGate };
 
 constexpr int kM = 128;          // lanes of a tile
-constexpr int kBoxMaps = 5;      // column-operand maps with boxes of 16 << k rows
+constexpr int kBoxMaps = 4;      // column-operand maps with boxes of 16 << k rows
 constexpr int kMaxGroups = 512;
 
 constexpr bool is_mx(Mode m) { return m == kMxGate || m == kMxMul; }
 constexpr bool is_gated(Mode m) { return m == kMxGate || m == kGate; }
-constexpr bool a_mn(Mode m) { return m == kDx || m == kDw; }   // lanes operand stored reduction-major
-constexpr bool b_mn(Mode m) { return m == kDw; }
 
 // the kernel's parameters (tensor maps apart)
 struct Args {
-    const int32_t *offsets;    // [E + 1] rows of each group (null: every group is rows 0 .. rows)
+    const int32_t *offsets;    // [E + 1] rows of each group (null: one group of all rows)
     int E;                     // groups
     int rows;                  // columns of the output (tokens) in all
     int M;                     // lanes dimension of one group
     int ksteps;                // stages of the whole reduction
-    int kphase;                // kDx: stages of the first phase (gate); else == ksteps
     int split;                 // CTAs that share a tile (the cluster size)
     // scale bytes [rows][sf_ld] of the lanes operands (groups * M rows) and the columns operand
     const uint8_t *sfa[2], *sfb;
     int sf_ld;                 // K / 32
     long long sfa_rows;        // E * M
-    void *out[3];              // y | (h, g, u) | (dWg, dWu) | (codes, scales)
+    void *out[3];              // y | (h, g, u) | (codes, scales)
     int ld;                    // row stride of out, in elements (codes: of M)
     int dtype;                 // MOE_DTYPE_* of out
     uint32_t idesc;            // instruction descriptor without N and the scale ids
@@ -78,7 +72,7 @@ struct Args {
 
 struct Maps {
     CUtensorMap a[2];
-    CUtensorMap b[2][kBoxMaps];   // [0]: boxes 16 << k rows (reduction contiguous); kDw: [g][0], 64 x 64 boxes
+    CUtensorMap b[kBoxMaps];   // boxes of 16 << k rows
 };
 
 template <Mode MODE, int BN>
@@ -161,14 +155,6 @@ __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
         : "memory");
-}
-
-// descriptor of an operand tile stored reduction-major (64 lanes or columns of 128 bytes per
-// reduction index, 128-byte swizzle): 64-wide chunks 8192 bytes apart, 8 reduction indices 1024
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr)
-{
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(8192u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
 // descriptor of a 512-byte scale block: 32 rows of 16 bytes, no swizzle, 8-row groups 128 apart
@@ -260,7 +246,10 @@ __device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
     return r;
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// g sigmoid(g).  The fast exponential and quotient are off by a few units of fp32's last place
+// (more by |g| * 2^-24 for large |g|), far below the 16-bit or 4-bit rounding that follows; the
+// exact ones were most of the epilogue's instructions.  An exponential that overflows gives 0.
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 __device__ __forceinline__ void store(void *p, int dtype, size_t i, float v)
 {
@@ -307,7 +296,7 @@ __device__ __forceinline__ void emit_mx8(const Args &a, const float (&v)[8], int
 
 // NC columns of a tile (acc[0..NA-1][j]) -> the outputs; col(j): column j's output row, or -1
 template <Mode MODE, int NC, class Col>
-__device__ __forceinline__ void emit(const Args &a, const float (&g)[NC], const float (&u)[NC], int e, int m, int lane,
+__device__ __forceinline__ void emit(const Args &a, const float (&g)[NC], const float (&u)[NC], int m, int lane,
                                      Col col)
 {
     if constexpr (MODE == kMxGate) {
@@ -320,7 +309,7 @@ __device__ __forceinline__ void emit(const Args &a, const float (&g)[NC], const 
         }
     } else {
         if (m >= a.M) return;
-        void *out = MODE == kDw ? a.out[e] : a.out[0];
+        void *out = a.out[0];
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             const int r = col(j);
@@ -451,35 +440,23 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
             const Tile q = get_tile<BN>(a, c, t);
-            const int boxes = (q.np + 63) >> 6;
-            const uint32_t bytes = C::NA * C::A_BYTES + (b_mn(MODE) ? boxes * 8192u : (uint32_t)q.np * 128u);
+            const uint32_t bytes = C::NA * C::A_BYTES + (uint32_t)q.np * 128u;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
                 const uint32_t bar = smem_u32(&c->full[s]);
                 const uint32_t as = r0 + s * (C::NA * C::A_BYTES + C::B_BYTES), bs = as + C::NA * C::A_BYTES;
                 expect_tx(bar, bytes);
-                const int ph = MODE == kDx && ks >= a.kphase;
-                const int kk = MODE == kDx && ph ? ks - a.kphase : ks;
-                if constexpr (a_mn(MODE)) {
-                    tma_2d(as, &maps.a[ph], q.m0, kk * 64, bar);
-                    tma_2d(as + 8192, &maps.a[ph], q.m0 + 64, kk * 64, bar);
-                } else {
+                const int x = ks * (C::MX ? 128 : 64);
 #pragma unroll
-                    for (int o = 0; o < C::NA; ++o)
-                        tma_2d(as + o * C::A_BYTES, &maps.a[o], kk * (C::MX ? 128 : 64), q.e * a.M + q.m0, bar);
-                }
-                if constexpr (b_mn(MODE)) {
-                    for (int i = 0; i < boxes; ++i) tma_2d(bs + i * 8192, &maps.b[q.e][0], q.row0 + 64 * i, kk * 64, bar);
-                } else {
-                    int r = 0;
+                for (int o = 0; o < C::NA; ++o) tma_2d(as + o * C::A_BYTES, &maps.a[o], x, q.e * a.M + q.m0, bar);
+                int r = 0;
 #pragma unroll
-                    for (int k = kBoxMaps - 1; k >= 0; --k)
-                        if (q.np - r >= (16 << k)) {
-                            tma_2d(bs + r * 128, &maps.b[ph][k], kk * (C::MX ? 128 : 64), q.row0 + r, bar);
-                            r += 16 << k;
-                        }
-                }
+                for (int k = kBoxMaps - 1; k >= 0; --k)
+                    if (q.np - r >= (16 << k)) {
+                        tma_2d(bs + r * 128, &maps.b[k], x, q.row0 + r, bar);
+                        r += 16 << k;
+                    }
             }
         }
         // copies still in flight (after a wait that gave up) land before the CTA ends
@@ -519,13 +496,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 } else {
                     tc::fence_after_sync();
                 }
-                const uint64_t bd = b_mn(MODE) ? sdesc_mn_sw128(bs) : tc::sdesc_kmajor_sw128(bs);
+                const uint64_t bd = tc::sdesc_kmajor_sw128(bs);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o) {
-                        const uint64_t ad = a_mn(MODE) ? sdesc_mn_sw128(as) : tc::sdesc_kmajor_sw128(as + o * C::A_BYTES);
-                        const uint64_t ka = ad + (a_mn(MODE) ? k * 128 : k * 2), kb = bd + (b_mn(MODE) ? k * 128 : k * 2);
+                        const uint64_t ka = tc::sdesc_kmajor_sw128(as + o * C::A_BYTES) + k * 2, kb = bd + k * 2;
                         if constexpr (C::MX) {
                             const uint32_t id = idesc | (uint32_t)((k & 1) * 2) << 29 | (uint32_t)((k & 1) * 2) << 4;
                             mma_mx4(d0 + o * BN, ka, kb, id, sfc + (k >> 1) * 16 + o * 4, sfc + (k >> 1) * 16 + 8, ks > ks0 || k > 0);
@@ -589,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                                 for (int r = 0; r < S; ++r) x += red[(o * C::RED_COLS + r * per + i0 + j) * kM + qd * 32 + lane];
                             v[o][j] = x;
                         }
-                    emit<MODE, 8>(a, v[0], v[C::NA - 1], q.e, m, lane, [&](int j) {
+                    emit<MODE, 8>(a, v[0], v[C::NA - 1], m, lane, [&](int j) {
                         const int k = (i0 + j) * S + rank;
                         return k < q.n ? q.row0 + k : -1;
                     });
@@ -613,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                     for (int o = 0; o < C::NA; ++o)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) f[o][j] = __uint_as_float(v[o][j]);
-                    emit<MODE, 16>(a, f[0], f[C::NA - 1], q.e, m, lane,
+                    emit<MODE, 16>(a, f[0], f[C::NA - 1], m, lane,
                                    [&](int j) { return c0 + j < q.n ? q.row0 + c0 + j : -1; });
                 }
             }

@@ -17,7 +17,7 @@ cudaError_t code_maps(Maps &m, const uint8_t *a0, const uint8_t *a1, long long a
 {
     cudaError_t e = rows_map(&m.a[0], a0, 8, K / 2, K / 2, arows, kM);
     if (e == cudaSuccess && a1) e = rows_map(&m.a[1], a1, 8, K / 2, K / 2, arows, kM);
-    for (int k = 0; k < kBoxMaps && e == cudaSuccess; ++k) e = rows_map(&m.b[0][k], b, 8, K / 2, K / 2, rows, 16 << k);
+    for (int k = 0; k < kBoxMaps && e == cudaSuccess; ++k) e = rows_map(&m.b[k], b, 8, K / 2, K / 2, rows, 16 << k);
     return e;
 }
 
@@ -52,7 +52,7 @@ cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, c
     a.E = E;
     a.rows = rows;
     a.M = N;
-    a.ksteps = a.kphase = (K + 255) / 256;
+    a.ksteps = (K + 255) / 256;
     a.sfa[0] = ws;
     a.sfb = xs;
     a.sf_ld = K / 32;
@@ -77,7 +77,7 @@ cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, 
     a.E = E;
     a.rows = rows;
     a.M = F;
-    a.ksteps = a.kphase = (K + 255) / 256;
+    a.ksteps = (K + 255) / 256;
     a.sfa[0] = sg;
     a.sfa[1] = su;
     a.sfb = xs;
