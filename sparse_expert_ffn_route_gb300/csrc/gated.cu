@@ -78,14 +78,6 @@ __global__ void __launch_bounds__(256)
     reinterpret_cast<uint4 *>(du)[i] = q.v;
 }
 
-template <int N>
-cudaError_t box_maps(CUtensorMap (&m)[N], const void *b, int cols, long long ld, int rows)
-{
-    cudaError_t e = cudaSuccess;
-    for (int k = 0; k < N && e == cudaSuccess; ++k) e = rows_map(&m[k], b, 16, cols, ld, rows, 16 << k);
-    return e;
-}
-
 // T <= kFewTokens: the weights' rows on the lanes, the tokens on the columns
 constexpr int kFewTokens = 32;
 
@@ -95,7 +87,7 @@ cudaError_t forward_few(const void *x, long long ldx, const void *wg, const void
     gemm::Maps m;
     cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, gemm::kM);
     if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, gemm::kM);
-    if (e == cudaSuccess) e = box_maps(m.b, x, H, ldx, T);
+    for (int k = 0; 16 * (k + 1) <= kFewTokens && e == cudaSuccess; ++k) e = rows_map(&m.b[k], x, 16, H, ldx, T, 16 * (k + 1));
     if (e != cudaSuccess) return e;
     gemm::Args a = {};
     a.E = 1;
@@ -118,11 +110,6 @@ cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu
                     void *h, void *g, void *u, int32_t *err, cudaStream_t st)
 {
     if (T <= kFewTokens) return forward_few(x, ldx, wg, wu, dtype, T, H, F, h, g, u, err, st);
-    gemm16::Maps m;
-    cudaError_t e = rows_map(&m.r[0], x, 16, H, ldx, T, gemm16::kLanes);
-    if (e == cudaSuccess) e = box_maps(m.c[0], wg, H, H, F);
-    if (e == cudaSuccess) e = box_maps(m.c[1], wu, H, H, F);
-    if (e != cudaSuccess) return e;
     gemm16::Args a = {};
     a.rows = T;
     a.cols = F;
@@ -134,18 +121,17 @@ cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu
     a.dtype = dtype;
     a.idesc = idesc16(dtype, 2 * gemm16::kLanes, false, false);
     a.err = err;
-    return gemm16::launch<gemm16::kGate2>(a, m, st);
+    gemm16::plan(a, 2);
+    gemm16::Maps m;
+    cudaError_t e = rows_map(&m.r[0], x, 16, H, ldx, T, gemm16::kLanes);
+    if (e == cudaSuccess) e = rows_map(&m.c[0], wg, 16, H, H, F, a.width / 2);
+    if (e == cudaSuccess) e = rows_map(&m.c[1], wu, 16, H, H, F, a.width / 2);
+    return e == cudaSuccess ? gemm16::launch<gemm16::kGate2>(a, m, st) : e;
 }
 
 cudaError_t grad_x(const void *dg, const void *du, const void *wg, const void *wu, int dtype, int T, int H, int F,
                    void *dx, int32_t *err, cudaStream_t st)
 {
-    gemm16::Maps m;
-    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, gemm16::kLanes);
-    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, gemm16::kLanes);
-    if (e == cudaSuccess) e = rows_map(&m.c[0][0], wg, 16, H, H, F, 64);
-    if (e == cudaSuccess) e = rows_map(&m.c[1][0], wu, 16, H, H, F, 64);
-    if (e != cudaSuccess) return e;
     gemm16::Args a = {};
     a.rows = T;
     a.cols = H;
@@ -156,17 +142,18 @@ cudaError_t grad_x(const void *dg, const void *du, const void *wg, const void *w
     a.dtype = dtype;
     a.idesc = idesc16(dtype, 2 * gemm16::kLanes, false, true);
     a.err = err;
-    return gemm16::launch<gemm16::kDx>(a, m, st);
+    gemm16::plan(a, 1);
+    gemm16::Maps m;
+    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, gemm16::kLanes);
+    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, gemm16::kLanes);
+    if (e == cudaSuccess) e = rows_map(&m.c[0], wg, 16, H, H, F, 64);
+    if (e == cudaSuccess) e = rows_map(&m.c[1], wu, 16, H, H, F, 64);
+    return e == cudaSuccess ? gemm16::launch<gemm16::kDx>(a, m, st) : e;
 }
 
 cudaError_t grad_w(const void *dg, const void *du, const void *x, long long ldx, int dtype, int T, int H, int F,
                    void *dwg, void *dwu, int32_t *err, cudaStream_t st)
 {
-    gemm16::Maps m;
-    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, 64);
-    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, 64);
-    if (e == cudaSuccess) e = rows_map(&m.c[0][0], x, 16, H, ldx, T, 64);
-    if (e != cudaSuccess) return e;
     gemm16::Args a = {};
     a.rows = F;
     a.cols = H;
@@ -177,7 +164,12 @@ cudaError_t grad_w(const void *dg, const void *du, const void *x, long long ldx,
     a.dtype = dtype;
     a.idesc = idesc16(dtype, 2 * gemm16::kLanes, true, true);
     a.err = err;
-    return gemm16::launch<gemm16::kDw>(a, m, st);
+    gemm16::plan(a, 1);
+    gemm16::Maps m;
+    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, 64);
+    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, 64);
+    if (e == cudaSuccess) e = rows_map(&m.c[0], x, 16, H, ldx, T, 64);
+    return e == cudaSuccess ? gemm16::launch<gemm16::kDw>(a, m, st) : e;
 }
 
 constexpr int kMaxGatedDim = 65536, kMaxGatedT = 1 << 24;

@@ -13,8 +13,10 @@
 // bytes at a time with no exchange between lanes.
 //
 // Tiles: 256 rows x `width` columns (a multiple of 32, chosen by the host so that the tiles
-// fill whole waves of SM pairs).  Warps of each CTA: 0 its operand loads (TMA), 1 of the leader
-// the MMAs, 4-11 the epilogue, two for each quarter of the lanes.  Barriers: `full` lives in
+// fill whole waves of SM pairs).  Warps of each CTA: 0-3 its operand loads, one TMA box of a
+// stage each (a box costs the warp that issues it about 270 cycles beside its 1.8 a row, and
+// boxes of different warps overlap: three boxes of a stage from one warp held the stage at 700
+// cycles), 4-11 the epilogue, two for each quarter of the lanes, 12 of the leader the MMAs.  Barriers: `full` lives in
 // the leader (both CTAs' copies complete on it); `empty` and `dfull` are in both (multicast
 // commits); `dempty` in the leader (both epilogues arrive).  Waits are bounded as in gemm_tc.cuh.
 #pragma once
@@ -32,8 +34,8 @@ enum Mode { kGate2, kDx, kDw };
 
 constexpr int kLanes = 128;   // rows of a CTA (a pair: 256)
 constexpr int kMaxCols = 256;
-constexpr int kBoxMaps = 4;   // column-operand maps with boxes of 16 << k rows
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
+constexpr int kWarpMma = 12;
 constexpr int kEpiWarps = 8;
 
 constexpr bool rows_mn(Mode m) { return m == kDw; }    // rows operand stored reduction-major
@@ -52,8 +54,8 @@ struct Args {
 };
 
 struct Maps {
-    CUtensorMap r[2];                 // rows operand, by phase (kDx) or group (kDw)
-    CUtensorMap c[2][kBoxMaps];       // columns operand: gate, up (kGate2) or by phase; reduction-major: [i][0] alone
+    CUtensorMap r[2];   // rows operand, by phase (kDx) or group (kDw): boxes of 128 rows, or 64 x 64
+    CUtensorMap c[2];   // columns operand: gate, up (kGate2) or by phase: boxes of width / 2 rows, or 64 x 64
 };
 
 template <Mode MODE>
@@ -84,20 +86,12 @@ __device__ __forceinline__ bool stopped(const Ctrl *c) { return *(volatile const
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
 {
-    uint32_t ok = 0;
-    for (int n = 0; n < kWaitLimit && !ok; ++n)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
+    const bool ok = mbar_wait(bar, parity);
     if (!ok) {
         atomicOr(err, kErrTimeout);
         atomicExch(&c->abort, 1);
     }
-    return __all_sync(0xffffffffu, ok != 0);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // TMA into this CTA's shared memory, completing on a barrier of either CTA of the pair
@@ -182,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     }
     pdl_wait();
     pdl_launch_dependents();
-    if (warp == 1) {
+    if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -193,63 +187,49 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     const uint32_t tmem = c->tmem;
     const int per_group = a.mtiles * a.ntiles, total = a.groups * per_group;
 
-    if (warp == 0) {
-        // ---------------- operands by TMA ---------------------------------------------------
+    if (warp < 4) {
+        // ---------------- operands by TMA: box `warp` of every stage -------------------------
+        // reduction-major operands take two boxes of 64 (the second only where it is needed),
+        // the others one; rows first
+        constexpr int RB = rows_mn(MODE) ? 2 : 1;
         const uint32_t r0 = smem_u32(ring);
+        const bool of_rows = warp < RB;
+        const int i = of_rows ? warp : warp - RB;
+        const int half = a.width >> 1, boxes = cols_mn(MODE) ? (half + 63) >> 6 : C::NB;
+        const uint32_t bytes = 2u * (C::OP + boxes * (cols_mn(MODE) ? 8192u : half * 128u));
+        const uint32_t to = r0 + (of_rows ? i * 8192 : C::OP + i * (cols_mn(MODE) ? 8192 : C::OP));
         uint32_t it = 0;
         bool ok = true;
-        for (int t = pair; t < total && ok && !stopped(c); t += pairs) {
-            const int g = t / per_group, mi = (t - g * per_group) / a.ntiles, ni = t - g * per_group - mi * a.ntiles;
-            const int m0 = mi * 2 * kLanes + rank * kLanes, n0 = ni * a.width;
-            const int half = ((min(a.width, a.cols - n0) + 31) & ~31) >> 1;   // this CTA's columns
-            const int boxes = (half + 63) >> 6;
-            const uint32_t bytes = 2u * (C::OP + C::NB * (cols_mn(MODE) ? boxes * 8192u : half * 128u));
-            for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
-                const uint32_t s = it % C::STAGES;
-                if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
-                if (rank == 0) expect_tx(smem_u32(&c->full[s]), bytes);
-                const uint32_t bar = map_rank(smem_u32(&c->full[s]), 0);
-                const uint32_t rs = r0 + s * C::STAGE, cs = rs + C::OP;
-                const int ph = MODE == kDx && ks >= a.kphase;
-                const int k = 64 * (ph ? ks - a.kphase : ks), sel = MODE == kDw ? g : ph;
-                if constexpr (rows_mn(MODE)) {
-                    tma_2d_pair(rs, &maps.r[sel], m0, k, bar);
-                    tma_2d_pair(rs + 8192, &maps.r[sel], m0 + 64, k, bar);
-                } else {
-                    tma_2d_pair(rs, &maps.r[sel], k, m0, bar);
-                }
-                const int cfirst = n0 + rank * half;
-#pragma unroll
-                for (int o = 0; o < C::NB; ++o) {
-                    if constexpr (cols_mn(MODE)) {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_2d_pair(cs + i * 8192, &maps.c[MODE == kDx ? ph : 0][0], cfirst + 64 * i, k, bar);
-                    } else {
-                        int r = 0;
-#pragma unroll
-                        for (int b = kBoxMaps - 1; b >= 0; --b)
-                            if (half - r >= (16 << b)) {
-                                tma_2d_pair(cs + o * C::OP + r * 128, &maps.c[o][b], k, cfirst + r, bar);
-                                r += 16 << b;
-                            }
-                    }
+        if (of_rows || i < boxes)
+            for (int t = pair; t < total && ok && !stopped(c); t += pairs) {
+                const int g = t / per_group, mi = (t - g * per_group) / a.ntiles, ni = t - g * per_group - mi * a.ntiles;
+                const int m0 = mi * 2 * kLanes + rank * kLanes + (rows_mn(MODE) ? 64 * i : 0);
+                const int n0 = ni * a.width + rank * half + (cols_mn(MODE) ? 64 * i : 0);
+                for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
+                    const uint32_t s = it % C::STAGES;
+                    if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
+                    if (warp == 0 && rank == 0) expect_tx(smem_u32(&c->full[s]), bytes);
+                    const uint32_t bar = map_rank(smem_u32(&c->full[s]), 0);
+                    const int ph = MODE == kDx && ks >= a.kphase;
+                    const int k = 64 * (ph ? ks - a.kphase : ks);
+                    const CUtensorMap *map = of_rows ? &maps.r[MODE == kDw ? g : ph] : &maps.c[MODE == kGate2 ? i : ph];
+                    const int o = of_rows ? m0 : n0;
+                    const bool mn = of_rows ? rows_mn(MODE) : cols_mn(MODE);
+                    tma_2d_pair(to + s * C::STAGE, map, mn ? o : k, mn ? k : o, bar);
                 }
             }
-        }
         // copies still in flight (after a wait that gave up) land before the pair ends
-        if (rank == 0)
+        if (warp == 0 && rank == 0)
             for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
                 mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
         __syncwarp();
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == kWarpMma && rank == 0) {
         // ---------------- MMA issue, for both CTAs ------------------------------------------
         const uint32_t r0 = smem_u32(ring);
         uint32_t it = 0, nt = 0;
         bool ok = true;
         for (int t = pair; t < total && ok && !stopped(c); t += pairs, ++nt) {
-            const int ni = t % per_group % a.ntiles;
-            const int np = (min(a.width, a.cols - ni * a.width) + 31) & ~31;
-            const uint32_t idesc = a.idesc | (uint32_t)(np >> 3) << 17;
+            const uint32_t idesc = a.idesc | (uint32_t)(a.width >> 3) << 17;
             const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
             if (use >= 1 && !(ok = wait_warp(&c->dempty[buf], (use - 1) & 1, c, a.err))) break;
             for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
@@ -272,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
         }
         commit_pair(&c->fin);   // every MMA is done before TMEM is freed
         wait_warp(&c->fin, 0, c, a.err);
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < kWarpMma) {
         // ---------------- epilogue ----------------------------------------------------------
         const int qd = warp & 3, part = (warp - 4) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
@@ -324,18 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     tc::fence_before_sync();
     __syncthreads();
     cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
-    if (warp == 1) {
+    if (warp == kWarpMma) {
         tc::fence_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
-template <Mode MODE>
-cudaError_t launch(Args a, const Maps &m, cudaStream_t st)
+// Column chunks: the count whose waves of SM pairs take least, by what a tile costs in cycles:
+// its reduction at the tensor pipe's rate or at the 50 bytes a cycle that reach an SM from L2,
+// whichever is more, and a fixed start and end.
+inline void plan(Args &a, int NB)
 {
-    // Column chunks: the count whose waves of SM pairs take least, by what a tile costs in
-    // cycles: its reduction at the tensor pipe's rate or what L2 feeds an SM, whichever is more,
-    // and a fixed start and end.
     const int pairs = num_sms() / 2;
     a.mtiles = (a.rows + 2 * kLanes - 1) / (2 * kLanes);
     double best = 0;
@@ -343,16 +322,21 @@ cudaError_t launch(Args a, const Maps &m, cudaStream_t st)
         const int w = ((a.cols + nt - 1) / nt + 31) & ~31;
         const long long tiles = (long long)a.groups * a.mtiles * ((a.cols + w - 1) / w);
         if (best > 0 && tiles > 8 * pairs) break;
-        const double stage = std::max(2.0 * w * Cfg<MODE>::NB, (16384.0 + 64.0 * w * Cfg<MODE>::NB) / 64);
-        const double cost = (double)((tiles + pairs - 1) / pairs) * (a.ksteps * stage + 3000.0 + 4.0 * w * Cfg<MODE>::NB);
+        const double stage = std::max(2.0 * w * NB, (16384.0 + 64.0 * w * NB) / 50);
+        const double cost = (double)((tiles + pairs - 1) / pairs) * (a.ksteps * stage + 3000.0 + 4.0 * w * NB);
         if (best == 0 || cost < best) {
             best = cost;
             a.width = w;
         }
     }
     a.ntiles = (a.cols + a.width - 1) / a.width;
+}
+
+template <Mode MODE>
+cudaError_t launch(const Args &a, const Maps &m, cudaStream_t st)
+{
     const long long tiles = (long long)a.groups * a.mtiles * a.ntiles;
-    const int grid = 2 * (int)std::min<long long>(tiles, pairs);
+    const int grid = 2 * (int)std::min<long long>(tiles, num_sms() / 2);
     return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(kThreads), Cfg<MODE>::SMEM, st, 2, a, m);
 }
 

@@ -18,7 +18,9 @@
 // A reduction step (stage) is 128 bytes of each operand row: 64 16-bit or 256 4-bit inputs, in
 // 128-byte-swizzled tiles fed by TMA.  Rows and inputs past a tensor's end are read as zero.
 //
-// Warps: 0 feeds the stages by TMA; 1 issues the MMAs; 4-7 are the epilogue (TMEM lanes
+// Warps: 0, 2 and 3 feed the stages by TMA, one box of a stage each (a box costs the warp that
+// issues it about 270 cycles beside its 1.8 a row, and boxes of different warps overlap): lanes
+// operands on 0 and 2, the columns on 3; 1 issues the MMAs; 4-7 are the epilogue (TMEM lanes
 // 32 * (warp - 4) ..); 8-11 (MXFP4 only) bring the scales, one operand of 128 rows each: global
 // rows of scale bytes -> shared memory blocks of 512 bytes (row r, block k of 4 at
 // 16 * (r % 32) + 4 * (r / 32) + k) that tcgen05.cp copies to TMEM.
@@ -45,7 +47,7 @@ namespace gemm {
 enum Mode { kMxGate, kMxMul, kGate };
 
 constexpr int kM = 128;          // lanes of a tile
-constexpr int kBoxMaps = 4;      // column-operand maps with boxes of 16 << k rows
+constexpr int kBoxMaps = 12;     // column-operand maps with boxes of 16 (k + 1) rows
 constexpr int kMaxGroups = 512;
 
 constexpr bool is_mx(Mode m) { return m == kMxGate || m == kMxMul; }
@@ -72,7 +74,7 @@ struct Args {
 
 struct Maps {
     CUtensorMap a[2];
-    CUtensorMap b[kBoxMaps];   // boxes of 16 << k rows
+    CUtensorMap b[kBoxMaps];   // boxes of 16 (k + 1) rows: one for each tile width
 };
 
 template <Mode MODE, int BN>
@@ -433,35 +435,30 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
     const uint32_t tmem = c->tmem;
     const int total = c->tiles;
 
-    if (warp == 0) {
-        // ---------------- operands by TMA ---------------------------------------------------
-        const uint32_t r0 = smem_u32(ring);
+    if (warp == 0 || warp == 3 || (C::NA == 2 && warp == 2)) {
+        // ---------------- operands by TMA: one box of every stage ---------------------------
+        const bool col = warp == 3;
+        const int o = warp >> 1;   // lanes operand
+        const uint32_t to = smem_u32(ring) + (col ? C::NA : o) * C::A_BYTES;
         uint32_t it = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
             const Tile q = get_tile<BN>(a, c, t);
             const uint32_t bytes = C::NA * C::A_BYTES + (uint32_t)q.np * 128u;
+            const CUtensorMap *map = col ? &maps.b[(q.np >> 4) - 1] : &maps.a[o];
+            const int y = col ? q.row0 : q.e * a.M + q.m0;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
                 const uint32_t bar = smem_u32(&c->full[s]);
-                const uint32_t as = r0 + s * (C::NA * C::A_BYTES + C::B_BYTES), bs = as + C::NA * C::A_BYTES;
-                expect_tx(bar, bytes);
-                const int x = ks * (C::MX ? 128 : 64);
-#pragma unroll
-                for (int o = 0; o < C::NA; ++o) tma_2d(as + o * C::A_BYTES, &maps.a[o], x, q.e * a.M + q.m0, bar);
-                int r = 0;
-#pragma unroll
-                for (int k = kBoxMaps - 1; k >= 0; --k)
-                    if (q.np - r >= (16 << k)) {
-                        tma_2d(bs + r * 128, &maps.b[k], x, q.row0 + r, bar);
-                        r += 16 << k;
-                    }
+                if (warp == 0) expect_tx(bar, bytes);
+                tma_2d(to + s * (C::NA * C::A_BYTES + C::B_BYTES), map, ks * (C::MX ? 128 : 64), y, bar);
             }
         }
         // copies still in flight (after a wait that gave up) land before the CTA ends
-        for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-            mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+        if (warp == 0)
+            for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA issue ---------------------------------------------------------

@@ -13,29 +13,35 @@ using namespace gemm;
 // e2m1 x e2m1 with ue8m0 scales, fp32 sums, both operands reduction-major, 128 lanes
 constexpr uint32_t kIdescMx = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(kM >> 4) << 24);
 
-cudaError_t code_maps(Maps &m, const uint8_t *a0, const uint8_t *a1, long long arows, const uint8_t *b, int rows, int K)
+cudaError_t code_maps(Maps &m, const uint8_t *a0, const uint8_t *a1, long long arows, const uint8_t *b, int rows, int K,
+                      int widest)
 {
     cudaError_t e = rows_map(&m.a[0], a0, 8, K / 2, K / 2, arows, kM);
     if (e == cudaSuccess && a1) e = rows_map(&m.a[1], a1, 8, K / 2, K / 2, arows, kM);
-    for (int k = 0; k < kBoxMaps && e == cudaSuccess; ++k) e = rows_map(&m.b[k], b, 8, K / 2, K / 2, rows, 16 << k);
+    for (int k = 0; 16 * (k + 1) <= widest && e == cudaSuccess; ++k)
+        e = rows_map(&m.b[k], b, 8, K / 2, K / 2, rows, 16 * (k + 1));
     return e;
 }
+
+// Few rows a group take tiles of 32 columns: more stages in flight, and a cluster a tile while
+// tiles are fewer than SMs.
+bool few_rows(int rows, int E) { return rows <= 24 * std::min(E, rows); }
+constexpr int kFew = 32, kMany = 192;
 
 template <Mode MODE>
 cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
 {
     const int sms = num_sms();
     const int mtiles = (a.M + kM - 1) / kM, used = std::min(a.E, a.rows);
-    if (a.rows <= 24 * used) {
-        // few rows a group: 32 columns, and a cluster a tile while tiles are fewer than SMs
-        const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + 31) / 32 + used);
-        a.split = choose_split<MODE, 32>((long long)mtiles * used, a.ksteps);
-        const long long clusters = std::min<long long>(tiles, sms / a.split);
-        return launch<MODE, 32>(a, m, (int)clusters * a.split, st);
+    const int widest = few_rows(a.rows, a.E) ? kFew : kMany;
+    // at most this many tiles: every group's last chunk may be short
+    const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + widest - 1) / widest + used);
+    if (widest == kFew) {
+        a.split = choose_split<MODE, kFew>((long long)mtiles * used, a.ksteps);
+        return launch<MODE, kFew>(a, m, (int)std::min<long long>(tiles, sms / a.split) * a.split, st);
     }
-    const long long tiles = (long long)mtiles * ((a.rows + 191) / 192 + used);
     a.split = 1;
-    return launch<MODE, 192>(a, m, (int)std::min<long long>(tiles, sms), st);
+    return launch<MODE, kMany>(a, m, (int)std::min<long long>(tiles, sms), st);
 }
 
 }  // namespace
@@ -45,7 +51,7 @@ cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, c
                                 cudaStream_t st)
 {
     Maps m;
-    const cudaError_t e = code_maps(m, w, nullptr, (long long)E * N, x, rows, K);
+    const cudaError_t e = code_maps(m, w, nullptr, (long long)E * N, x, rows, K, few_rows(rows, E) ? kFew : kMany);
     if (e != cudaSuccess) return e;
     Args a = {};
     a.offsets = offsets;
@@ -70,7 +76,7 @@ cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, 
                                  uint8_t *codes, uint8_t *scales, int32_t *err, cudaStream_t st)
 {
     Maps m;
-    const cudaError_t e = code_maps(m, wg, wu, (long long)E * F, x, rows, K);
+    const cudaError_t e = code_maps(m, wg, wu, (long long)E * F, x, rows, K, few_rows(rows, E) ? kFew : kMany);
     if (e != cudaSuccess) return e;
     Args a = {};
     a.offsets = offsets;
