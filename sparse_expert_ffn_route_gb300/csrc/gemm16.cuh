@@ -29,6 +29,7 @@ namespace gemm16 {
 using gemm::cluster_sync;
 using gemm::expect_tx;
 using gemm::map_rank;
+using gemm::uniform;
 
 enum Mode { kGate2, kDx, kDw };
 
@@ -82,7 +83,11 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr)
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-__device__ __forceinline__ bool stopped(const Ctrl *c) { return *(volatile const int *)&c->abort != 0; }
+// (a vote, so that loops on it are uniform across the warp for the compiler too)
+__device__ __forceinline__ bool stopped(const Ctrl *c)
+{
+    return __any_sync(0xffffffffu, *(volatile const int *)&c->abort != 0);
+}
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
 {
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     Ctrl *c = reinterpret_cast<Ctrl *>(ring + C::STAGES * C::STAGE);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     __syncthreads();
     cluster_sync();   // the pair's barriers and TMEM are ready
     tc::fence_after_sync();
-    const uint32_t tmem = c->tmem;
+    const uint32_t tmem = uniform(c->tmem);
     const int per_group = a.mtiles * a.ntiles, total = a.groups * per_group;
 
     if (warp < 4) {

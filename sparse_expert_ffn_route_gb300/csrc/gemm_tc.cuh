@@ -102,6 +102,12 @@ struct Cfg {
     static_assert(NBUF * NA * BN <= (MX ? SF_COL : 512), "TMEM budget");
 };
 
+// A value that all lanes hold alike, in a form that the compiler knows to be uniform: operands of
+// the MMA and TMA instructions live in uniform registers, and moving them there from ordinary
+// ones for each instruction held the issue of a stage's MMAs and copies at 50 to 70 cycles each.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
 struct Ctrl {
     uint64_t full[8], empty[8], dfull[2], dempty[2], rfull, rempty, fin;
     uint32_t tmem;
@@ -110,7 +116,11 @@ struct Ctrl {
     int32_t prefix[kMaxGroups + 1], off[kMaxGroups + 1];
 };
 
-__device__ __forceinline__ bool stopped(const Ctrl *c) { return *(volatile const int *)&c->abort != 0; }
+// (a vote, so that loops on it are uniform across the warp for the compiler too)
+__device__ __forceinline__ bool stopped(const Ctrl *c)
+{
+    return __any_sync(0xffffffffu, *(volatile const int *)&c->abort != 0);
+}
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
 {
@@ -244,6 +254,10 @@ __device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
     r.m0 = mi * kM;
     r.row0 = first + ni * w;
     r.n = max(0, min(w, rows - ni * w));
+    r.e = uniform(r.e);
+    r.m0 = uniform(r.m0);
+    r.row0 = uniform(r.row0);
+    r.n = uniform(r.n);
     r.np = max(16, (r.n + 15) & ~15);
     return r;
 }
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
     float *red = reinterpret_cast<float *>(sfring + C::STAGES * C::SF_BYTES);
     Ctrl *c = reinterpret_cast<Ctrl *>(reinterpret_cast<uint8_t *>(red) + C::RED_BYTES);
     static_assert(sizeof(Ctrl) <= C::CTRL_BYTES, "control block");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int mtiles = (a.M + kM - 1) / kM;
     const int S = C::SPLIT ? a.split : 1;
     const int rank = C::SPLIT ? (int)(blockIdx.x % S) : 0;
@@ -432,8 +446,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     if (C::SPLIT && S > 1) cluster_sync();   // every rank's barriers are ready
-    const uint32_t tmem = c->tmem;
-    const int total = c->tiles;
+    const uint32_t tmem = uniform(c->tmem);
+    const int total = uniform(c->tiles);
 
     if (warp == 0 || warp == 3 || (C::NA == 2 && warp == 2)) {
         // ---------------- operands by TMA: one box of every stage ---------------------------
