@@ -20,8 +20,8 @@
 //
 // Warps: 0, 2 and 3 feed the stages by TMA, one box of a stage each (a box costs the warp that
 // issues it about 270 cycles beside its 1.8 a row, and boxes of different warps overlap): lanes
-// operands on 0 and 2, the columns on 3; 1 issues the MMAs; 4-7 are the epilogue (TMEM lanes
-// 32 * (warp - 4) ..); 8-11 (MXFP4 only) bring the scales, one operand of 128 rows each: global
+// operands on 0 and 2, the columns on 3; 1 issues the MMAs; 4-11 are the epilogue (TMEM lanes
+// 32 * (warp % 4) .., two warps for each quarter); 12-15 (MXFP4 only) bring the scales, one operand of 128 rows each: global
 // rows of scale bytes -> shared memory blocks of 512 bytes (row r, block k of 4 at
 // 16 * (r % 32) + 4 * (r / 32) + k) that tcgen05.cp copies to TMEM.
 //
@@ -49,6 +49,7 @@ enum Mode { kMxGate, kMxMul, kGate };
 constexpr int kM = 128;          // lanes of a tile
 constexpr int kBoxMaps = 12;     // column-operand maps with boxes of 16 (k + 1) rows
 constexpr int kMaxGroups = 512;
+constexpr int kEpiWarps = 8;
 
 constexpr bool is_mx(Mode m) { return m == kMxGate || m == kMxMul; }
 constexpr bool is_gated(Mode m) { return m == kMxGate || m == kGate; }
@@ -81,7 +82,9 @@ template <Mode MODE, int BN>
 struct Cfg {
     static constexpr bool MX = is_mx(MODE), GATED = is_gated(MODE);
     static constexpr int NA = GATED ? 2 : 1;               // lanes operands (accumulators) of a tile
-    static constexpr int NBUF = NA * BN <= 192 ? 2 : 512 / (NA * BN) >= 2 && !MX ? 2 : 1;
+    // TMEM: two halves of accumulators.  A tile takes one half, so that its epilogue runs beside
+    // the next tile's MMAs; two accumulators of more than HALF / 2 columns take both.
+    static constexpr int HALF = 224;
     static constexpr int A_BYTES = kM * 128;
     static constexpr int B_BYTES = BN * 128;
     static constexpr int SFB_UNITS = MX ? (BN + 127) / 128 : 0;
@@ -95,11 +98,12 @@ struct Cfg {
     static constexpr int BUDGET = 232448 - 1024 - CTRL_BYTES - RED_BYTES;
     static constexpr int STAGES = BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
     static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + CTRL_BYTES;
-    static constexpr int THREADS = MX ? 384 : 256;
+    static constexpr int THREADS = MX ? 512 : 384;
     static constexpr int SF_COL = 448;                     // first TMEM column of the scales: 2 buffers
     static constexpr int SF_BUF = 32;                      // columns of one buffer
     static_assert(STAGES >= 3, "shared memory budget");
-    static_assert(NBUF * NA * BN <= (MX ? SF_COL : 512), "TMEM budget");
+    static_assert(2 * HALF <= SF_COL && NA * BN <= 2 * HALF, "TMEM budget");
+    static constexpr bool both_halves(int np) { return NA * np > HALF; }
 };
 
 // A value that all lanes hold alike, in a form that the compiler knows to be uniform: operands of
@@ -396,10 +400,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->dfull[i], 1);
-            mbar_init(&c->dempty[i], 4);
+            mbar_init(&c->dempty[i], kEpiWarps);
         }
-        mbar_init(&c->rfull, 4 * S);
-        mbar_init(&c->rempty, 4 * S);
+        mbar_init(&c->rfull, kEpiWarps * S);
+        mbar_init(&c->rempty, kEpiWarps * S);
         mbar_init(&c->fin, 1);
         c->abort = 0;
         fence_mbar_init();
@@ -477,14 +481,19 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
     } else if (warp == 1) {
         // ---------------- MMA issue ---------------------------------------------------------
         const uint32_t r0 = smem_u32(ring), sf0 = smem_u32(sfring);
-        uint32_t it = 0, nt = 0;
+        uint32_t it = 0, h = 0;
+        uint32_t gave = 0;   // bit i: the parity of half i's next wait; bit 2 + i: it has been used
         bool ok = true;
-        for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
+        for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
             const Tile q = get_tile<BN>(a, c, t);
             const uint32_t idesc = a.idesc | (uint32_t)(q.np >> 3) << 17;
-            const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
-            const uint32_t d0 = tmem + buf * (C::NA * BN);
-            if (use >= 1 && !(ok = wait_warp(&c->dempty[buf], (use - 1) & 1, c, a.err))) break;
+            const bool both = C::both_halves(q.np);
+            if (both) h = 0;
+            const uint32_t mine = both ? 3u : 1u << h;
+            if ((mine & 1u) && (gave & 4u) && !(ok = wait_warp(&c->dempty[0], gave & 1u, c, a.err))) break;
+            if ((mine & 2u) && (gave & 8u) && !(ok = wait_warp(&c->dempty[1], (gave >> 1) & 1u, c, a.err))) break;
+            gave = (gave ^ (mine & (gave >> 2))) | mine << 2;   // the first use waits for nothing
+            const uint32_t d0 = tmem + h * C::HALF, dstep = both ? BN : C::HALF / 2;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (!(ok = wait_warp(&c->full[s], (it / C::STAGES) & 1, c, a.err))) break;
@@ -515,30 +524,38 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                         const uint64_t ka = tc::sdesc_kmajor_sw128(as + o * C::A_BYTES) + k * 2, kb = bd + k * 2;
                         if constexpr (C::MX) {
                             const uint32_t id = idesc | (uint32_t)((k & 1) * 2) << 29 | (uint32_t)((k & 1) * 2) << 4;
-                            mma_mx4(d0 + o * BN, ka, kb, id, sfc + (k >> 1) * 16 + o * 4, sfc + (k >> 1) * 16 + 8, ks > ks0 || k > 0);
+                            mma_mx4(d0 + o * dstep, ka, kb, id, sfc + (k >> 1) * 16 + o * 4, sfc + (k >> 1) * 16 + 8, ks > ks0 || k > 0);
                         } else {
-                            mma_f16(d0 + o * BN, ka, kb, idesc, ks > ks0 || k > 0);
+                            mma_f16(d0 + o * dstep, ka, kb, idesc, ks > ks0 || k > 0);
                         }
                     }
                 }
                 tc::commit_elect(&c->empty[s]);
             }
-            tc::commit_elect(&c->dfull[buf]);
+            tc::commit_elect(&c->dfull[h]);
+            if (both) tc::commit_elect(&c->dfull[1]);
+            else h ^= 1;
         }
         tc::commit_elect(&c->fin);   // every MMA issued here is done before TMEM is freed
         wait_warp(&c->fin, 0, c, a.err);
-    } else if (warp >= 4 && warp < 8) {
-        // ---------------- epilogue ----------------------------------------------------------
-        const int qd = warp - 4;
+    } else if (warp >= 4 && warp < 4 + kEpiWarps) {
+        // ---------------- epilogue: every second 16 columns of 32 lanes ---------------------
+        const int qd = warp & 3, part = (warp - 4) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
-        uint32_t nt = 0;
+        uint32_t nt = 0, h = 0, parity = 0;   // parity: bit i of half i's next wait
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
             const Tile q = get_tile<BN>(a, c, t);
-            const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
             const int m = q.m0 + qd * 32 + lane;
-            if (!(ok = wait_warp(&c->dfull[buf], use & 1, c, a.err))) break;
+            const bool both = C::both_halves(q.np);
+            if (both) h = 0;
+            const uint32_t mine = both ? 3u : 1u << h;   // the tile's halves
+            if ((mine & 1u) && !(ok = wait_warp(&c->dfull[0], parity & 1u, c, a.err))) break;
+            if ((mine & 2u) && !(ok = wait_warp(&c->dfull[1], (parity >> 1) & 1u, c, a.err))) break;
+            parity ^= mine;
             tc::fence_after_sync();
+            const uint32_t d0 = tl + h * C::HALF, dstep = both ? BN : C::HALF / 2;
+            if (!both) h ^= 1;
             if (C::SPLIT && S > 1) {
                 // send the partial sums to their columns' owners (column k to rank k % S), then
                 // add up the own columns in rank order
@@ -546,9 +563,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 const uint32_t rb = smem_u32(red);
 #pragma unroll
                 for (int o = 0; o < C::NA; ++o)
-                    for (int c0 = 0; c0 < q.np; c0 += 16) {
+                    for (int c0 = part * 16; c0 < q.np; c0 += 32) {
                         uint32_t v[16];
-                        tc::ld16(tl + buf * (C::NA * BN) + o * BN + c0, v);
+                        tc::ld16(d0 + o * dstep + c0, v);
                         tc::wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -561,11 +578,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 tc::fence_before_sync();
                 fence_cluster();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c->dempty[buf]);
+                if (lane == 0) mbar_arrive(&c->dempty[mine >> 1]);   // tiles of this form take one half
                 if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rfull), lane));
                 if (!(ok = wait_warp_cluster(&c->rfull, nt & 1, c, a.err))) break;
                 const int per = (BN + S - 1) / S;
-                for (int i0 = 0; i0 * S + rank < q.n; i0 += 8) {
+                for (int i0 = part * 8; i0 * S + rank < q.n; i0 += 16) {
                     float v[2][8];
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o)
@@ -585,16 +602,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 __syncwarp();
                 if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rempty), lane));
             } else {
-                for (int c0 = 0; c0 < q.np; c0 += 16) {
+                for (int c0 = part * 16; c0 < q.np; c0 += 32) {
                     uint32_t v[2][16];
 #pragma unroll
-                    for (int o = 0; o < C::NA; ++o) tc::ld16(tl + buf * (C::NA * BN) + o * BN + c0, v[o]);
+                    for (int o = 0; o < C::NA; ++o) tc::ld16(d0 + o * dstep + c0, v[o]);
                     tc::wait_ld();
-                    if (c0 + 16 >= q.np) {   // the accumulator is in registers
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&c->dempty[buf]);
-                    }
                     float f[2][16];
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o)
@@ -603,43 +615,61 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                     emit<MODE, 16>(a, f[0], f[C::NA - 1], m, lane,
                                    [&](int j) { return c0 + j < q.n ? q.row0 + c0 + j : -1; });
                 }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0 && (mine & 1u)) mbar_arrive(&c->dempty[0]);
+                if (lane == 0 && (mine & 2u)) mbar_arrive(&c->dempty[1]);
             }
         }
-    } else if (C::MX && warp >= 8 && warp - 8 < C::SF_UNITS) {
+    } else if (C::MX && warp >= 12 && warp - 12 < C::SF_UNITS) {
         // ---------------- scales: this warp's operand, 128 rows -----------------------------
-        const int u = warp - 8;
-        uint32_t it = 0;
-        bool ok = true;
-        for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
-            const Tile q = get_tile<BN>(a, c, t);
-            const uint8_t *base = u < C::NA ? a.sfa[u] : a.sfb;
-            const long long row0 = u < C::NA ? (long long)q.e * a.M + q.m0 : (long long)q.row0 + (u - C::NA) * 128;
-            const long long rows = u < C::NA ? a.sfa_rows : a.rows;
-            // chunks of 512 inputs (16 scale bytes of a row), one chunk ahead in registers
-            uint4 cur[4], nxt[4];
-            int kc = ks0 >> 1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) nxt[i] = load_scales(base, row0 + lane + 32 * i, rows, a.sf_ld, kc);
-            for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                if (ks == ks0 || (ks & 1) == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-                    ++kc;
-                    if (2 * kc < ks1) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) nxt[i] = load_scales(base, row0 + lane + 32 * i, rows, a.sf_ld, kc);
-                    }
+        // Chunks of 512 inputs (16 scale bytes of a row, two stages), the next one in registers
+        // while one is stored, over the tiles' ends too.  (Two or four chunks ahead were slower:
+        // a decode batch 494 and 519 us, one ahead 485.)
+        const int u = warp - 12;
+        const uint8_t *base = u < C::NA ? a.sfa[u] : a.sfb;
+        const long long rows = u < C::NA ? a.sfa_rows : a.rows;
+        const int kc0 = ks0 >> 1, kc1 = (ks1 + 1) >> 1;
+        const int chunks = tile0 < total ? (total - tile0 + tstep - 1) / tstep * (kc1 - kc0) : 0;
+        int lt = tile0 - tstep, lk = kc1;   // the next load: tile, chunk
+        long long lrow = 0;
+        uint4 v[4];
+        auto load = [&] {
+            if (lk == kc1) {
+                lt += tstep;
+                lk = kc0;
+                if (lt < total) {
+                    const Tile q = get_tile<BN>(a, c, lt);
+                    lrow = u < C::NA ? (long long)q.e * a.M + q.m0 : (long long)q.row0 + (u - C::NA) * 128;
                 }
+            }
+            if (lt < total) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = load_scales(base, lrow + lane + 32 * i, rows, a.sf_ld, lk);
+                ++lk;
+            }
+        };
+        load();
+        uint32_t it = 0;
+        int kc = kc0;
+        bool ok = true;
+        for (int i = 0; i < chunks && ok; ++i) {
+            uint4 now[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) now[j] = v[j];
+            load();
+            for (int ks = max(ks0, 2 * kc); ks < min(ks1, 2 * kc + 2); ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
                 uint4 *dst = reinterpret_cast<uint4 *>(sfring + s * C::SF_BYTES + u * 1024) + lane;
                 const bool odd = ks & 1;
-                dst[0] = make_uint4(odd ? cur[0].z : cur[0].x, odd ? cur[1].z : cur[1].x, odd ? cur[2].z : cur[2].x, odd ? cur[3].z : cur[3].x);
-                dst[32] = make_uint4(odd ? cur[0].w : cur[0].y, odd ? cur[1].w : cur[1].y, odd ? cur[2].w : cur[2].y, odd ? cur[3].w : cur[3].y);
+                dst[0] = make_uint4(odd ? now[0].z : now[0].x, odd ? now[1].z : now[1].x, odd ? now[2].z : now[2].x, odd ? now[3].z : now[3].x);
+                dst[32] = make_uint4(odd ? now[0].w : now[0].y, odd ? now[1].w : now[1].y, odd ? now[2].w : now[2].y, odd ? now[3].w : now[3].y);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->full[s]);
             }
+            if (++kc == kc1) kc = kc0;
         }
     }
 
