@@ -20,10 +20,16 @@
 //
 // Warps: 0, 2 and 3 feed the stages by TMA, one box of a stage each (a box costs the warp that
 // issues it about 270 cycles beside its 1.8 a row, and boxes of different warps overlap): lanes
-// operands on 0 and 2, the columns on 3; 1 issues the MMAs; 4-11 are the epilogue (TMEM lanes
-// 32 * (warp % 4) .., two warps for each quarter); 12-15 (MXFP4 only) bring the scales, one operand of 128 rows each: global
+// operands on 0 and 2, the columns on 3; 1 issues the MMAs; 4-11 (4-7 for few columns) are the
+// epilogue (TMEM lanes 32 * (warp % 4) ..); those after it (MXFP4 only) bring the scales, one operand of 128 rows each: global
 // rows of scale bytes -> shared memory blocks of 512 bytes (row r, block k of 4 at
 // 16 * (r % 32) + 4 * (r / 32) + k) that tcgen05.cp copies to TMEM.
+//
+// For few columns (BN 32) two CTAs fit an SM, so that a kernel of a chain starts beside the end
+// of the one before it.  With `early` set the lanes operands (weights) and their scales are
+// loaded before the wait for that kernel: the caller says that they and the offsets were
+// complete before it began.  No bounded wait then starts before that kernel's end: the waits of
+// this file measure this kernel's own progress.
 //
 // Every wait is bounded: one that gives up sets the workspace's error word and ends the CTA's
 // loops; its copies in flight and MMAs are waited for and TMEM is freed.
@@ -49,7 +55,7 @@ enum Mode { kMxGate, kMxMul, kGate };
 constexpr int kM = 128;          // lanes of a tile
 constexpr int kBoxMaps = 12;     // column-operand maps with boxes of 16 (k + 1) rows
 constexpr int kMaxGroups = 512;
-constexpr int kEpiWarps = 8;
+constexpr int kSplitCols = 16;   // columns of a tile that CTAs share
 
 constexpr bool is_mx(Mode m) { return m == kMxGate || m == kMxMul; }
 constexpr bool is_gated(Mode m) { return m == kMxGate || m == kGate; }
@@ -62,6 +68,8 @@ struct Args {
     int M;                     // lanes dimension of one group
     int ksteps;                // stages of the whole reduction
     int split;                 // CTAs that share a tile (the cluster size)
+    int width;                 // columns of a tile at most (BN; kSplitCols in a cluster)
+    int early;                 // weights, their scales and offsets are older than the last kernel
     // scale bytes [rows][sf_ld] of the lanes operands (groups * M rows) and the columns operand
     const uint8_t *sfa[2], *sfb;
     int sf_ld;                 // K / 32
@@ -82,27 +90,31 @@ template <Mode MODE, int BN>
 struct Cfg {
     static constexpr bool MX = is_mx(MODE), GATED = is_gated(MODE);
     static constexpr int NA = GATED ? 2 : 1;               // lanes operands (accumulators) of a tile
+    static constexpr bool FEW = BN <= 32;                  // two CTAs an SM; clusters may share a tile
+    static constexpr int EPI = FEW ? 4 : 8;                // epilogue warps
     // TMEM: two halves of accumulators.  A tile takes one half, so that its epilogue runs beside
     // the next tile's MMAs; two accumulators of more than HALF / 2 columns take both.
-    static constexpr int HALF = 224;
+    static constexpr int HALF = FEW ? NA * BN : 224;
     static constexpr int A_BYTES = kM * 128;
     static constexpr int B_BYTES = BN * 128;
     static constexpr int SFB_UNITS = MX ? (BN + 127) / 128 : 0;
     static constexpr int SF_UNITS = MX ? NA + SFB_UNITS : 0;   // 128-row scale blocks of a stage (2 x 512 B each)
     static constexpr int SF_BYTES = SF_UNITS * 1024;
-    static constexpr bool SPLIT = BN <= 32;
-    static constexpr int RED_COLS = 40;                    // >= S * ceil(32 / S) for S <= 8
-    static constexpr int RED_BYTES = SPLIT ? NA * RED_COLS * kM * 4 : 0;
-    static constexpr int CTRL_BYTES = 8192;                // control block and the groups' prefix
+    static constexpr int RED_COLS = 24;                    // >= S * ceil(16 / S) for S <= 8
+    static constexpr int RED_BYTES = FEW ? NA * RED_COLS * kM * 4 : 0;
+    static constexpr int CTRL_BYTES = 5120;                // control block and the groups' prefix
     static constexpr int STAGE = NA * A_BYTES + B_BYTES + SF_BYTES;
-    static constexpr int BUDGET = 232448 - 1024 - CTRL_BYTES - RED_BYTES;
+    static constexpr int BUDGET = (FEW ? 115712 : 232448) - 1024 - CTRL_BYTES - RED_BYTES;
     static constexpr int STAGES = BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
     static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + CTRL_BYTES;
-    static constexpr int THREADS = MX ? 512 : 384;
-    static constexpr int SF_COL = 448;                     // first TMEM column of the scales: 2 buffers
+    static constexpr int SF_WARP = 4 + EPI;
+    static constexpr int THREADS = 32 * (SF_WARP + SF_UNITS);
+    static constexpr int PER_SM = FEW ? 2 : 1;
+    static constexpr int SF_COL = 2 * HALF;                // first TMEM column of the scales: 2 buffers
     static constexpr int SF_BUF = 32;                      // columns of one buffer
-    static_assert(STAGES >= 3, "shared memory budget");
-    static_assert(2 * HALF <= SF_COL && NA * BN <= 2 * HALF, "TMEM budget");
+    static constexpr int TMEM_COLS = FEW ? 256 : 512;
+    static_assert(STAGES >= 2, "shared memory budget");
+    static_assert(SF_COL + (MX ? 2 * SF_BUF : 0) <= TMEM_COLS && NA * BN <= 2 * HALF, "TMEM budget");
     static constexpr bool both_halves(int np) { return NA * np > HALF; }
 };
 
@@ -117,6 +129,7 @@ struct Ctrl {
     uint32_t tmem;
     int abort;
     int tiles;
+    int warp_tiles[16];
     int32_t prefix[kMaxGroups + 1], off[kMaxGroups + 1];
 };
 
@@ -238,7 +251,6 @@ struct Tile {
 // columns of a group of c rows in nt chunks of equal size (a multiple of 16)
 __device__ __forceinline__ int chunk_cols(int c, int nt) { return ((c + nt - 1) / nt + 15) & ~15; }
 
-template <int BN>
 __device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
 {
     int lo = 0, hi = a.E;
@@ -249,7 +261,7 @@ __device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
     }
     const int first = a.offsets ? c->off[lo] : 0;
     const int rows = a.offsets ? c->off[lo + 1] - first : a.rows;
-    const int nt = (rows + BN - 1) / BN;
+    const int nt = (rows + a.width - 1) / a.width;
     const int w = chunk_cols(rows, nt);
     const int local = t - c->prefix[lo];
     const int mi = local / nt, ni = local - mi * nt;   // a weight tile's chunks run next to one another
@@ -371,12 +383,12 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t *base, long long row,
 }
 
 template <Mode MODE, int BN>
-__global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
     using C = Cfg<MODE, BN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    pdl_wait();
+    if (!a.early) pdl_wait();
     pdl_launch_dependents();
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sfring = ring + C::STAGES * (C::NA * C::A_BYTES + C::B_BYTES);
@@ -385,14 +397,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
     static_assert(sizeof(Ctrl) <= C::CTRL_BYTES, "control block");
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int mtiles = (a.M + kM - 1) / kM;
-    const int S = C::SPLIT ? a.split : 1;
-    const int rank = C::SPLIT ? (int)(blockIdx.x % S) : 0;
-    const int tile0 = C::SPLIT ? (int)(blockIdx.x / S) : (int)blockIdx.x;
-    const int tstep = C::SPLIT ? (int)(gridDim.x / S) : (int)gridDim.x;
+    const int S = C::FEW ? a.split : 1;
+    const int rank = C::FEW ? (int)(blockIdx.x % S) : 0;
+    const int tile0 = C::FEW ? (int)(blockIdx.x / S) : (int)blockIdx.x;
+    const int tstep = C::FEW ? (int)(gridDim.x / S) : (int)gridDim.x;
     const int ks0 = (int)((long long)a.ksteps * rank / S), ks1 = (int)((long long)a.ksteps * (rank + 1) / S);
 
-    if (a.offsets)
-        for (int e = tid; e <= a.E; e += C::THREADS) c->off[e] = a.offsets[e];
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&c->full[i], 1 + C::SF_UNITS);
@@ -400,73 +410,82 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->dfull[i], 1);
-            mbar_init(&c->dempty[i], kEpiWarps);
+            mbar_init(&c->dempty[i], C::EPI);
         }
-        mbar_init(&c->rfull, kEpiWarps * S);
-        mbar_init(&c->rempty, kEpiWarps * S);
+        mbar_init(&c->rfull, C::EPI * S);
+        mbar_init(&c->rempty, C::EPI * S);
         mbar_init(&c->fin, 1);
         c->abort = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        tc::tmem_alloc(&c->tmem, 512);
+        tc::tmem_alloc(&c->tmem, C::TMEM_COLS);
         tc::tmem_relinquish();
     }
-    __syncthreads();
-    if (warp == 0) {
-        // tiles before each group; a group whose offsets do not lie in order within the rows is
-        // recorded and left out
-        int carry = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            int n = 0;
-            if (e < a.E) {
-                int rows = a.rows;
-                if (a.offsets) {
-                    const int lo = c->off[e], hi = c->off[e + 1];
-                    rows = hi - lo;
-                    if (lo < 0 || hi > a.rows || hi < lo) {
-                        atomicOr(a.err, kErrBadOffsets);
-                        rows = 0;
-                    }
+    // tiles before each group: thread e (in rounds of the block) has group e, a scan within each
+    // warp, then the warps' sums.  A group whose offsets do not lie in order within the rows is
+    // recorded and left out.
+    for (int e0 = 0, carry = 0; e0 < a.E; e0 += C::THREADS) {
+        const int e = e0 + tid;
+        int n = 0;
+        if (e < a.E) {
+            int rows = a.rows;
+            if (a.offsets) {
+                const int lo = a.offsets[e], hi = a.offsets[e + 1];
+                rows = hi - lo;
+                c->off[e] = lo;
+                if (e == a.E - 1) c->off[a.E] = hi;
+                if (lo < 0 || hi > a.rows || hi < lo) {
+                    atomicOr(a.err, kErrBadOffsets);
+                    rows = 0;
                 }
-                n = mtiles * ((rows + BN - 1) / BN);
             }
-            int s = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, s, d);
-                if (lane >= d) s += o;
-            }
-            if (e < a.E) c->prefix[e] = carry + s - n;
-            carry += __shfl_sync(0xffffffffu, s, 31);
+            n = mtiles * ((rows + a.width - 1) / a.width);
         }
-        if (lane == 0) {
-            c->prefix[a.E] = carry;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (lane == 31) c->warp_tiles[warp] = sum;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < C::THREADS / 32; ++w) {
+            const int v = c->warp_tiles[w];
+            if (w < warp) before += v;
+            carry += v;
+        }
+        if (e < a.E) c->prefix[e] = before + sum - n;
+        if (tid == 0) {
+            c->prefix[a.E] = carry;   // the last round's stays
             c->tiles = carry;
         }
+        __syncthreads();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (C::SPLIT && S > 1) cluster_sync();   // every rank's barriers are ready
+    if (C::FEW && S > 1) cluster_sync();   // every rank's barriers are ready
     const uint32_t tmem = uniform(c->tmem);
     const int total = uniform(c->tiles);
 
     if (warp == 0 || warp == 3 || (C::NA == 2 && warp == 2)) {
         // ---------------- operands by TMA: one box of every stage ---------------------------
         const bool col = warp == 3;
+        if (col && a.early) pdl_wait();
         const int o = warp >> 1;   // lanes operand
         const uint32_t to = smem_u32(ring) + (col ? C::NA : o) * C::A_BYTES;
         uint32_t it = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
-            const Tile q = get_tile<BN>(a, c, t);
+            const Tile q = get_tile(a, c, t);
             const uint32_t bytes = C::NA * C::A_BYTES + (uint32_t)q.np * 128u;
             const CUtensorMap *map = col ? &maps.b[(q.np >> 4) - 1] : &maps.a[o];
             const int y = col ? q.row0 : q.e * a.M + q.m0;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
+                if (a.early && it == C::STAGES) pdl_wait();
                 if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
                 const uint32_t bar = smem_u32(&c->full[s]);
                 if (warp == 0) expect_tx(bar, bytes);
@@ -474,18 +493,20 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
             }
         }
         // copies still in flight (after a wait that gave up) land before the CTA ends
+        if (a.early) pdl_wait();
         if (warp == 0)
             for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
                 mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA issue ---------------------------------------------------------
+        if (a.early) pdl_wait();
         const uint32_t r0 = smem_u32(ring), sf0 = smem_u32(sfring);
         uint32_t it = 0, h = 0;
         uint32_t gave = 0;   // bit i: the parity of half i's next wait; bit 2 + i: it has been used
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
-            const Tile q = get_tile<BN>(a, c, t);
+            const Tile q = get_tile(a, c, t);
             const uint32_t idesc = a.idesc | (uint32_t)(q.np >> 3) << 17;
             const bool both = C::both_halves(q.np);
             if (both) h = 0;
@@ -538,14 +559,15 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
         }
         tc::commit_elect(&c->fin);   // every MMA issued here is done before TMEM is freed
         wait_warp(&c->fin, 0, c, a.err);
-    } else if (warp >= 4 && warp < 4 + kEpiWarps) {
-        // ---------------- epilogue: every second 16 columns of 32 lanes ---------------------
+    } else if (warp >= 4 && warp < 4 + C::EPI) {
+        // ---------------- epilogue: 32 lanes, 16 columns at a time; two warps take turns ----
+        if (a.early) pdl_wait();
         const int qd = warp & 3, part = (warp - 4) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
         uint32_t nt = 0, h = 0, parity = 0;   // parity: bit i of half i's next wait
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
-            const Tile q = get_tile<BN>(a, c, t);
+            const Tile q = get_tile(a, c, t);
             const int m = q.m0 + qd * 32 + lane;
             const bool both = C::both_halves(q.np);
             if (both) h = 0;
@@ -556,14 +578,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
             tc::fence_after_sync();
             const uint32_t d0 = tl + h * C::HALF, dstep = both ? BN : C::HALF / 2;
             if (!both) h ^= 1;
-            if (C::SPLIT && S > 1) {
+            if (C::FEW && S > 1) {
                 // send the partial sums to their columns' owners (column k to rank k % S), then
                 // add up the own columns in rank order
                 if (nt >= 1 && !(ok = wait_warp_cluster(&c->rempty, (nt - 1) & 1, c, a.err))) break;
                 const uint32_t rb = smem_u32(red);
 #pragma unroll
                 for (int o = 0; o < C::NA; ++o)
-                    for (int c0 = part * 16; c0 < q.np; c0 += 32) {
+                    for (int c0 = part * 16; c0 < q.np; c0 += 4 * C::EPI) {
                         uint32_t v[16];
                         tc::ld16(d0 + o * dstep + c0, v);
                         tc::wait_ld();
@@ -571,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                         for (int j = 0; j < 16; ++j) {
                             const int k = c0 + j;
                             if (k < q.n)
-                                st_cluster(map_rank(rb + (uint32_t)(((o * C::RED_COLS + rank * ((BN + S - 1) / S) + k / S) * kM + qd * 32 + lane) * 4), k % S),
+                                st_cluster(map_rank(rb + (uint32_t)(((o * C::RED_COLS + rank * ((kSplitCols + S - 1) / S) + k / S) * kM + qd * 32 + lane) * 4), k % S),
                                            __uint_as_float(v[j]));
                         }
                     }
@@ -581,8 +603,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 if (lane == 0) mbar_arrive(&c->dempty[mine >> 1]);   // tiles of this form take one half
                 if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rfull), lane));
                 if (!(ok = wait_warp_cluster(&c->rfull, nt & 1, c, a.err))) break;
-                const int per = (BN + S - 1) / S;
-                for (int i0 = part * 8; i0 * S + rank < q.n; i0 += 16) {
+                const int per = (kSplitCols + S - 1) / S;
+                for (int i0 = part * 8; i0 * S + rank < q.n; i0 += 2 * C::EPI) {
                     float v[2][8];
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o)
@@ -602,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 __syncwarp();
                 if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rempty), lane));
             } else {
-                for (int c0 = part * 16; c0 < q.np; c0 += 32) {
+                for (int c0 = part * 16; c0 < q.np; c0 += 4 * C::EPI) {
                     uint32_t v[2][16];
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o) tc::ld16(d0 + o * dstep + c0, v[o]);
@@ -621,12 +643,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 if (lane == 0 && (mine & 2u)) mbar_arrive(&c->dempty[1]);
             }
         }
-    } else if (C::MX && warp >= 12 && warp - 12 < C::SF_UNITS) {
+    } else if (C::MX && warp >= C::SF_WARP) {
         // ---------------- scales: this warp's operand, 128 rows -----------------------------
-        // Chunks of 512 inputs (16 scale bytes of a row, two stages), the next one in registers
-        // while one is stored, over the tiles' ends too.  (Two or four chunks ahead were slower:
-        // a decode batch 494 and 519 us, one ahead 485.)
-        const int u = warp - 12;
+        // Chunks of 512 inputs (16 scale bytes of a row, two stages), one ahead in registers, over
+        // the tiles' ends too.  The next chunk is loaded before this one is stored where the MMAs
+        // set the pace (prompt 1255 us, after: 1276), after it where the weights' stream does (decode
+        // batch 486 us, before: 502); two or four chunks ahead were slower in both.
+        const int u = warp - C::SF_WARP;
+        if (u >= C::NA && a.early) pdl_wait();
         const uint8_t *base = u < C::NA ? a.sfa[u] : a.sfb;
         const long long rows = u < C::NA ? a.sfa_rows : a.rows;
         const int kc0 = ks0 >> 1, kc1 = (ks1 + 1) >> 1;
@@ -639,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 lt += tstep;
                 lk = kc0;
                 if (lt < total) {
-                    const Tile q = get_tile<BN>(a, c, lt);
+                    const Tile q = get_tile(a, c, lt);
                     lrow = u < C::NA ? (long long)q.e * a.M + q.m0 : (long long)q.row0 + (u - C::NA) * 128;
                 }
             }
@@ -657,9 +681,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
             uint4 now[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) now[j] = v[j];
-            load();
+            if (!C::FEW) load();
             for (int ks = max(ks0, 2 * kc); ks < min(ks1, 2 * kc + 2); ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
+                if (a.early && it == C::STAGES) pdl_wait();
                 if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
                 uint4 *dst = reinterpret_cast<uint4 *>(sfring + s * C::SF_BYTES + u * 1024) + lane;
                 const bool odd = ks & 1;
@@ -669,22 +694,24 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->full[s]);
             }
+            if (C::FEW) load();
             if (++kc == kc1) kc = kc0;
         }
     }
 
+    if (a.early) pdl_wait();   // a CTA without tiles too: this grid ends after the one before it
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 512);
+        tc::tmem_dealloc(tmem, C::TMEM_COLS);
     }
-    if (C::SPLIT && S > 1) cluster_sync();   // no rank leaves while another may still write to it
+    if (C::FEW && S > 1) cluster_sync();   // no rank leaves while another may still write to it
 }
 
 // Clusters of `size` CTAs of this kernel that the current device holds at once (0 if unknown); a
 // cluster lies within one of the device's processor groups, so this is less than SMs / size
-// (measured on GB300: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
+// (measured on GB300 with one CTA an SM: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
 template <Mode MODE, int BN>
 int max_clusters(int size)
 {
@@ -721,7 +748,7 @@ template <Mode MODE, int BN>
 int choose_split(long long tiles, int ksteps)
 {
     int best = 1;
-    if (Cfg<MODE, BN>::SPLIT)
+    if (Cfg<MODE, BN>::FEW)
         for (int s = 2; s <= 8 && s <= ksteps && s * tiles <= num_sms(); ++s)
             if (max_clusters<MODE, BN>(s) >= tiles) best = s;
     return best;

@@ -215,13 +215,15 @@ cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales,
                                     int dtype, cudaStream_t st);
 
 // MXFP4 products (mxfp4_gemm.cu): y [rows][N] = x W^T over `E` groups of rows, and
-// codes/scales [rows][F] = q(silu(x Wg^T) * (x Wu^T))
+// codes/scales [rows][F] = q(silu(x Wg^T) * (x Wu^T)).  early: the weights, their scales and the
+// offsets were complete before the last kernel on the stream began (they are read before it ends)
 cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *w, const uint8_t *ws,
-                                int E, const int32_t *offsets, int N, int K, void *y, int dtype, int32_t *err,
+                                int E, const int32_t *offsets, int N, int K, void *y, int dtype, int early, int32_t *err,
                                 cudaStream_t st);
 cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *wg, const uint8_t *sg,
                                  const uint8_t *wu, const uint8_t *su, int E, const int32_t *offsets, int F, int K,
-                                 uint8_t *codes, uint8_t *scales, int32_t *err, cudaStream_t st);
+                                 uint8_t *codes, uint8_t *scales, int early, int32_t *err,
+                                 cudaStream_t st);
 
 // diagnostic: one bounded wait on an mbarrier nothing arrives at (selftest.cu)
 cudaError_t launch_selftest_wait(int32_t *err, int polls, cudaStream_t st);

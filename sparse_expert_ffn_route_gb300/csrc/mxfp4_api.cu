@@ -123,7 +123,7 @@ int moe_mxfp4_matmul(const uint8_t *x, const uint8_t *x_scales, int rows, const 
     if (groups > 1 && !offsets) return set_error(MOE_ERR_ARG, "offsets is NULL with %d groups", groups);
     if (off(offsets, 4)) return set_error(MOE_ERR_ALIGN, "offsets is not 4-byte aligned");
     if ((rc = check_workspace(workspace, workspace_bytes, 256)) || (rc = require_device())) return rc;
-    return done(launch_mxfp4_matmul(x, x_scales, rows, w, w_scales, groups, offsets, N, K, y, dtype,
+    return done(launch_mxfp4_matmul(x, x_scales, rows, w, w_scales, groups, offsets, N, K, y, dtype, 0,
                                     static_cast<int32_t *>(workspace), (cudaStream_t)stream),
                 "MXFP4 product launch");
 }
@@ -161,13 +161,15 @@ int moe_mxfp4_expert_ffn(const moe_config *cfg, const void *x, int x_dtype, int 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     int32_t *err = static_cast<int32_t *>(workspace);
     const int E = cfg->n_experts, H = cfg->hidden, F = cfg->d_ff, P = T * cfg->top_k;
+    // The quantiser waits for what the stream held before the call before it lets the next kernel
+    // start, so that the two products may read weights and lists early.
     cudaError_t e = launch_quantize_mxfp4(x, x_dtype, H, P, H, tok, offsets ? offsets + E : nullptr, T, ws + L.x,
                                           ws + L.xs, err, st);
     if (e == cudaSuccess)
         e = launch_mxfp4_gate_up(ws + L.x, ws + L.xs, P, w->w_gate, w->s_gate, w->w_up, w->s_up, E, offsets, F, H,
-                                 ws + L.h, ws + L.hs, err, st);
+                                 ws + L.h, ws + L.hs, 1, err, st);
     if (e == cudaSuccess)
-        e = launch_mxfp4_matmul(ws + L.h, ws + L.hs, P, w->w_down, w->s_down, E, offsets, H, F, y_pairs, y_dtype, err, st);
+        e = launch_mxfp4_matmul(ws + L.h, ws + L.hs, P, w->w_down, w->s_down, E, offsets, H, F, y_pairs, y_dtype, 1, err, st);
     return done(e, "MXFP4 expert FFN launch");
 }
 

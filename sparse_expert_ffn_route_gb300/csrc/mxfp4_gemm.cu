@@ -34,20 +34,19 @@ cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
     const int sms = num_sms();
     const int mtiles = (a.M + kM - 1) / kM, used = std::min(a.E, a.rows);
     const int widest = few_rows(a.rows, a.E) ? kFew : kMany;
+    a.split = widest == kFew ? choose_split<MODE, kFew>((long long)mtiles * used, a.ksteps) : 1;
+    a.width = a.split > 1 ? kSplitCols : widest;
     // at most this many tiles: every group's last chunk may be short
-    const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + widest - 1) / widest + used);
-    if (widest == kFew) {
-        a.split = choose_split<MODE, kFew>((long long)mtiles * used, a.ksteps);
-        return launch<MODE, kFew>(a, m, (int)std::min<long long>(tiles, sms / a.split) * a.split, st);
-    }
-    a.split = 1;
+    const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + a.width - 1) / a.width + used);
+    if (widest == kFew)
+        return launch<MODE, kFew>(a, m, (int)std::min<long long>(tiles, 2 * sms / a.split) * a.split, st);
     return launch<MODE, kMany>(a, m, (int)std::min<long long>(tiles, sms), st);
 }
 
 }  // namespace
 
 cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *w, const uint8_t *ws,
-                                int E, const int32_t *offsets, int N, int K, void *y, int dtype, int32_t *err,
+                                int E, const int32_t *offsets, int N, int K, void *y, int dtype, int early, int32_t *err,
                                 cudaStream_t st)
 {
     Maps m;
@@ -67,13 +66,15 @@ cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, c
     a.ld = N;
     a.dtype = dtype;
     a.idesc = kIdescMx;
+    a.early = early;
     a.err = err;
     return run<kMxMul>(a, m, st);
 }
 
 cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *wg, const uint8_t *sg,
                                  const uint8_t *wu, const uint8_t *su, int E, const int32_t *offsets, int F, int K,
-                                 uint8_t *codes, uint8_t *scales, int32_t *err, cudaStream_t st)
+                                 uint8_t *codes, uint8_t *scales, int early, int32_t *err,
+                                 cudaStream_t st)
 {
     Maps m;
     const cudaError_t e = code_maps(m, wg, wu, (long long)E * F, x, rows, K, few_rows(rows, E) ? kFew : kMany);
@@ -93,6 +94,7 @@ cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, 
     a.out[1] = scales;
     a.ld = F;
     a.idesc = kIdescMx;
+    a.early = early;
     a.err = err;
     return run<kMxGate>(a, m, st);
 }
