@@ -279,6 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
 #pragma unroll
                 for (int o = 0; o < C::NB; ++o) tc::ld32(tl + buf * kMaxCols + o * kMaxCols + c0, v[o]);
                 tc::wait_ld();
+#pragma unroll
+                for (int o = 0; o < C::NB; ++o)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[o][j]));   // read after the wait
                 if (row < a.rows) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {

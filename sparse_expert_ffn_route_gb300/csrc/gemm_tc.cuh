@@ -222,6 +222,26 @@ __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc)
         : "memory");
 }
 
+// one 32-bit column of this thread's TMEM lane from each of N accumulators, `step` columns apart
+template <int N>
+__device__ __forceinline__ void ld1(uint32_t taddr, uint32_t step, uint32_t (&v)[2])
+{
+    v[1] = 0;
+    if constexpr (N == 2)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
+            "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(v[0]), "=r"(v[1])
+            : "r"(taddr), "r"(taddr + step)
+            : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                     : "=r"(v[0])
+                     : "r"(taddr)
+                     : "memory");
+}
+
 // --- cluster ----------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, int rank)
 {
@@ -229,15 +249,16 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, int rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v)
+// asynchronous 4-byte store into another CTA's shared memory that counts on a barrier there
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -253,18 +274,17 @@ __device__ __forceinline__ int chunk_cols(int c, int nt) { return ((c + nt - 1) 
 
 __device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
 {
-    int lo = 0, hi = a.E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (c->prefix[mid] <= t) lo = mid;
-        else hi = mid;
-    }
+    // the last group with prefix <= t, in two looks of the warp: which 16 groups, which of them
+    const int lane = threadIdx.x & 31;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, 16 * lane < a.E && c->prefix[16 * lane] <= t));
+    const int at = 16 * k + (lane & 15);
+    const int lo = 16 * k + 31 - __clz(__ballot_sync(0xffffffffu, lane < 16 && at < a.E && c->prefix[at] <= t));
     const int first = a.offsets ? c->off[lo] : 0;
     const int rows = a.offsets ? c->off[lo + 1] - first : a.rows;
     const int nt = (rows + a.width - 1) / a.width;
     const int w = chunk_cols(rows, nt);
     const int local = t - c->prefix[lo];
-    const int mi = local / nt, ni = local - mi * nt;   // a weight tile's chunks run next to one another
+    const int mi = nt == 1 ? local : local / nt, ni = local - mi * nt;   // a weight tile's chunks run next to one another
     Tile r;
     r.e = lo;
     r.m0 = mi * kM;
@@ -326,14 +346,13 @@ __device__ __forceinline__ void emit_mx8(const Args &a, const float (&v)[8], int
     }
 }
 
-// NC columns of a tile (acc[0..NA-1][j]) -> the outputs; col(j): column j's output row, or -1
-template <Mode MODE, int NC, class Col>
-__device__ __forceinline__ void emit(const Args &a, const float (&g)[NC], const float (&u)[NC], int m, int lane,
-                                     Col col)
+// 16 columns of a tile -> the outputs; col(j): column j's output row, or -1
+template <Mode MODE, class Col>
+__device__ __forceinline__ void emit16(const Args &a, const float (&g)[16], const float (&u)[16], int m, int lane, Col col)
 {
     if constexpr (MODE == kMxGate) {
 #pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 8) {
+        for (int j0 = 0; j0 < 16; j0 += 8) {
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = silu(g[j0 + j]) * u[j0 + j];
@@ -341,21 +360,42 @@ __device__ __forceinline__ void emit(const Args &a, const float (&g)[NC], const 
         }
     } else {
         if (m >= a.M) return;
-        void *out = a.out[0];
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
+        for (int j = 0; j < 16; ++j) {
             const int r = col(j);
-            if (r < 0) continue;
+            if (r >= 0) store(a.out[0], a.dtype, (size_t)r * a.ld + m, g[j]);
+        }
+    }
+}
+
+// One column of a tile (few columns): row `r` of the output.  A rolled loop over the columns in
+// place of the unrolled 16 keeps the code of a one-token call small: there every instruction is
+// fetched once and used once.
+template <Mode MODE>
+__device__ __forceinline__ void emit1(const Args &a, float g, float u, int m, int lane, int r)
+{
+    if constexpr (MODE == kMxGate) {
+        const float v = silu(g) * u;
+        float f;
+        const uint32_t sb = mx_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu), f);
+        uint32_t w = e2m1x2(f == 0.0f ? 0.0f : v * f, 0.0f) << (4 * (lane & 7));
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, d);
+        if (m < a.M) {
             const size_t at = (size_t)r * a.ld + m;
-            if constexpr (MODE == kGate) {
-                store(out, a.dtype, at, silu(g[j]) * u[j]);
-                if (a.out[1]) {
-                    store(a.out[1], a.dtype, at, g[j]);
-                    store(a.out[2], a.dtype, at, u[j]);
-                }
-            } else {
-                store(out, a.dtype, at, g[j]);
+            if ((lane & 7) == 0) *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.out[0]) + (at >> 1)) = w;
+            if (lane == 0) static_cast<uint8_t *>(a.out[1])[at >> 5] = (uint8_t)sb;
+        }
+    } else if (m < a.M) {
+        const size_t at = (size_t)r * a.ld + m;
+        if constexpr (MODE == kGate) {
+            store(a.out[0], a.dtype, at, silu(g) * u);
+            if (a.out[1]) {
+                store(a.out[1], a.dtype, at, g);
+                store(a.out[2], a.dtype, at, u);
             }
+        } else {
+            store(a.out[0], a.dtype, at, g);
         }
     }
 }
@@ -403,19 +443,19 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     const int tstep = C::FEW ? (int)(gridDim.x / S) : (int)gridDim.x;
     const int ks0 = (int)((long long)a.ksteps * rank / S), ks1 = (int)((long long)a.ksteps * (rank + 1) / S);
 
-    if (tid == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&c->full[i], 1 + C::SF_UNITS);
-            mbar_init(&c->empty[i], 1);
+    if (tid < 32) {
+        if (tid < C::STAGES) {
+            mbar_init(&c->full[tid], 1 + C::SF_UNITS);
+            mbar_init(&c->empty[tid], 1);
+        } else if (tid < C::STAGES + 2) {
+            mbar_init(&c->dfull[tid - C::STAGES], 1);
+            mbar_init(&c->dempty[tid - C::STAGES], C::EPI);
+        } else if (tid == 31) {
+            mbar_init(&c->rfull, 1);
+            mbar_init(&c->rempty, C::EPI * S);
+            mbar_init(&c->fin, 1);
+            c->abort = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c->dfull[i], 1);
-            mbar_init(&c->dempty[i], C::EPI);
-        }
-        mbar_init(&c->rfull, C::EPI * S);
-        mbar_init(&c->rempty, C::EPI * S);
-        mbar_init(&c->fin, 1);
-        c->abort = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -564,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         if (a.early) pdl_wait();
         const int qd = warp & 3, part = (warp - 4) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
-        uint32_t nt = 0, h = 0, parity = 0;   // parity: bit i of half i's next wait
+        uint32_t nt = 0, h = 0, red_parity = 0, parity = 0;   // parity: bit i of half i's next wait
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
             const Tile q = get_tile(a, c, t);
@@ -581,48 +621,50 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             if (C::FEW && S > 1) {
                 // send the partial sums to their columns' owners (column k to rank k % S), then
                 // add up the own columns in rank order
+                const bool more = t + tstep < total;   // the buffers are used again
+                const int per = (kSplitCols + S - 1) / S, own = q.n > rank ? (q.n - rank + S - 1) / S : 0;
+                if (warp == 4 && lane == 0 && own > 0)
+                    mbar_arrive_expect_tx(&c->rfull, (uint32_t)(S * own * C::NA * kM * 4));
                 if (nt >= 1 && !(ok = wait_warp_cluster(&c->rempty, (nt - 1) & 1, c, a.err))) break;
-                const uint32_t rb = smem_u32(red);
-#pragma unroll
-                for (int o = 0; o < C::NA; ++o)
-                    for (int c0 = part * 16; c0 < q.np; c0 += 4 * C::EPI) {
-                        uint32_t v[16];
-                        tc::ld16(d0 + o * dstep + c0, v);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int k = c0 + j;
-                            if (k < q.n)
-                                st_cluster(map_rank(rb + (uint32_t)(((o * C::RED_COLS + rank * ((kSplitCols + S - 1) / S) + k / S) * kM + qd * 32 + lane) * 4), k % S),
-                                           __uint_as_float(v[j]));
-                        }
-                    }
-                tc::fence_before_sync();
-                fence_cluster();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c->dempty[mine >> 1]);   // tiles of this form take one half
-                if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rfull), lane));
-                if (!(ok = wait_warp_cluster(&c->rfull, nt & 1, c, a.err))) break;
-                const int per = (kSplitCols + S - 1) / S;
-                for (int i0 = part * 8; i0 * S + rank < q.n; i0 += 2 * C::EPI) {
-                    float v[2][8];
+                const uint32_t mine0 = smem_u32(red) + (uint32_t)((rank * per * kM + qd * 32 + lane) * 4);
+                const uint32_t rbar = smem_u32(&c->rfull);
+                for (int k = 0, owner = 0, slot = 0; k < q.n; ++k) {
+                    uint32_t v[2];
+                    ld1<C::NA>(d0 + k, dstep, v);
+                    const uint32_t bar = map_rank(rbar, owner);
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float x = 0.0f;
-                            if ((i0 + j) * S + rank < q.n)
-                                for (int r = 0; r < S; ++r) x += red[(o * C::RED_COLS + r * per + i0 + j) * kM + qd * 32 + lane];
-                            v[o][j] = x;
-                        }
-                    emit<MODE, 8>(a, v[0], v[C::NA - 1], m, lane, [&](int j) {
-                        const int k = (i0 + j) * S + rank;
-                        return k < q.n ? q.row0 + k : -1;
-                    });
+                        st_async(map_rank(mine0 + (uint32_t)((o * C::RED_COLS + slot) * kM * 4), owner), v[o], bar);
+                    if (++owner == S) {
+                        owner = 0;
+                        ++slot;
+                    }
                 }
-                fence_cluster();
+                tc::fence_before_sync();
                 __syncwarp();
-                if (lane < S) arrive_cluster(map_rank(smem_u32(&c->rempty), lane));
+                if (lane == 0) mbar_arrive(&c->dempty[mine >> 1]);   // tiles of this form take one half
+                if (own > 0) {
+                    if (!(ok = wait_warp_cluster(&c->rfull, red_parity, c, a.err))) break;
+                    red_parity ^= 1;
+                    for (int i = 0; i < own; ++i) {
+                        float x[2] = {0.0f, 0.0f};
+                        for (int r = 0; r < S; ++r)
+#pragma unroll
+                            for (int o = 0; o < C::NA; ++o) x[o] += red[(o * C::RED_COLS + r * per + i) * kM + qd * 32 + lane];
+                        emit1<MODE>(a, x[0], x[1], m, lane, q.row0 + i * S + rank);
+                    }
+                }
+                __syncwarp();
+                if (more && lane < S) arrive_cluster(map_rank(smem_u32(&c->rempty), lane));
+            } else if (C::FEW) {
+                for (int k = 0; k < q.n; ++k) {
+                    uint32_t v[2];
+                    ld1<C::NA>(d0 + k, dstep, v);
+                    emit1<MODE>(a, __uint_as_float(v[0]), __uint_as_float(v[1]), m, lane, q.row0 + k);
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->dempty[mine >> 1]);
             } else {
                 for (int c0 = part * 16; c0 < q.np; c0 += 4 * C::EPI) {
                     uint32_t v[2][16];
@@ -633,8 +675,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[o][j] = __uint_as_float(v[o][j]);
-                    emit<MODE, 16>(a, f[0], f[C::NA - 1], m, lane,
+                        for (int j = 0; j < 16; ++j) {
+                            asm volatile("" : "+r"(v[o][j]));   // read after the wait
+                            f[o][j] = __uint_as_float(v[o][j]);
+                        }
+                    emit16<MODE>(a, f[0], f[C::NA - 1], m, lane,
                                    [&](int j) { return c0 + j < q.n ? q.row0 + c0 + j : -1; });
                 }
                 tc::fence_before_sync();
