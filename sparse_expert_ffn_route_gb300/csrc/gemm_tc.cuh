@@ -279,28 +279,21 @@ __device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
     const int k = 31 - __clz(__ballot_sync(0xffffffffu, 16 * lane < a.E && c->prefix[16 * lane] <= t));
     const int at = 16 * k + (lane & 15);
     const int lo = 16 * k + 31 - __clz(__ballot_sync(0xffffffffu, lane < 16 && at < a.E && c->prefix[at] <= t));
-    const int first = a.offsets ? c->off[lo] : 0;
-    const int rows = a.offsets ? c->off[lo + 1] - first : a.rows;
-    const int nt = (rows + a.width - 1) / a.width;
-    const int w = chunk_cols(rows, nt);
-    const int local = t - c->prefix[lo];
+    const int first = a.offsets ? uniform(c->off[lo]) : 0;
+    const int rows = a.offsets ? uniform(c->off[lo + 1]) - first : a.rows;
+    const int nt = rows > a.width ? (rows + a.width - 1) / a.width : 1;
+    const int w = nt == 1 ? rows : chunk_cols(rows, nt);
+    const int local = t - uniform(c->prefix[lo]);
     const int mi = nt == 1 ? local : local / nt, ni = local - mi * nt;   // a weight tile's chunks run next to one another
     Tile r;
     r.e = lo;
     r.m0 = mi * kM;
     r.row0 = first + ni * w;
     r.n = max(0, min(w, rows - ni * w));
-    r.e = uniform(r.e);
-    r.m0 = uniform(r.m0);
-    r.row0 = uniform(r.row0);
-    r.n = uniform(r.n);
     r.np = max(16, (r.n + 15) & ~15);
     return r;
 }
 
-// g sigmoid(g).  The fast exponential and quotient are off by a few units of fp32's last place
-// (more by |g| * 2^-24 for large |g|), far below the 16-bit or 4-bit rounding that follows; the
-// exact ones were most of the epilogue's instructions.  An exponential that overflows gives 0.
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 __device__ __forceinline__ void store(void *p, int dtype, size_t i, float v)
@@ -401,13 +394,14 @@ __device__ __forceinline__ void emit1(const Args &a, float g, float u, int m, in
 }
 
 // 16 scale bytes (blocks 16 kc .. 16 kc + 15) of a row of K / 32; past the end: 0 (2^-127, on
-// codes that are zero there)
+// codes that are zero there).  WHOLE: K is a multiple of 512, every row's 16 are one aligned load;
+// a kernel of its own, since the other form's code beside it cost one-token calls a microsecond.
+template <bool WHOLE>
 __device__ __forceinline__ uint4 load_scales(const uint8_t *base, long long row, long long rows, int ld, int kc)
 {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row >= rows) return v;
+    if (row >= rows) return make_uint4(0, 0, 0, 0);
     const uint8_t *p = base + row * ld + 16 * kc;
-    if ((ld & 15) == 0) return __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (WHOLE) return __ldg(reinterpret_cast<const uint4 *>(p));
     const int left = min(16, ld - 16 * kc);
     uint32_t w[4] = {0, 0, 0, 0};
     if ((ld & 3) == 0) {   // K a multiple of 128: whole words
@@ -422,14 +416,12 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t *base, long long row,
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <Mode MODE, int BN>
+template <Mode MODE, int BN, bool WHOLE>
 __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     gemm_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
     using C = Cfg<MODE, BN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    if (!a.early) pdl_wait();
-    pdl_launch_dependents();
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sfring = ring + C::STAGES * (C::NA * C::A_BYTES + C::B_BYTES);
     float *red = reinterpret_cast<float *>(sfring + C::STAGES * C::SF_BYTES);
@@ -462,6 +454,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         tc::tmem_alloc(&c->tmem, C::TMEM_COLS);
         tc::tmem_relinquish();
     }
+    if (!a.early) pdl_wait();
+    pdl_launch_dependents();
     // tiles before each group: thread e (in rounds of the block) has group e, a scan within each
     // warp, then the warps' sums.  A group whose offsets do not lie in order within the rows is
     // recorded and left out.
@@ -714,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             }
             if (lt < total) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = load_scales(base, lrow + lane + 32 * i, rows, a.sf_ld, lk);
+                for (int i = 0; i < 4; ++i) v[i] = load_scales<WHOLE>(base, lrow + lane + 32 * i, rows, a.sf_ld, lk);
                 ++lk;
             }
         };
@@ -726,7 +720,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             uint4 now[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) now[j] = v[j];
-            if (!C::FEW) load();
+            if (!C::FEW || i == 0) load();
             for (int ks = max(ks0, 2 * kc); ks < min(ks1, 2 * kc + 2); ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (a.early && it == C::STAGES) pdl_wait();
@@ -739,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->full[s]);
             }
-            if (C::FEW) load();
+            if (C::FEW && i > 0) load();
             if (++kc == kc1) kc = kc0;
         }
     }
@@ -757,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
 // Clusters of `size` CTAs of this kernel that the current device holds at once (0 if unknown); a
 // cluster lies within one of the device's processor groups, so this is less than SMs / size
 // (measured on GB300 with one CTA an SM: 76, 46, 36, 28, 23, 15, 15 for 2 to 8).
-template <Mode MODE, int BN>
+template <Mode MODE, int BN, bool WHOLE>
 int max_clusters(int size)
 {
     static std::atomic<int> known[64][9];
@@ -775,7 +769,7 @@ int max_clusters(int size)
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        const void *k = reinterpret_cast<const void *>(gemm_kernel<MODE, BN>);
+        const void *k = reinterpret_cast<const void *>(gemm_kernel<MODE, BN, WHOLE>);
         if (ensure_dynamic_smem(k, Cfg<MODE, BN>::SMEM) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
             cudaGetLastError();
@@ -786,24 +780,26 @@ int max_clusters(int size)
     return n;
 }
 
-// CTAs that share a tile when `tiles` of them would leave SMs idle: the largest cluster of
-// which the device holds as many as there are tiles (a second wave would cost more than the
-// finer split gains)
-template <Mode MODE, int BN>
+// CTAs that share a tile when `tiles` of them would leave SMs idle.  Each keeps at least 8 stages
+// of the reduction: below that the exchange of the sums costs what the shorter stream saves
+// (one token, microseconds with 1, 2, 4, 8 CTAs a tile: 48 tiles of 8 stages 6.0, 6.6, 6.1, 10.4;
+// 16 tiles of 96 stages 32.7, 18.7, 11.7, 9.3).  All clusters run at once: the query counts one CTA
+// an SM, two fit.
+template <Mode MODE, int BN, bool WHOLE>
 int choose_split(long long tiles, int ksteps)
 {
     int best = 1;
     if (Cfg<MODE, BN>::FEW)
-        for (int s = 2; s <= 8 && s <= ksteps && s * tiles <= num_sms(); ++s)
-            if (max_clusters<MODE, BN>(s) >= tiles) best = s;
+        for (int s = 2; s <= 8 && 8 * s <= ksteps && s * tiles <= num_sms(); ++s)
+            if (Cfg<MODE, BN>::PER_SM * max_clusters<MODE, BN, WHOLE>(s) >= tiles) best = s;
     return best;
 }
 
-template <Mode MODE, int BN>
+template <Mode MODE, int BN, bool WHOLE>
 cudaError_t launch(const Args &a, const Maps &m, int grid, cudaStream_t st)
 {
     using C = Cfg<MODE, BN>;
-    return launch_kernel(gemm_kernel<MODE, BN>, dim3(grid), dim3(C::THREADS), C::SMEM, st, a.split, a, m);
+    return launch_kernel(gemm_kernel<MODE, BN, WHOLE>, dim3(grid), dim3(C::THREADS), C::SMEM, st, a.split, a, m);
 }
 
 }  // namespace gemm

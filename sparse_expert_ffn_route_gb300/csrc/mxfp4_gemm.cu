@@ -28,19 +28,25 @@ cudaError_t code_maps(Maps &m, const uint8_t *a0, const uint8_t *a1, long long a
 bool few_rows(int rows, int E) { return rows <= 24 * std::min(E, rows); }
 constexpr int kFew = 32, kMany = 192;
 
-template <Mode MODE>
-cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
+template <Mode MODE, bool WHOLE>
+cudaError_t run_as(Args &a, const Maps &m, cudaStream_t st)
 {
     const int sms = num_sms();
     const int mtiles = (a.M + kM - 1) / kM, used = std::min(a.E, a.rows);
     const int widest = few_rows(a.rows, a.E) ? kFew : kMany;
-    a.split = widest == kFew ? choose_split<MODE, kFew>((long long)mtiles * used, a.ksteps) : 1;
+    a.split = widest == kFew ? choose_split<MODE, kFew, WHOLE>((long long)mtiles * used, a.ksteps) : 1;
     a.width = a.split > 1 ? kSplitCols : widest;
     // at most this many tiles: every group's last chunk may be short
     const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + a.width - 1) / a.width + used);
     if (widest == kFew)
-        return launch<MODE, kFew>(a, m, (int)std::min<long long>(tiles, 2 * sms / a.split) * a.split, st);
-    return launch<MODE, kMany>(a, m, (int)std::min<long long>(tiles, sms), st);
+        return launch<MODE, kFew, WHOLE>(a, m, (int)std::min<long long>(tiles, 2 * sms / a.split) * a.split, st);
+    return launch<MODE, kMany, WHOLE>(a, m, (int)std::min<long long>(tiles, sms), st);
+}
+
+template <Mode MODE>
+cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
+{
+    return a.sf_ld % 16 ? run_as<MODE, false>(a, m, st) : run_as<MODE, true>(a, m, st);
 }
 
 }  // namespace
