@@ -362,10 +362,10 @@ def _dtype(t: torch.Tensor, name: str) -> int:
 
 def _dense(t: torch.Tensor, name: str, shape, dtype) -> int:
     """Device pointer of a contiguous CUDA tensor of the given shape and type."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("%s must be a contiguous CUDA tensor %s of %s (got %s of %s%s)" % (
-            name, shape, dtype, tuple(t.shape), t.dtype, "" if t.is_contiguous() else ", strided"))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous CUDA tensor %s of %s (got %s of %s%s)" % (
+        name, shape, dtype, tuple(t.shape), t.dtype, "" if t.is_contiguous() else ", strided"))
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -394,12 +394,15 @@ def moe_quantize_mxfp4(x, codes, scales, stream=None):
 
 def moe_dequantize_mxfp4(codes, scales, y, stream=None):
     """The values that MXFP4 codes [..][K/2] and scales [..][K/32] stand for, into y [..][K]."""
-    K = y.shape[-1]
-    rows, lead = (y.numel() // K if K else 0), tuple(y.shape[:-1])
+    if y.dim() == 2:
+        rows, K = y.shape
+        c, sc = (rows, K // 2), (rows, K // 32)
+    else:
+        K, lead = y.shape[-1], tuple(y.shape[:-1])
+        rows, c, sc = (y.numel() // K if K else 0), lead + (K // 2,), lead + (K // 32,)
     _check(load_library().moe_dequantize_mxfp4(
-        _dense(codes, "codes", lead + (K // 2,), torch.uint8),
-        _dense(scales, "scales", lead + (K // 32,), torch.uint8), rows, K,
-        _dense(y, "y", lead + (K,), y.dtype), _dtype(y, "y"), _raw_stream(stream)), "moe_dequantize_mxfp4")
+        _dense(codes, "codes", c, torch.uint8), _dense(scales, "scales", sc, torch.uint8), rows, K,
+        _dense(y, "y", y.shape, y.dtype), _dtype(y, "y"), _raw_stream(stream)), "moe_dequantize_mxfp4")
 
 
 def alloc_mxfp4_matmul_workspace(device="cuda") -> torch.Tensor:
@@ -411,13 +414,17 @@ def moe_mxfp4_matmul(x, x_scales, w, w_scales, y, workspace, offsets=None, strea
     """y [rows][N] = x w^T by group: x [rows][K/2], x_scales [rows][K/32]; w [groups][N][K/2] (or
     [N][K/2]), w_scales alike; offsets [groups + 1] int32 (None: one group, all rows)."""
     rows, half = x.shape
-    groups, N = (1, w.shape[0]) if w.dim() == 2 else w.shape[:2]
-    K, u8, lead = 2 * half, torch.uint8, tuple(w.shape[:-1])
+    K32, u8 = half // 16, torch.uint8
+    if w.dim() == 2:
+        groups, N = 1, w.shape[0]
+        pw, psw = _dense(w, "w", (N, half), u8), _dense(w_scales, "w_scales", (N, K32), u8)
+    else:
+        groups, N = w.shape[0], w.shape[1]
+        pw, psw = _dense(w, "w", (groups, N, half), u8), _dense(w_scales, "w_scales", (groups, N, K32), u8)
     _check(load_library().moe_mxfp4_matmul(
-        _dense(x, "x", (rows, half), u8), _dense(x_scales, "x_scales", (rows, K // 32), u8), rows,
-        _dense(w, "w", lead + (half,), u8), _dense(w_scales, "w_scales", lead + (K // 32,), u8), groups,
-        None if offsets is None else _dense(offsets, "offsets", (groups + 1,), torch.int32), N, K,
-        _dense(y, "y", (rows, N), y.dtype), _dtype(y, "y"), _ptr(workspace), workspace.numel(),
+        _dense(x, "x", (rows, half), u8), _dense(x_scales, "x_scales", (rows, K32), u8), rows, pw, psw, groups,
+        None if offsets is None else _dense(offsets, "offsets", (groups + 1,), torch.int32), N, 2 * half,
+        _dense(y, "y", (rows, N), y.dtype), _dtype(y, "y"), workspace.data_ptr(), workspace.numel(),
         _raw_stream(stream)), "moe_mxfp4_matmul")
 
 
@@ -441,16 +448,20 @@ def moe_mxfp4_expert_ffn(cfg, x, weights: Dict[str, torch.Tensor], y_pairs, work
     offsets / tok (as moe_permute writes them; both None: one expert, every token).  weights:
     w_gate, w_up [E][F][H/2], w_down [E][H][F/2] and s_gate, s_up [E][F][H/32],
     s_down [E][H][F/32], uint8."""
-    T, H, F, E, u8 = x.shape[0], cfg.hidden, cfg.d_ff, cfg.n_experts, torch.uint8
-    shapes = {"w_gate": (E, F, H // 2), "s_gate": (E, F, H // 32), "w_up": (E, F, H // 2),
-              "s_up": (E, F, H // 32), "w_down": (E, H, F // 2), "s_down": (E, H, F // 32)}
-    w = ExpertMxfp4(*[_dense(weights[k], k, s, u8) for k, s in shapes.items()])
+    T, H, F, E, P = x.shape[0], cfg.hidden, cfg.d_ff, cfg.n_experts, y_pairs.shape[0]
+    u8, up, down = torch.uint8, (E, F, H // 2), (E, H, F // 2)
+    s_up, s_down = (E, F, H // 32), (E, H, F // 32)
+    w = ExpertMxfp4(_dense(weights["w_gate"], "w_gate", up, u8), _dense(weights["s_gate"], "s_gate", s_up, u8),
+                    _dense(weights["w_up"], "w_up", up, u8), _dense(weights["s_up"], "s_up", s_up, u8),
+                    _dense(weights["w_down"], "w_down", down, u8), _dense(weights["s_down"], "s_down", s_down, u8))
+    if P != T * cfg.top_k:
+        raise ValueError("y_pairs must have T * top_k = %d rows (got %d)" % (T * cfg.top_k, P))
     _check(load_library().moe_mxfp4_expert_ffn(
         ctypes.byref(cfg), _dense(x, "x", (T, H), x.dtype), _dtype(x, "x"), T, ctypes.byref(w),
         None if offsets is None else _dense(offsets, "offsets", (E + 1,), torch.int32),
-        None if tok is None else _dense(tok, "tok", (T * cfg.top_k,), torch.int32),
-        _dense(y_pairs, "y_pairs", (T * cfg.top_k, H), y_pairs.dtype), _dtype(y_pairs, "y_pairs"),
-        _ptr(workspace), workspace.numel(), _raw_stream(stream)), "moe_mxfp4_expert_ffn")
+        None if tok is None else _dense(tok, "tok", (P,), torch.int32),
+        _dense(y_pairs, "y_pairs", (P, H), y_pairs.dtype), _dtype(y_pairs, "y_pairs"),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream)), "moe_mxfp4_expert_ffn")
 
 
 def moe_gated_workspace_size(T: int, H: int, F: int, train: bool) -> int:

@@ -211,6 +211,10 @@ cudaError_t launch_quantize_int3(const float *w, int rows, int K, uint8_t *packe
 cudaError_t launch_quantize_mxfp4(const void *x, int dtype, long long ldx, long long rows, int K, const int32_t *tok,
                                   const int32_t *limit, int T, uint8_t *codes, uint8_t *scales, int32_t *err,
                                   cudaStream_t st);
+// quantised rows in the order of tok (K a multiple of 64), limit and T as above
+cudaError_t launch_gather_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K, const int32_t *tok,
+                                const int32_t *limit, int T, uint8_t *to_codes, uint8_t *to_scales, int32_t *err,
+                                cudaStream_t st);
 cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K, void *y,
                                     int dtype, cudaStream_t st);
 

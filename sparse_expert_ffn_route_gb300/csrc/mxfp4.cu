@@ -133,9 +133,44 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Quantised rows in the order of a list: row r from row tok[r] for r < *limit, one warp a row.
+// A bad index: NaN scales and a record, as in the quantiser.
+__global__ void __launch_bounds__(kThreads)
+    gather_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, long long rows, int K,
+                  const int32_t *__restrict__ tok, const int32_t *__restrict__ limit, int nx, uint8_t *__restrict__ to_codes,
+                  uint8_t *__restrict__ to_scales, int32_t *err)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    if (row >= rows || row >= *limit) return;
+    const int src = tok[row];
+    const bool bad = src < 0 || src >= nx;
+    if (bad && lane == 0) atomicOr(err, kErrBadToken);
+    const int chunks = K / 32;   // 16 bytes of codes and a scale byte each
+    const uint4 *from = reinterpret_cast<const uint4 *>(codes) + (long long)(bad ? 0 : src) * chunks;
+    uint4 *to = reinterpret_cast<uint4 *>(to_codes) + row * chunks;
+    for (int i0 = lane; i0 < chunks; i0 += 4 * 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (i0 + 32 * j < chunks && !bad) v[j] = __ldg(from + i0 + 32 * j);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + 32 * j < chunks) to[i0 + 32 * j] = v[j];
+    }
+    // K is a multiple of 64: an even number of scale bytes a row
+    const uint16_t *sf = reinterpret_cast<const uint16_t *>(scales) + (long long)(bad ? 0 : src) * (chunks / 2);
+    uint16_t *st = reinterpret_cast<uint16_t *>(to_scales) + row * (chunks / 2);
+    for (int i = lane; i < chunks / 2; i += 32) st[i] = bad ? (uint16_t)0xffff : __ldg(sf + i);
+}
+
 // A lane writes 16 consecutive bytes a step, so that a warp's stores are 512 consecutive bytes:
 // 4 values in fp32 (8, as two stores 32 bytes apart over the warp, wrote 403 MB at 4.9 TB/s; this
-// way at DEQ32 TB/s), 8 in 16 bits.
+// way at 6.5 TB/s), 8 in 16 bits.
 __device__ __forceinline__ void put(float *p, const float (&v)[4])
 {
     *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -213,6 +248,15 @@ cudaError_t launch_quantize_mxfp4(const void *x, int dtype, long long ldx, long 
     if (dtype == MOE_DTYPE_F32) return quantize<float>(x, ldx, rows, K, tok, limit, T, codes, scales, err, st);
     if (dtype == MOE_DTYPE_BF16) return quantize<__nv_bfloat16>(x, ldx, rows, K, tok, limit, T, codes, scales, err, st);
     return quantize<__half>(x, ldx, rows, K, tok, limit, T, codes, scales, err, st);
+}
+
+cudaError_t launch_gather_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K, const int32_t *tok,
+                                const int32_t *limit, int T, uint8_t *to_codes, uint8_t *to_scales, int32_t *err,
+                                cudaStream_t st)
+{
+    const dim3 grid((unsigned)((rows * 32 + kThreads - 1) / kThreads));
+    return launch_kernel(gather_kernel, grid, dim3(kThreads), 0, st, 1, codes, scales, rows, K, tok, limit, T, to_codes,
+                         to_scales, err);
 }
 
 cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, long long rows, int K, void *y,

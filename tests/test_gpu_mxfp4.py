@@ -274,6 +274,37 @@ def test_expert_ffn_dense_and_partial_lists():
     assert (got[3:] == 7).all()
 
 
+def test_expert_ffn_quantised_once_a_token():
+    """Enough pairs that each token is quantised once and its row copied: lists that leave rows and
+    an expert out, a bad index and a NaN row."""
+    rng = np.random.default_rng(21)
+    T, E, K, H, F = 1100, 4, 4, 2048, 64
+    cfg = moe.MoeConfig.make(H, E, K, F)
+    w, val = expert_weights(rng, E, H, F)
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    x[7, 100] = np.inf
+    counts = [900, 0, 1100, 300]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    tok = np.concatenate([rng.permutation(T)[:n] for n in counts] + [np.zeros(T * K - off[-1])]).astype(np.int32)
+    tok[5] = T
+    y = torch.full((T * K, H), 7.0, device="cuda")
+    ws = moe.alloc_mxfp4_workspace(cfg, T)
+    moe.moe_mxfp4_expert_ffn(cfg, dev(x), w, y, ws, offsets=dev(off), tok=dev(tok))
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_check_errors(ws)
+    assert e.value.code == moe.MOE_ERR_DEVICE
+    got = y.cpu().double().numpy()
+    assert (got[off[-1]:] == 7).all()
+    nan = np.zeros(T * K, bool)
+    nan[:off[-1]] = (tok[:off[-1]] == 7) | (tok[:off[-1]] == T)
+    assert np.isnan(got[nan]).all() and np.isfinite(got[~nan]).all()
+    for e in range(E):
+        rows = np.arange(off[e], off[e + 1])
+        rows = rows[~nan[rows]]
+        if len(rows):
+            check_ffn(got[rows], x[tok[rows]].astype(np.float64), val, e, torch.float32)
+
+
 def test_expert_ffn_bad_token_and_nan_rows():
     rng = np.random.default_rng(12)
     H, F = 128, 64
