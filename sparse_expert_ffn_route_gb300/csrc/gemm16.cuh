@@ -27,8 +27,10 @@ namespace moe {
 namespace gemm16 {
 
 using gemm::cluster_sync;
+using gemm::commit_pair;
 using gemm::expect_tx;
 using gemm::map_rank;
+using gemm::tma_2d_pair;
 using gemm::uniform;
 
 enum Mode { kGate2, kDx, kDw };
@@ -99,17 +101,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *
     return __all_sync(0xffffffffu, ok);
 }
 
-// TMA into this CTA's shared memory, completing on a barrier of either CTA of the pair
-__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-        "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
@@ -117,21 +108,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
-}
-
-// one arrival on this barrier of both CTAs once the MMAs issued so far are done
-__device__ __forceinline__ void commit_pair(uint64_t *bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
-            smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void arrive_remote(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 8 consecutive columns -> 16 bytes
@@ -272,6 +248,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
             tc::fence_after_sync();
             const size_t at = (size_t)row * a.cols + n0;
             void *out = MODE == kDw ? a.out[g] : a.out[0];
+            const auto give_back = [&] {   // the accumulator, once this warp has read its part
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) gemm::arrive_cluster_relaxed(map_rank(smem_u32(&c->dempty[buf]), 0));
+            };
+            if (part * 32 >= n) give_back();
             // 32 columns at a time, alternately to the two warps of these lanes; the width is a
             // multiple of 32, the columns of 8
             for (int c0 = part * 32; c0 < n; c0 += 64) {
@@ -283,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                 for (int o = 0; o < C::NB; ++o)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[o][j]));   // read after the wait
+                if (c0 + 64 >= n) give_back();
                 if (row < a.rows) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
@@ -304,9 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                     }
                 }
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive_remote(map_rank(smem_u32(&c->dempty[buf]), 0));
         }
     }
 

@@ -9,9 +9,15 @@
 // are, and a warp's lanes write consecutive output elements.  The MMA's column count follows the
 // tile's token count in steps of 16, so one token costs 16 columns.
 //
-// Work.  A tile is 128 lanes x up to BN columns over the whole reduction; groups (experts) are
-// cut into equal column chunks of at most BN.  CTAs run tiles blockIdx, blockIdx + grid, ...
-// With few tiles a cluster of S CTAs shares one: each takes a slice of the reduction, sends its
+// Work.  A tile is 128 lanes (256 on a pair) x up to BN columns over the whole reduction; groups
+// (experts) are cut into equal column chunks.  CTAs run tiles blockIdx, blockIdx + grid, ...
+//
+// Many columns (BN 224) run on pairs of SMs (cta_group::2): each holds its 128 weight rows and
+// half of the tokens.  What feeds the tensor pipe is the bound, about 50 bytes a cycle from L2
+// into an SM: one SM's 128 x 192 tile needs 43 KB a stage for 384 cycles of the pipe and ran at
+// 826 (a 4096-token prompt of 6144 x 6144 in 73 us), a pair's 256 x 224 33 KB for 448.
+//
+// Few columns (BN 32): with few tiles a cluster of S CTAs shares one: each takes a slice of the reduction, sends its
 // partial sums to the owner of each column through distributed shared memory, and the owner
 // adds them in rank order (the sums do not depend on timing).
 //
@@ -53,7 +59,7 @@ namespace gemm {
 enum Mode { kMxGate, kMxMul, kGate };
 
 constexpr int kM = 128;          // lanes of a tile
-constexpr int kBoxMaps = 12;     // column-operand maps with boxes of 16 (k + 1) rows
+constexpr int kBoxMaps = 7;      // column-operand maps with boxes of 16 (k + 1) rows
 constexpr int kMaxGroups = 512;
 constexpr int kSplitCols = 16;   // columns of a tile that CTAs share
 
@@ -83,7 +89,7 @@ struct Args {
 
 struct Maps {
     CUtensorMap a[2];
-    CUtensorMap b[kBoxMaps];   // boxes of 16 (k + 1) rows: one for each tile width
+    CUtensorMap b[kBoxMaps];   // boxes of 16 (k + 1) rows: one for each number of columns that a CTA loads
 };
 
 template <Mode MODE, int BN>
@@ -91,12 +97,15 @@ struct Cfg {
     static constexpr bool MX = is_mx(MODE), GATED = is_gated(MODE);
     static constexpr int NA = GATED ? 2 : 1;               // lanes operands (accumulators) of a tile
     static constexpr bool FEW = BN <= 32;                  // two CTAs an SM; clusters may share a tile
-    static constexpr int EPI = FEW ? 4 : 8;                // epilogue warps
+    static constexpr bool PAIR = !FEW;                     // two SMs a tile: 256 lanes, each half of the columns' operand
+    static constexpr int LANES = PAIR ? 2 * kM : kM;       // of a tile
+    static constexpr int STEP = PAIR ? 32 : 16;            // the MMA's column count is a multiple
+    static constexpr int EPI = FEW ? 4 : MX && GATED ? 16 : 8;   // epilogue warps
     // TMEM: two halves of accumulators.  A tile takes one half, so that its epilogue runs beside
     // the next tile's MMAs; two accumulators of more than HALF / 2 columns take both.
     static constexpr int HALF = FEW ? NA * BN : 224;
     static constexpr int A_BYTES = kM * 128;
-    static constexpr int B_BYTES = BN * 128;
+    static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * 128;
     static constexpr int SFB_UNITS = MX ? (BN + 127) / 128 : 0;
     static constexpr int SF_UNITS = MX ? NA + SFB_UNITS : 0;   // 128-row scale blocks of a stage (2 x 512 B each)
     static constexpr int SF_BYTES = SF_UNITS * 1024;
@@ -125,11 +134,11 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sy
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 struct Ctrl {
-    uint64_t full[8], empty[8], dfull[2], dempty[2], rfull, rempty, fin;
+    uint64_t full[8], empty[8], sfull[8], dfull[2], dempty[2], rfull, rempty, fin;
     uint32_t tmem;
     int abort;
     int tiles;
-    int warp_tiles[16];
+    int warp_tiles[24];
     int32_t prefix[kMaxGroups + 1], off[kMaxGroups + 1];
 };
 
@@ -259,9 +268,94 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// the same for what needs no order of memory, the end of TMEM reads (a release at cluster scope waits
+// for the warp's global stores, 1500 cycles and more)
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// --- pairs of SMs (cta_group::2) ---------------------------------------------------------
+// TMA into this CTA's shared memory, completing on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// one arrival on this barrier of both CTAs once the tensor operations issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+// one arrival on this barrier of the pair's leader
+__device__ __forceinline__ void commit_leader(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 1;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+
+// each CTA's block at this place of its shared memory into its TMEM
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    if constexpr (PAIR) commit_pair(bar);
+    else tc::commit_elect(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols)
+{
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tc::tmem_alloc(dst, cols);
+        tc::tmem_relinquish();
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols)
+{
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+    else tc::tmem_dealloc(taddr, cols);
 }
 
 // --- tiles ------------------------------------------------------------------------------
@@ -272,25 +366,26 @@ struct Tile {
 // columns of a group of c rows in nt chunks of equal size (a multiple of 16)
 __device__ __forceinline__ int chunk_cols(int c, int nt) { return ((c + nt - 1) / nt + 15) & ~15; }
 
-__device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *c, int t)
+template <class C>
+__device__ __forceinline__ Tile get_tile(const Args &a, const Ctrl *ctrl, int t)
 {
     // the last group with prefix <= t, in two looks of the warp: which 16 groups, which of them
     const int lane = threadIdx.x & 31;
-    const int k = 31 - __clz(__ballot_sync(0xffffffffu, 16 * lane < a.E && c->prefix[16 * lane] <= t));
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, 16 * lane < a.E && ctrl->prefix[16 * lane] <= t));
     const int at = 16 * k + (lane & 15);
-    const int lo = 16 * k + 31 - __clz(__ballot_sync(0xffffffffu, lane < 16 && at < a.E && c->prefix[at] <= t));
-    const int first = a.offsets ? uniform(c->off[lo]) : 0;
-    const int rows = a.offsets ? uniform(c->off[lo + 1]) - first : a.rows;
+    const int lo = 16 * k + 31 - __clz(__ballot_sync(0xffffffffu, lane < 16 && at < a.E && ctrl->prefix[at] <= t));
+    const int first = a.offsets ? uniform(ctrl->off[lo]) : 0;
+    const int rows = a.offsets ? uniform(ctrl->off[lo + 1]) - first : a.rows;
     const int nt = rows > a.width ? (rows + a.width - 1) / a.width : 1;
     const int w = nt == 1 ? rows : chunk_cols(rows, nt);
-    const int local = t - uniform(c->prefix[lo]);
+    const int local = t - uniform(ctrl->prefix[lo]);
     const int mi = nt == 1 ? local : local / nt, ni = local - mi * nt;   // a weight tile's chunks run next to one another
     Tile r;
     r.e = lo;
-    r.m0 = mi * kM;
+    r.m0 = mi * C::LANES;   // the pair's first lane
     r.row0 = first + ni * w;
     r.n = max(0, min(w, rows - ni * w));
-    r.np = max(16, (r.n + 15) & ~15);
+    r.np = max(C::STEP, (r.n + C::STEP - 1) & ~(C::STEP - 1));
     return r;
 }
 
@@ -428,20 +523,23 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     Ctrl *c = reinterpret_cast<Ctrl *>(reinterpret_cast<uint8_t *>(red) + C::RED_BYTES);
     static_assert(sizeof(Ctrl) <= C::CTRL_BYTES, "control block");
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    const int mtiles = (a.M + kM - 1) / kM;
+    const int mtiles = (a.M + C::LANES - 1) / C::LANES;
     const int S = C::FEW ? a.split : 1;
-    const int rank = C::FEW ? (int)(blockIdx.x % S) : 0;
-    const int tile0 = C::FEW ? (int)(blockIdx.x / S) : (int)blockIdx.x;
-    const int tstep = C::FEW ? (int)(gridDim.x / S) : (int)gridDim.x;
-    const int ks0 = (int)((long long)a.ksteps * rank / S), ks1 = (int)((long long)a.ksteps * (rank + 1) / S);
+    // CTAs of a cluster: S that share a tile's reduction, or the two of a pair
+    const int CS = C::PAIR ? 2 : S;
+    const int rank = (int)(blockIdx.x % CS), tile0 = (int)(blockIdx.x / CS), tstep = (int)(gridDim.x / CS);
+    const int ks0 = C::PAIR ? 0 : (int)((long long)a.ksteps * rank / S);
+    const int ks1 = C::PAIR ? a.ksteps : (int)((long long)a.ksteps * (rank + 1) / S);
+    const int lane0 = C::PAIR ? rank * kM : 0;   // this CTA's first lane in the tile
 
     if (tid < 32) {
         if (tid < C::STAGES) {
-            mbar_init(&c->full[tid], 1 + C::SF_UNITS);
+            mbar_init(&c->full[tid], C::PAIR ? 2 : 1 + C::SF_UNITS);
+            mbar_init(&c->sfull[tid], C::SF_UNITS > 0 ? C::SF_UNITS : 1);
             mbar_init(&c->empty[tid], 1);
         } else if (tid < C::STAGES + 2) {
             mbar_init(&c->dfull[tid - C::STAGES], 1);
-            mbar_init(&c->dempty[tid - C::STAGES], C::EPI);
+            mbar_init(&c->dempty[tid - C::STAGES], (C::PAIR ? 2 : 1) * C::EPI);
         } else if (tid == 31) {
             mbar_init(&c->rfull, 1);
             mbar_init(&c->rempty, C::EPI * S);
@@ -451,8 +549,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         fence_mbar_init();
     }
     if (warp == 1) {
-        tc::tmem_alloc(&c->tmem, C::TMEM_COLS);
-        tc::tmem_relinquish();
+        tmem_alloc<C::PAIR>(&c->tmem, C::TMEM_COLS);
     }
     if (!a.early) pdl_wait();
     pdl_launch_dependents();
@@ -500,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (C::FEW && S > 1) cluster_sync();   // every rank's barriers are ready
+    if (CS > 1) cluster_sync();   // every rank's barriers are ready
     const uint32_t tmem = uniform(c->tmem);
     const int total = uniform(c->tiles);
 
@@ -513,26 +610,28 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         uint32_t it = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
-            const Tile q = get_tile(a, c, t);
-            const uint32_t bytes = C::NA * C::A_BYTES + (uint32_t)q.np * 128u;
-            const CUtensorMap *map = col ? &maps.b[(q.np >> 4) - 1] : &maps.a[o];
-            const int y = col ? q.row0 : q.e * a.M + q.m0;
+            const Tile q = get_tile<C>(a, c, t);
+            const int cols = C::PAIR ? q.np >> 1 : q.np;   // this CTA's
+            const uint32_t bytes = (C::PAIR ? 2u : 1u) * (C::NA * C::A_BYTES + (uint32_t)cols * 128u);
+            const CUtensorMap *map = col ? &maps.b[(cols >> 4) - 1] : &maps.a[o];
+            const int y = col ? q.row0 + (C::PAIR ? rank * cols : 0) : q.e * a.M + q.m0 + lane0;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (a.early && it == C::STAGES) pdl_wait();
                 if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
-                const uint32_t bar = smem_u32(&c->full[s]);
-                if (warp == 0) expect_tx(bar, bytes);
-                tma_2d(to + s * (C::NA * C::A_BYTES + C::B_BYTES), map, ks * (C::MX ? 128 : 64), y, bar);
+                const uint32_t bar = smem_u32(&c->full[s]), dst = to + s * (C::NA * C::A_BYTES + C::B_BYTES);
+                if (warp == 0 && (!C::PAIR || rank == 0)) expect_tx(bar, bytes);
+                if constexpr (C::PAIR) tma_2d_pair(dst, map, ks * (C::MX ? 128 : 64), y, map_rank(bar, 0));
+                else tma_2d(dst, map, ks * (C::MX ? 128 : 64), y, bar);
             }
         }
         // copies still in flight (after a wait that gave up) land before the CTA ends
         if (a.early) pdl_wait();
-        if (warp == 0)
+        if (warp == 0 && (!C::PAIR || rank == 0))
             for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
                 mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && !(C::PAIR && rank == 1)) {
         // ---------------- MMA issue ---------------------------------------------------------
         if (a.early) pdl_wait();
         const uint32_t r0 = smem_u32(ring), sf0 = smem_u32(sfring);
@@ -540,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         uint32_t gave = 0;   // bit i: the parity of half i's next wait; bit 2 + i: it has been used
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep) {
-            const Tile q = get_tile(a, c, t);
+            const Tile q = get_tile<C>(a, c, t);
             const uint32_t idesc = a.idesc | (uint32_t)(q.np >> 3) << 17;
             const bool both = C::both_halves(q.np);
             if (both) h = 0;
@@ -552,6 +651,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (!(ok = wait_warp(&c->full[s], (it / C::STAGES) & 1, c, a.err))) break;
+                if (C::PAIR && !(ok = wait_warp(&c->sfull[s], (it / C::STAGES) & 1, c, a.err))) break;
                 const uint32_t as = r0 + s * (C::NA * C::A_BYTES + C::B_BYTES), bs = as + C::NA * C::A_BYTES;
                 uint32_t sfc = 0;
                 if constexpr (C::MX) {
@@ -565,8 +665,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
 #pragma unroll
-                        for (int u = 0; u < C::SF_UNITS; ++u)
-                            cp_scales(sfc + b * 16 + (u < C::NA ? u * 4 : 8 + (u - C::NA) * 4), sd + (uint64_t)((u * 1024 + b * 512) >> 4));
+                        for (int u = 0; u < C::SF_UNITS; ++u) {
+                            const uint32_t to = sfc + b * 16 + (u < C::NA ? u * 4 : 8 + (u - C::NA) * 4);
+                            const uint64_t from = sd + (uint64_t)((u * 1024 + b * 512) >> 4);
+                            if constexpr (C::PAIR) cp_scales_pair(to, from);
+                            else cp_scales(to, from);
+                        }
                     }
                 } else {
                     tc::fence_after_sync();
@@ -579,20 +683,37 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                         const uint64_t ka = tc::sdesc_kmajor_sw128(as + o * C::A_BYTES) + k * 2, kb = bd + k * 2;
                         if constexpr (C::MX) {
                             const uint32_t id = idesc | (uint32_t)((k & 1) * 2) << 29 | (uint32_t)((k & 1) * 2) << 4;
-                            mma_mx4(d0 + o * dstep, ka, kb, id, sfc + (k >> 1) * 16 + o * 4, sfc + (k >> 1) * 16 + 8, ks > ks0 || k > 0);
+                            const uint32_t sa = sfc + (k >> 1) * 16 + o * 4, sb = sfc + (k >> 1) * 16 + 8;
+                            if constexpr (C::PAIR) mma_mx4_pair(d0 + o * dstep, ka, kb, id, sa, sb, ks > ks0 || k > 0);
+                            else mma_mx4(d0 + o * dstep, ka, kb, id, sa, sb, ks > ks0 || k > 0);
                         } else {
                             mma_f16(d0 + o * dstep, ka, kb, idesc, ks > ks0 || k > 0);
                         }
                     }
                 }
-                tc::commit_elect(&c->empty[s]);
+                commit<C::PAIR>(&c->empty[s]);
             }
-            tc::commit_elect(&c->dfull[h]);
-            if (both) tc::commit_elect(&c->dfull[1]);
+            commit<C::PAIR>(&c->dfull[h]);
+            if (both) commit<C::PAIR>(&c->dfull[1]);
             else h ^= 1;
         }
-        tc::commit_elect(&c->fin);   // every MMA issued here is done before TMEM is freed
+        commit<C::PAIR>(&c->fin);   // every MMA issued here is done before TMEM is freed
         wait_warp(&c->fin, 0, c, a.err);
+    } else if (C::PAIR && warp == 1) {
+        // ---------------- the peer's scales: one word a stage to the leader ------------------
+        // The warps that wrote the scales have made them visible to the tensor unit (the async proxy)
+        // before they arrived here; the word goes out as a commit of no operations, which costs
+        // the warp little.  (An ordinary arrival with release at cluster scope took about 1500
+        // cycles a stage from here, 2000 from the warps that load the scales.)
+        if (a.early) pdl_wait();
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok && !stopped(c); t += tstep)
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                const uint32_t s = it % C::STAGES;
+                if (!(ok = wait_warp(&c->sfull[s], (it / C::STAGES) & 1, c, a.err))) break;
+                commit_leader(&c->full[s]);
+            }
     } else if (warp >= 4 && warp < 4 + C::EPI) {
         // ---------------- epilogue: 32 lanes, 16 columns at a time; two warps take turns ----
         if (a.early) pdl_wait();
@@ -601,8 +722,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         uint32_t nt = 0, h = 0, red_parity = 0, parity = 0;   // parity: bit i of half i's next wait
         bool ok = true;
         for (int t = tile0; t < total && ok && !stopped(c); t += tstep, ++nt) {
-            const Tile q = get_tile(a, c, t);
-            const int m = q.m0 + qd * 32 + lane;
+            const Tile q = get_tile<C>(a, c, t);
+            const int m = q.m0 + lane0 + qd * 32 + lane;
             const bool both = C::both_halves(q.np);
             if (both) h = 0;
             const uint32_t mine = both ? 3u : 1u << h;   // the tile's halves
@@ -660,6 +781,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->dempty[mine >> 1]);
             } else {
+                // the accumulators go back to the pair's leader once this warp has read its part
+                const auto give_back = [&] {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0 && (mine & 1u)) arrive_cluster_relaxed(map_rank(smem_u32(&c->dempty[0]), 0));
+                    if (lane == 0 && (mine & 2u)) arrive_cluster_relaxed(map_rank(smem_u32(&c->dempty[1]), 0));
+                };
+                if (part * 16 >= q.np) give_back();
                 for (int c0 = part * 16; c0 < q.np; c0 += 4 * C::EPI) {
                     uint32_t v[2][16];
 #pragma unroll
@@ -673,13 +802,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                             asm volatile("" : "+r"(v[o][j]));   // read after the wait
                             f[o][j] = __uint_as_float(v[o][j]);
                         }
+                    if (c0 + 4 * C::EPI >= q.np) give_back();
                     emit16<MODE>(a, f[0], f[C::NA - 1], m, lane,
-                                   [&](int j) { return c0 + j < q.n ? q.row0 + c0 + j : -1; });
+                                 [&](int j) { return c0 + j < q.n ? q.row0 + c0 + j : -1; });
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0 && (mine & 1u)) mbar_arrive(&c->dempty[0]);
-                if (lane == 0 && (mine & 2u)) mbar_arrive(&c->dempty[1]);
             }
         }
     } else if (C::MX && warp >= C::SF_WARP) {
@@ -702,8 +828,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 lt += tstep;
                 lk = kc0;
                 if (lt < total) {
-                    const Tile q = get_tile(a, c, lt);
-                    lrow = u < C::NA ? (long long)q.e * a.M + q.m0 : (long long)q.row0 + (u - C::NA) * 128;
+                    const Tile q = get_tile<C>(a, c, lt);
+                    lrow = u < C::NA ? (long long)q.e * a.M + q.m0 + lane0 : (long long)q.row0 + (u - C::NA) * 128;
                 }
             }
             if (lt < total) {
@@ -731,7 +857,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 dst[32] = make_uint4(odd ? now[0].w : now[0].y, odd ? now[1].w : now[1].y, odd ? now[2].w : now[2].y, odd ? now[3].w : now[3].y);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c->full[s]);
+                if (lane == 0) mbar_arrive(C::PAIR ? &c->sfull[s] : &c->full[s]);
             }
             if (C::FEW && i > 0) load();
             if (++kc == kc1) kc = kc0;
@@ -741,11 +867,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     if (a.early) pdl_wait();   // a CTA without tiles too: this grid ends after the one before it
     tc::fence_before_sync();
     __syncthreads();
+    // no CTA of a cluster frees its TMEM or leaves while another may still use its memory
+    if (CS > 1) cluster_sync();
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, C::TMEM_COLS);
+        tmem_dealloc<C::PAIR>(tmem, C::TMEM_COLS);
     }
-    if (C::FEW && S > 1) cluster_sync();   // no rank leaves while another may still write to it
 }
 
 // Clusters of `size` CTAs of this kernel that the current device holds at once (0 if unknown); a
@@ -799,7 +926,7 @@ template <Mode MODE, int BN, bool WHOLE>
 cudaError_t launch(const Args &a, const Maps &m, int grid, cudaStream_t st)
 {
     using C = Cfg<MODE, BN>;
-    return launch_kernel(gemm_kernel<MODE, BN, WHOLE>, dim3(grid), dim3(C::THREADS), C::SMEM, st, a.split, a, m);
+    return launch_kernel(gemm_kernel<MODE, BN, WHOLE>, dim3(grid), dim3(C::THREADS), C::SMEM, st, C::PAIR ? 2 : a.split, a, m);
 }
 
 }  // namespace gemm

@@ -10,43 +10,67 @@ namespace {
 
 using namespace gemm;
 
-// e2m1 x e2m1 with ue8m0 scales, fp32 sums, both operands reduction-major, 128 lanes
-constexpr uint32_t kIdescMx = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(kM >> 4) << 24);
+// e2m1 x e2m1 with ue8m0 scales, fp32 sums, both operands reduction-major (without the lanes)
+constexpr uint32_t kIdescMx = (1u << 7) | (1u << 10) | (1u << 23);
+
+// Few rows a group take tiles of 32 columns on one SM: more stages in flight, two CTAs an SM, and
+// a cluster a tile while tiles are fewer than SMs.  Microseconds of a product, few columns and many,
+// by rows a group: 6144 x 6144 8: 8.8, 11.0; 24: 11.4, 11.1; 32 groups of 6144 x 2048 8: 38, 43;
+// 24: 40, 44; 48: 55, 45.
+bool few_rows(int rows, int E) { return rows <= 24 * std::min(E, rows); }
+constexpr int kFew = 32, kMany = 224;
 
 cudaError_t code_maps(Maps &m, const uint8_t *a0, const uint8_t *a1, long long arows, const uint8_t *b, int rows, int K,
-                      int widest)
+                      bool few)
 {
     cudaError_t e = rows_map(&m.a[0], a0, 8, K / 2, K / 2, arows, kM);
     if (e == cudaSuccess && a1) e = rows_map(&m.a[1], a1, 8, K / 2, K / 2, arows, kM);
-    for (int k = 0; 16 * (k + 1) <= widest && e == cudaSuccess; ++k)
+    for (int k = 0; 16 * (k + 1) <= (few ? kFew : kMany / 2) && e == cudaSuccess; ++k)
         e = rows_map(&m.b[k], b, 8, K / 2, K / 2, rows, 16 * (k + 1));
     return e;
 }
 
-// Few rows a group take tiles of 32 columns: more stages in flight, and a cluster a tile while
-// tiles are fewer than SMs.
-bool few_rows(int rows, int E) { return rows <= 24 * std::min(E, rows); }
-constexpr int kFew = 32, kMany = 192;
-
 template <Mode MODE, bool WHOLE>
-cudaError_t run_as(Args &a, const Maps &m, cudaStream_t st)
+cudaError_t run_as(Args &a, const Maps &m, bool few, cudaStream_t st)
 {
-    const int sms = num_sms();
-    const int mtiles = (a.M + kM - 1) / kM, used = std::min(a.E, a.rows);
-    const int widest = few_rows(a.rows, a.E) ? kFew : kMany;
-    a.split = widest == kFew ? choose_split<MODE, kFew, WHOLE>((long long)mtiles * used, a.ksteps) : 1;
-    a.width = a.split > 1 ? kSplitCols : widest;
-    // at most this many tiles: every group's last chunk may be short
-    const long long tiles = (long long)mtiles * std::min<long long>(a.rows, (a.rows + a.width - 1) / a.width + used);
-    if (widest == kFew)
-        return launch<MODE, kFew, WHOLE>(a, m, (int)std::min<long long>(tiles, 2 * sms / a.split) * a.split, st);
-    return launch<MODE, kMany, WHOLE>(a, m, (int)std::min<long long>(tiles, sms), st);
+    const int sms = num_sms(), used = std::min(a.E, a.rows);
+    // a bound on the tiles: every group's last chunk may be short
+    const auto tiles = [&](int mtiles) {
+        return (long long)mtiles * std::min<long long>(a.rows, (a.rows + a.width - 1) / a.width + used);
+    };
+    if (few) {
+        const int mtiles = (a.M + kM - 1) / kM;
+        a.idesc |= (uint32_t)(kM >> 4) << 24;
+        a.split = choose_split<MODE, kFew, WHOLE>((long long)mtiles * used, a.ksteps);
+        a.width = a.split > 1 ? kSplitCols : kFew;
+        return launch<MODE, kFew, WHOLE>(a, m, (int)std::min<long long>(tiles(mtiles), 2 * sms / a.split) * a.split, st);
+    }
+    const int mtiles = (a.M + 2 * kM - 1) / (2 * kM), pairs = sms / 2;
+    a.idesc |= (uint32_t)(2 * kM >> 4) << 24;
+    a.split = 1;
+    a.width = kMany;
+    if (a.E == 1) {
+        // one group: the chunk width whose waves of pairs take least (a stage costs the pipe
+        // 2 cycles a column and sum, or what L2 feeds: 50 bytes a cycle; a tile 1500 more)
+        double best = 0;
+        for (int w = kMany; w >= 32; w -= 32) {
+            const long long t = (long long)mtiles * ((a.rows + w - 1) / w);
+            const int na = MODE == kMxGate ? 2 : 1;
+            const double stage = std::max(2.0 * na * w, (16384.0 * na + 64.0 * w) / 50);
+            const double cost = (double)((t + pairs - 1) / pairs) * (a.ksteps * stage + 1500);
+            if (best == 0 || cost < best) {
+                best = cost;
+                a.width = w;
+            }
+        }
+    }
+    return launch<MODE, kMany, WHOLE>(a, m, 2 * (int)std::min<long long>(tiles(mtiles), pairs), st);
 }
 
 template <Mode MODE>
-cudaError_t run(Args &a, const Maps &m, cudaStream_t st)
+cudaError_t run(Args &a, const Maps &m, bool few, cudaStream_t st)
 {
-    return a.sf_ld % 16 ? run_as<MODE, false>(a, m, st) : run_as<MODE, true>(a, m, st);
+    return a.sf_ld % 16 ? run_as<MODE, false>(a, m, few, st) : run_as<MODE, true>(a, m, few, st);
 }
 
 }  // namespace
@@ -56,7 +80,8 @@ cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, c
                                 cudaStream_t st)
 {
     Maps m;
-    const cudaError_t e = code_maps(m, w, nullptr, (long long)E * N, x, rows, K, few_rows(rows, E) ? kFew : kMany);
+    const bool few = few_rows(rows, E);
+    const cudaError_t e = code_maps(m, w, nullptr, (long long)E * N, x, rows, K, few);
     if (e != cudaSuccess) return e;
     Args a = {};
     a.offsets = offsets;
@@ -74,7 +99,7 @@ cudaError_t launch_mxfp4_matmul(const uint8_t *x, const uint8_t *xs, int rows, c
     a.idesc = kIdescMx;
     a.early = early;
     a.err = err;
-    return run<kMxMul>(a, m, st);
+    return run<kMxMul>(a, m, few, st);
 }
 
 cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, const uint8_t *wg, const uint8_t *sg,
@@ -83,7 +108,8 @@ cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, 
                                  cudaStream_t st)
 {
     Maps m;
-    const cudaError_t e = code_maps(m, wg, wu, (long long)E * F, x, rows, K, few_rows(rows, E) ? kFew : kMany);
+    const bool few = few_rows(rows, E);
+    const cudaError_t e = code_maps(m, wg, wu, (long long)E * F, x, rows, K, few);
     if (e != cudaSuccess) return e;
     Args a = {};
     a.offsets = offsets;
@@ -102,7 +128,7 @@ cudaError_t launch_mxfp4_gate_up(const uint8_t *x, const uint8_t *xs, int rows, 
     a.idesc = kIdescMx;
     a.early = early;
     a.err = err;
-    return run<kMxGate>(a, m, st);
+    return run<kMxGate>(a, m, few, st);
 }
 
 }  // namespace moe
