@@ -9,7 +9,7 @@
 // into an SM; that form stood at 1.28 PFLOP/s.  A pair works on 256 x 256, each SM holding its
 // 128 rows and half of the columns' operand: 32 KB in and out.
 //
-// A thread of the epilogue holds consecutive columns of one output row, so that it writes 16
+// A thread of the epilogue holds consecutive columns of one output row, so that it writes 32
 // bytes at a time with no exchange between lanes.
 //
 // Tiles: 256 rows x `width` columns (a multiple of 32, chosen by the host so that the tiles
@@ -52,6 +52,7 @@ struct Args {
     int ksteps, kphase;      // stages of 64; kDx: stages of the first phase
     void *out[3];            // (h, g, u) | dx | (dWg, dWu)
     int dtype;
+    int wide;                // rows and outputs lie on 32-byte boundaries
     uint32_t idesc;          // without N
     int32_t *err;
 };
@@ -128,9 +129,20 @@ __device__ __forceinline__ uint4 pack8(const float *v, int dtype)
     return o;
 }
 
-__device__ __forceinline__ void put8(void *out, size_t at, const float *v, int dtype)
+// 16 columns of a row, those below `n`: one 32-byte store where rows allow it (a whole sector a
+// lane: 16-byte stores of 32 rows each are as many requests), else 16 bytes at a time
+__device__ __forceinline__ void put16(void *out, size_t at, const float *v, int n, const Args &a)
 {
-    *reinterpret_cast<uint4 *>(static_cast<char *>(out) + at * 2) = pack8(v, dtype);
+    const uint4 lo = pack8(v, a.dtype), hi = pack8(v + 8, a.dtype);
+    char *p = static_cast<char *>(out) + at * 2;
+    if (a.wide && n >= 16) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                     "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(p) = lo;
+        if (n >= 16) *reinterpret_cast<uint4 *>(p + 16) = hi;
+    }
 }
 
 template <Mode MODE>
@@ -268,22 +280,23 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                 if (c0 + 64 >= n) give_back();
                 if (row < a.rows) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 32; j += 16) {
                         if (c0 + j >= n) break;
-                        float x[8], y[8];
+                        const int left = n - c0 - j;   // 8, or 16 and more
+                        float x[16], y[16];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[0][j + i]);
+                        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[0][j + i]);
                         if constexpr (MODE == kGate2) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(v[1][j + i]);
+                            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[1][j + i]);
                             if (a.out[1]) {
-                                put8(a.out[1], at + c0 + j, x, a.dtype);
-                                put8(a.out[2], at + c0 + j, y, a.dtype);
+                                put16(a.out[1], at + c0 + j, x, left, a);
+                                put16(a.out[2], at + c0 + j, y, left, a);
                             }
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = gemm::silu(x[i]) * y[i];
+                            for (int i = 0; i < 16; ++i) x[i] = gemm::silu(x[i]) * y[i];
                         }
-                        put8(out, at + c0 + j, x, a.dtype);
+                        put16(out, at + c0 + j, x, left, a);
                     }
                 }
             }
@@ -322,8 +335,11 @@ inline void plan(Args &a, int NB)
 }
 
 template <Mode MODE>
-cudaError_t launch(const Args &a, const Maps &m, cudaStream_t st)
+cudaError_t launch(Args a, const Maps &m, cudaStream_t st)
 {
+    uintptr_t bits = (uintptr_t)a.cols * 2;
+    for (void *p : a.out) bits |= reinterpret_cast<uintptr_t>(p);
+    a.wide = bits % 32 == 0;
     const long long tiles = (long long)a.groups * a.mtiles * a.ntiles;
     const int grid = 2 * (int)std::min<long long>(tiles, num_sms() / 2);
     return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(kThreads), Cfg<MODE>::SMEM, st, 2, a, m);
