@@ -125,7 +125,7 @@ cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu
     a.err = err;
     gemm16::plan(a, 2);
     gemm16::Maps m;
-    cudaError_t e = rows_map(&m.r[0], x, 16, H, ldx, T, gemm16::kLanes);
+    cudaError_t e = rows_map(&m.r[0], x, 16, H, ldx, T, a.rbox);
     if (e == cudaSuccess) e = rows_map(&m.c[0], wg, 16, H, H, F, a.width / 2);
     if (e == cudaSuccess) e = rows_map(&m.c[1], wu, 16, H, H, F, a.width / 2);
     return e == cudaSuccess ? gemm16::launch<gemm16::kGate2>(a, m, st) : e;
@@ -146,8 +146,8 @@ cudaError_t grad_x(const void *dg, const void *du, const void *wg, const void *w
     a.err = err;
     gemm16::plan(a, 1);
     gemm16::Maps m;
-    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, gemm16::kLanes);
-    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, gemm16::kLanes);
+    cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, a.rbox);
+    if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, a.rbox);
     if (e == cudaSuccess) e = rows_map(&m.c[0], wg, 16, H, H, F, 64);
     if (e == cudaSuccess) e = rows_map(&m.c[1], wu, 16, H, H, F, 64);
     return e == cudaSuccess ? gemm16::launch<gemm16::kDx>(a, m, st) : e;

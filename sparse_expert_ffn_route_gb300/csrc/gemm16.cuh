@@ -49,6 +49,8 @@ struct Args {
     int mtiles, ntiles;      // 256-row tiles, column chunks
     int width;               // columns of a chunk, a multiple of 32, at most 256
     int groups;              // kDw: 2 (gate, up)
+    int rbox;                // rows of the rows operand's box: 128, or what a call of fewer has (the
+                             // lanes after them hold whatever was there; none of them is stored)
     int ksteps, kphase;      // stages of 64; kDx: stages of the first phase
     void *out[3];            // (h, g, u) | dx | (dWg, dWu)
     int dtype;
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
         const bool of_rows = warp < RB;
         const int i = of_rows ? warp : warp - RB;
         const int half = a.width >> 1, boxes = cols_mn(MODE) ? (half + 63) >> 6 : C::NB;
-        const uint32_t bytes = 2u * (C::OP + boxes * (cols_mn(MODE) ? 8192u : half * 128u));
+        const uint32_t bytes = 2u * ((rows_mn(MODE) ? C::OP : a.rbox * 128) + boxes * (cols_mn(MODE) ? 8192u : half * 128u));
         const uint32_t to = r0 + (of_rows ? i * 8192 : C::OP + i * (cols_mn(MODE) ? 8192 : C::OP));
         uint32_t it = 0;
         bool ok = true;
@@ -319,6 +321,7 @@ inline void plan(Args &a, int NB)
 {
     const int pairs = num_sms() / 2;
     a.mtiles = (a.rows + 2 * kLanes - 1) / (2 * kLanes);
+    a.rbox = std::min(kLanes, (a.rows + 15) / 16 * 16);
     double best = 0;
     for (int nt = (a.cols + kMaxCols - 1) / kMaxCols; nt <= (a.cols + 31) / 32; ++nt) {
         const int w = ((a.cols + nt - 1) / nt + 31) & ~31;
