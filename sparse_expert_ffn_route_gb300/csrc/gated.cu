@@ -102,10 +102,10 @@ cudaError_t forward_few(const void *x, long long ldx, const void *wg, const void
     a.idesc = idesc16(dtype, gemm::kM, false, false);
     a.err = err;
     const int mtiles = (F + gemm::kM - 1) / gemm::kM;
-    a.split = gemm::choose_split<gemm::kGate, kFewTokens, true>(mtiles, a.ksteps);
+    a.split = gemm::choose_split<gemm::kGate, kFewTokens, true>(mtiles * ((T + gemm::kSplitCols - 1) / gemm::kSplitCols), a.ksteps);
     a.width = a.split > 1 ? gemm::kSplitCols : kFewTokens;
     const int tiles = mtiles * ((T + a.width - 1) / a.width);
-    return gemm::launch<gemm::kGate, kFewTokens, true>(a, m, std::min(tiles, 2 * num_sms() / a.split) * a.split, st);
+    return gemm::launch<gemm::kGate, kFewTokens, true>(a, m, std::min(tiles, num_sms() / a.split) * a.split, st);
 }
 
 cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,

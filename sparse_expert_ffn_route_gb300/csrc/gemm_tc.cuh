@@ -96,7 +96,7 @@ template <Mode MODE, int BN>
 struct Cfg {
     static constexpr bool MX = is_mx(MODE), GATED = is_gated(MODE);
     static constexpr int NA = GATED ? 2 : 1;               // lanes operands (accumulators) of a tile
-    static constexpr bool FEW = BN <= 32;                  // two CTAs an SM; clusters may share a tile
+    static constexpr bool FEW = BN <= 32;                  // clusters may share a tile
     static constexpr bool PAIR = !FEW;                     // two SMs a tile: 256 lanes, each half of the columns' operand
     static constexpr int LANES = PAIR ? 2 * kM : kM;       // of a tile
     static constexpr int STEP = PAIR ? 32 : 16;            // the MMA's column count is a multiple
@@ -113,12 +113,15 @@ struct Cfg {
     static constexpr int RED_BYTES = FEW ? NA * RED_COLS * kM * 4 : 0;
     static constexpr int CTRL_BYTES = 5120;                // control block and the groups' prefix
     static constexpr int STAGE = NA * A_BYTES + B_BYTES + SF_BYTES;
-    static constexpr int BUDGET = (FEW ? 115712 : 232448) - 1024 - CTRL_BYTES - RED_BYTES;
+    // Two CTAs an SM where a chain of kernels overlaps (MXFP4, few columns).  The 16-bit block is one
+    // kernel: one CTA with 5 stages in place of 2 (one token, weights from DRAM: 12.0 us, two CTAs
+    // with 2 stages each 15.7).
+    static constexpr int PER_SM = FEW && MX ? 2 : 1;
+    static constexpr int BUDGET = (PER_SM == 2 ? 115712 : 232448) - 1024 - CTRL_BYTES - RED_BYTES;
     static constexpr int STAGES = BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
     static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + CTRL_BYTES;
     static constexpr int SF_WARP = 4 + EPI;
     static constexpr int THREADS = 32 * (SF_WARP + SF_UNITS);
-    static constexpr int PER_SM = FEW ? 2 : 1;
     static constexpr int SF_COL = 2 * HALF;                // first TMEM column of the scales: 2 buffers
     static constexpr int SF_BUF = 32;                      // columns of one buffer
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
@@ -274,6 +277,8 @@ __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -597,7 +602,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (CS > 1) cluster_sync();   // every rank's barriers are ready
+    // Every rank's barriers are ready: a pair's loads need that; where ranks share a tile only the
+    // sums' exchange does, and the other warps pass the barrier at the end.
+    if (C::PAIR) cluster_sync();
+    else if (S > 1) cluster_arrive();
     const uint32_t tmem = uniform(c->tmem);
     const int total = uniform(c->tiles);
 
@@ -716,6 +724,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             }
     } else if (warp >= 4 && warp < 4 + C::EPI) {
         // ---------------- epilogue: 32 lanes, 16 columns at a time; two warps take turns ----
+        if (!C::PAIR && S > 1) cluster_wait();
         if (a.early) pdl_wait();
         const int qd = warp & 3, part = (warp - 4) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
@@ -864,6 +873,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         }
     }
 
+    if (!C::PAIR && S > 1 && !(warp >= 4 && warp < 4 + C::EPI)) cluster_wait();
     if (a.early) pdl_wait();   // a CTA without tiles too: this grid ends after the one before it
     tc::fence_before_sync();
     __syncthreads();

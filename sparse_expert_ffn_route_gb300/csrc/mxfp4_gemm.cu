@@ -41,7 +41,7 @@ cudaError_t run_as(Args &a, const Maps &m, bool few, cudaStream_t st)
     if (few) {
         const int mtiles = (a.M + kM - 1) / kM;
         a.idesc |= (uint32_t)(kM >> 4) << 24;
-        a.split = choose_split<MODE, kFew, WHOLE>((long long)mtiles * used, a.ksteps);
+        a.split = choose_split<MODE, kFew, WHOLE>(mtiles * std::min<long long>(a.rows, a.rows / kSplitCols + used), a.ksteps);
         a.width = a.split > 1 ? kSplitCols : kFew;
         return launch<MODE, kFew, WHOLE>(a, m, (int)std::min<long long>(tiles(mtiles), 2 * sms / a.split) * a.split, st);
     }
