@@ -13,10 +13,11 @@
 // bytes at a time with no exchange between lanes.
 //
 // Tiles: 256 rows x `width` columns (a multiple of 32, chosen by the host so that the tiles
-// fill whole waves of SM pairs).  Warps of each CTA: 0-3 its operand loads, one TMA box of a
-// stage each (a box costs the warp that issues it about 270 cycles beside its 1.8 a row, and
-// boxes of different warps overlap: three boxes of a stage from one warp held the stage at 700
-// cycles), 4-11 the epilogue, two for each quarter of the lanes, 12 of the leader the MMAs.  Barriers: `full` lives in
+// fill whole waves of SM pairs).  Warps of each CTA: 0-7 its operand loads, one TMA box
+// of every second stage each (a box costs the warp that issues it about 270 cycles beside its 1.8
+// a row, and boxes of different warps overlap: three boxes of a stage from one warp held the stage
+// at 700 cycles), 8-15 the epilogue, two for each quarter of the lanes, 16 of the leader the MMAs.
+// Barriers: `full` lives in
 // the leader (both CTAs' copies complete on it); `empty` and `dfull` are in both (multicast
 // commits); `dempty` in the leader (both epilogues arrive).  Waits are bounded as in gemm_tc.cuh.
 #pragma once
@@ -37,8 +38,9 @@ enum Mode { kGate2, kDx, kDw };
 
 constexpr int kLanes = 128;   // rows of a CTA (a pair: 256)
 constexpr int kMaxCols = 256;
-constexpr int kThreads = 416;
-constexpr int kWarpMma = 12;
+constexpr int kThreads = 544;
+constexpr int kBoxes = 4;                     // TMA boxes of a stage, at most
+constexpr int kWarpEpi = 2 * kBoxes, kWarpMma = 16;
 constexpr int kEpiWarps = 8;
 
 constexpr bool rows_mn(Mode m) { return m == kDw; }    // rows operand stored reduction-major
@@ -169,8 +171,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
         c->abort = 0;
         fence_mbar_init();
     }
-    pdl_wait();
-    pdl_launch_dependents();
     if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -179,17 +179,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     __syncthreads();
     cluster_sync();   // the pair's barriers and TMEM are ready
     tc::fence_after_sync();
+    pdl_wait();
+    pdl_launch_dependents();
     const uint32_t tmem = uniform(c->tmem);
     const int per_group = a.mtiles * a.ntiles, total = a.groups * per_group;
 
-    if (warp < 4) {
-        // ---------------- operands by TMA: box `warp` of every stage -------------------------
+    if (warp < kWarpEpi) {
+        // ---------------- operands by TMA: box `b` of every second stage ---------------------
         // reduction-major operands take two boxes of 64 (the second only where it is needed),
         // the others one; rows first
         constexpr int RB = rows_mn(MODE) ? 2 : 1;
         const uint32_t r0 = smem_u32(ring);
-        const bool of_rows = warp < RB;
-        const int i = of_rows ? warp : warp - RB;
+        const int b = warp % kBoxes;
+        const uint32_t turn = warp / kBoxes;
+        const bool of_rows = b < RB;
+        const int i = of_rows ? b : b - RB;
         const int half = a.width >> 1, boxes = cols_mn(MODE) ? (half + 63) >> 6 : C::NB;
         const uint32_t bytes = 2u * ((rows_mn(MODE) ? C::OP : a.rbox * 128) + boxes * (cols_mn(MODE) ? 8192u : half * 128u));
         const uint32_t to = r0 + (of_rows ? i * 8192 : C::OP + i * (cols_mn(MODE) ? 8192 : C::OP));
@@ -201,9 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                 const int m0 = mi * 2 * kLanes + rank * kLanes + (rows_mn(MODE) ? 64 * i : 0);
                 const int n0 = ni * a.width + rank * half + (cols_mn(MODE) ? 64 * i : 0);
                 for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
+                    if ((it & 1) != turn) continue;
                     const uint32_t s = it % C::STAGES;
                     if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
-                    if (warp == 0 && rank == 0) expect_tx(smem_u32(&c->full[s]), bytes);
+                    if (b == 0 && rank == 0) expect_tx(smem_u32(&c->full[s]), bytes);
                     const uint32_t bar = map_rank(smem_u32(&c->full[s]), 0);
                     const int ph = MODE == kDx && ks >= a.kphase;
                     const int k = 64 * (ph ? ks - a.kphase : ks);
@@ -247,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
         }
         commit_pair(&c->fin);   // every MMA is done before TMEM is freed
         wait_warp(&c->fin, 0, c, a.err);
-    } else if (warp >= 4 && warp < kWarpMma) {
+    } else if (warp >= kWarpEpi && warp < kWarpMma) {
         // ---------------- epilogue ----------------------------------------------------------
-        const int qd = warp & 3, part = (warp - 4) >> 2;
+        const int qd = warp & 3, part = (warp - kWarpEpi) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
         uint32_t nt = 0;
         bool ok = true;
