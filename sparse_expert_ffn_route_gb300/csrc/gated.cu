@@ -123,7 +123,7 @@ cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu
     a.dtype = dtype;
     a.idesc = idesc16(dtype, 2 * gemm16::kLanes, false, false);
     a.err = err;
-    gemm16::plan(a, 2);
+    gemm16::plan<gemm16::kGate2>(a);
     gemm16::Maps m;
     cudaError_t e = rows_map(&m.r[0], x, 16, H, ldx, T, a.rbox);
     if (e == cudaSuccess) e = rows_map(&m.c[0], wg, 16, H, H, F, a.width / 2);
@@ -144,7 +144,7 @@ cudaError_t grad_x(const void *dg, const void *du, const void *wg, const void *w
     a.dtype = dtype;
     a.idesc = idesc16(dtype, 2 * gemm16::kLanes, false, true);
     a.err = err;
-    gemm16::plan(a, 1);
+    gemm16::plan<gemm16::kDx>(a);
     gemm16::Maps m;
     cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, a.rbox);
     if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, a.rbox);
@@ -166,7 +166,7 @@ cudaError_t grad_w(const void *dg, const void *du, const void *x, long long ldx,
     a.dtype = dtype;
     a.idesc = idesc16(dtype, 2 * gemm16::kLanes, true, true);
     a.err = err;
-    gemm16::plan(a, 1);
+    gemm16::plan<gemm16::kDw>(a);
     gemm16::Maps m;
     cudaError_t e = rows_map(&m.r[0], dg, 16, F, F, T, 64);
     if (e == cudaSuccess) e = rows_map(&m.r[1], du, 16, F, F, T, 64);

@@ -55,6 +55,9 @@ struct Args {
                              // lanes after them hold whatever was there; none of them is stored)
     int ksteps, kphase;      // stages of 64; kDx: stages of the first phase
     void *out[3];            // (h, g, u) | dx | (dWg, dWu)
+    int stages, stage_bytes; // of the ring: a tile of few rows and columns has more and smaller ones
+    int rows_bytes;          // the rows operand's part of a stage
+    int cols_bytes;          // one columns operand's
     int dtype;
     int wide;                // rows and outputs lie on 32-byte boundaries
     uint32_t idesc;          // without N
@@ -70,14 +73,14 @@ template <Mode MODE>
 struct Cfg {
     static constexpr int NB = MODE == kGate2 ? 2 : 1;
     static constexpr int NBUF = MODE == kGate2 ? 1 : 2;
-    static constexpr int OP = kLanes * 128;                 // bytes of one operand's part in a CTA
-    static constexpr int STAGE = (1 + NB) * OP;
-    static constexpr int STAGES = MODE == kGate2 ? 4 : 6;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + 512;
 };
 
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 13 * 16384;   // the MMA reads 16 KB from a stage's rows, however few they are
+constexpr int kSmemBytes = 1024 + kRingBytes + 512;
+
 struct Ctrl {
-    uint64_t full[6], empty[6], dfull[2], dempty[2], fin;
+    uint64_t full[kMaxStages], empty[kMaxStages], dfull[2], dempty[2], fin;
     uint32_t tmem;
     int abort;
 };
@@ -155,20 +158,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     using C = Cfg<MODE>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    Ctrl *c = reinterpret_cast<Ctrl *>(ring + C::STAGES * C::STAGE);
+    Ctrl *c = reinterpret_cast<Ctrl *>(ring + kRingBytes);
+    static_assert(sizeof(Ctrl) <= 512, "control block");
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    if (tid == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&c->full[i], 1);
-            mbar_init(&c->empty[i], 1);
+    if (tid < 32) {
+        if (tid < kMaxStages) {
+            mbar_init(&c->full[tid], 1);
+            mbar_init(&c->empty[tid], 1);
+        } else if (tid < kMaxStages + 2) {
+            mbar_init(&c->dfull[tid - kMaxStages], 1);
+            mbar_init(&c->dempty[tid - kMaxStages], 2 * kEpiWarps);
+        } else if (tid == 31) {
+            mbar_init(&c->fin, 1);
+            c->abort = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c->dfull[i], 1);
-            mbar_init(&c->dempty[i], 2 * kEpiWarps);
-        }
-        mbar_init(&c->fin, 1);
-        c->abort = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -195,19 +199,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
         const bool of_rows = b < RB;
         const int i = of_rows ? b : b - RB;
         const int half = a.width >> 1, boxes = cols_mn(MODE) ? (half + 63) >> 6 : C::NB;
-        const uint32_t bytes = 2u * ((rows_mn(MODE) ? C::OP : a.rbox * 128) + boxes * (cols_mn(MODE) ? 8192u : half * 128u));
-        const uint32_t to = r0 + (of_rows ? i * 8192 : C::OP + i * (cols_mn(MODE) ? 8192 : C::OP));
-        uint32_t it = 0;
+        const uint32_t bytes = 2u * ((rows_mn(MODE) ? 16384u : a.rbox * 128u) + boxes * (cols_mn(MODE) ? 8192u : half * 128u));
+        const uint32_t to = r0 + (of_rows ? i * 8192 : a.rows_bytes + i * (cols_mn(MODE) ? 8192 : a.cols_bytes));
+        uint32_t it = 0, s = 0, phase = 0;   // stage, and the ring's turn
         bool ok = true;
         if (of_rows || i < boxes)
             for (int t = pair; t < total && ok && !stopped(c); t += pairs) {
                 const int g = t / per_group, mi = (t - g * per_group) / a.ntiles, ni = t - g * per_group - mi * a.ntiles;
                 const int m0 = mi * 2 * kLanes + rank * kLanes + (rows_mn(MODE) ? 64 * i : 0);
                 const int n0 = ni * a.width + rank * half + (cols_mn(MODE) ? 64 * i : 0);
-                for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
+                for (int ks = 0; ks < a.ksteps; ++ks, ++it, s = s + 1 == a.stages ? 0 : s + 1, phase ^= s == 0) {
                     if ((it & 1) != turn) continue;
-                    const uint32_t s = it % C::STAGES;
-                    if (it >= C::STAGES && !(ok = wait_warp(&c->empty[s], ((it / C::STAGES) - 1) & 1, c, a.err))) break;
+                    if (it >= a.stages && !(ok = wait_warp(&c->empty[s], phase ^ 1, c, a.err))) break;
                     if (b == 0 && rank == 0) expect_tx(smem_u32(&c->full[s]), bytes);
                     const uint32_t bar = map_rank(smem_u32(&c->full[s]), 0);
                     const int ph = MODE == kDx && ks >= a.kphase;
@@ -215,34 +218,33 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                     const CUtensorMap *map = of_rows ? &maps.r[MODE == kDw ? g : ph] : &maps.c[MODE == kGate2 ? i : ph];
                     const int o = of_rows ? m0 : n0;
                     const bool mn = of_rows ? rows_mn(MODE) : cols_mn(MODE);
-                    tma_2d_pair(to + s * C::STAGE, map, mn ? o : k, mn ? k : o, bar);
+                    tma_2d_pair(to + s * a.stage_bytes, map, mn ? o : k, mn ? k : o, bar);
                 }
             }
         // copies still in flight (after a wait that gave up) land before the pair ends
         if (warp == 0 && rank == 0)
-            for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+            for (uint32_t j = it > (uint32_t)a.stages ? it - a.stages : 0; j < it; ++j)
+                mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1);
         __syncwarp();
     } else if (warp == kWarpMma && rank == 0) {
         // ---------------- MMA issue, for both CTAs ------------------------------------------
         const uint32_t r0 = smem_u32(ring);
-        uint32_t it = 0, nt = 0;
+        uint32_t s = 0, phase = 0, nt = 0;
         bool ok = true;
         for (int t = pair; t < total && ok && !stopped(c); t += pairs, ++nt) {
             const uint32_t idesc = a.idesc | (uint32_t)(a.width >> 3) << 17;
             const uint32_t buf = nt % C::NBUF, use = nt / C::NBUF;
             if (use >= 1 && !(ok = wait_warp(&c->dempty[buf], (use - 1) & 1, c, a.err))) break;
-            for (int ks = 0; ks < a.ksteps; ++ks, ++it) {
-                const uint32_t s = it % C::STAGES;
-                if (!(ok = wait_warp(&c->full[s], (it / C::STAGES) & 1, c, a.err))) break;
+            for (int ks = 0; ks < a.ksteps; ++ks, s = s + 1 == a.stages ? 0 : s + 1, phase ^= s == 0) {
+                if (!(ok = wait_warp(&c->full[s], phase, c, a.err))) break;
                 tc::fence_after_sync();
-                const uint32_t rs = r0 + s * C::STAGE, cs = rs + C::OP;
+                const uint32_t rs = r0 + s * a.stage_bytes, cs = rs + a.rows_bytes;
                 const uint64_t rd = rows_mn(MODE) ? sdesc_mn_sw128(rs) : tc::sdesc_kmajor_sw128(rs);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int o = 0; o < C::NB; ++o) {
-                        const uint64_t cd = cols_mn(MODE) ? sdesc_mn_sw128(cs) : tc::sdesc_kmajor_sw128(cs + o * C::OP);
+                        const uint64_t cd = cols_mn(MODE) ? sdesc_mn_sw128(cs) : tc::sdesc_kmajor_sw128(cs + o * a.cols_bytes);
                         mma_pair(tmem + buf * kMaxCols + o * kMaxCols, rd + (rows_mn(MODE) ? k * 128 : k * 2),
                                  cd + (cols_mn(MODE) ? k * 128 : k * 2), idesc, ks > 0 || k > 0);
                     }
@@ -322,8 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
 // Column chunks: the count whose waves of SM pairs take least, by what a tile costs in cycles:
 // its reduction at the tensor pipe's rate or at the 50 bytes a cycle that reach an SM from L2,
 // whichever is more, and a fixed start and end.
-inline void plan(Args &a, int NB)
+template <Mode MODE>
+void plan(Args &a)
 {
+    constexpr int NB = Cfg<MODE>::NB;
     const int pairs = num_sms() / 2;
     a.mtiles = (a.rows + 2 * kLanes - 1) / (2 * kLanes);
     a.rbox = std::min(kLanes, (a.rows + 15) / 16 * 16);
@@ -340,6 +344,11 @@ inline void plan(Args &a, int NB)
         }
     }
     a.ntiles = (a.cols + a.width - 1) / a.width;
+    const int boxes = (a.width / 2 + 63) / 64;
+    a.rows_bytes = MODE == kDw ? 16384 : a.rbox * 128;
+    a.cols_bytes = cols_mn(MODE) ? boxes * 8192 : a.width / 2 * 128;
+    a.stage_bytes = a.rows_bytes + NB * a.cols_bytes;
+    a.stages = std::min(kMaxStages, (kRingBytes - 16384) / a.stage_bytes);
 }
 
 template <Mode MODE>
@@ -350,7 +359,7 @@ cudaError_t launch(Args a, const Maps &m, cudaStream_t st)
     a.wide = bits % 32 == 0;
     const long long tiles = (long long)a.groups * a.mtiles * a.ntiles;
     const int grid = 2 * (int)std::min<long long>(tiles, num_sms() / 2);
-    return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(kThreads), Cfg<MODE>::SMEM, st, 2, a, m);
+    return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, 2, a, m);
 }
 
 }  // namespace gemm16
