@@ -342,12 +342,13 @@ def moe_stage_times(reset: bool = True):
 
 # --- MXFP4 and the 16-bit gated block ----------------------------------------------------
 # These check what the C entry points cannot see: types, shapes and strides of the tensors.
-def _raw_stream(stream=None) -> int:
-    """The stream handle, without the Stream object that torch.cuda.current_stream makes (2.9 us
-    against 0.1 us a call on the host, where a one-token call takes 5)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The handle of `stream`, or of the current stream of t's device, without the Stream object that
+    torch.cuda.current_stream makes (2.9 us against 0.1 us a call, where a one-token call takes 5)."""
+    return _current_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
@@ -365,44 +366,51 @@ def _dense(t: torch.Tensor, name: str, shape, dtype) -> int:
     if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
         return t.data_ptr()
     raise ValueError("%s must be a contiguous CUDA tensor %s of %s (got %s of %s%s)" % (
-        name, shape, dtype, tuple(t.shape), t.dtype, "" if t.is_contiguous() else ", strided"))
+        name, tuple(shape), dtype, tuple(t.shape), t.dtype, "" if t.is_contiguous() else ", strided"))
 
 
 def _rows(t: torch.Tensor, name: str):
     """(rows, width, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda:
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
         raise ValueError("%s must be a 2-D CUDA tensor" % name)
-    rows, width = t.shape
+    rows, width = shape
+    if t.is_contiguous():
+        return rows, width, width
     if width > 1 and t.stride(1) != 1:
         raise ValueError("rows of %s must be contiguous" % name)
-    return rows, width, (t.stride(0) if rows > 1 else width)
+    return rows, width, t.stride(0)
 
 
 def moe_quantize_mxfp4(x, codes, scales, stream=None):
     """Rows x [rows][K] (float32, bfloat16 or float16; K a multiple of 32, rows may be strided)
     -> MXFP4: codes [rows][K/2] uint8 and scales [rows][K/32] uint8.  A contiguous x of more
     dimensions is taken as its rows laid end to end."""
-    if x.dim() != 2 and x.is_contiguous() and x.dim() > 0:
-        K = x.shape[-1]
-        x = x.view(-1, K)
+    if len(x.shape) > 2 and x.is_contiguous():
+        x = x.view(-1, x.shape[-1])
         codes, scales = codes.view(-1, codes.shape[-1]), scales.view(-1, scales.shape[-1])
     rows, K, ld = _rows(x, "x")
-    _check(load_library().moe_quantize_mxfp4(
+    rc = load_library().moe_quantize_mxfp4(
         x.data_ptr(), _dtype(x, "x"), ld, rows, K, _dense(codes, "codes", (rows, K // 2), torch.uint8),
-        _dense(scales, "scales", (rows, K // 32), torch.uint8), _raw_stream(stream)), "moe_quantize_mxfp4")
+        _dense(scales, "scales", (rows, K // 32), torch.uint8), _raw_stream(stream, x))
+    if rc:
+        _check(rc, "moe_quantize_mxfp4")
 
 
 def moe_dequantize_mxfp4(codes, scales, y, stream=None):
     """The values that MXFP4 codes [..][K/2] and scales [..][K/32] stand for, into y [..][K]."""
-    if y.dim() == 2:
-        rows, K = y.shape
+    shape = y.shape
+    if len(shape) == 2:
+        rows, K = shape
         c, sc = (rows, K // 2), (rows, K // 32)
     else:
-        K, lead = y.shape[-1], tuple(y.shape[:-1])
+        K, lead = shape[-1], tuple(shape[:-1])
         rows, c, sc = (y.numel() // K if K else 0), lead + (K // 2,), lead + (K // 32,)
-    _check(load_library().moe_dequantize_mxfp4(
+    rc = load_library().moe_dequantize_mxfp4(
         _dense(codes, "codes", c, torch.uint8), _dense(scales, "scales", sc, torch.uint8), rows, K,
-        _dense(y, "y", y.shape, y.dtype), _dtype(y, "y"), _raw_stream(stream)), "moe_dequantize_mxfp4")
+        _dense(y, "y", shape, y.dtype), _dtype(y, "y"), _raw_stream(stream, y))
+    if rc:
+        _check(rc, "moe_dequantize_mxfp4")
 
 
 def alloc_mxfp4_matmul_workspace(device="cuda") -> torch.Tensor:
@@ -425,7 +433,7 @@ def moe_mxfp4_matmul(x, x_scales, w, w_scales, y, workspace, offsets=None, strea
         _dense(x, "x", (rows, half), u8), _dense(x_scales, "x_scales", (rows, K32), u8), rows, pw, psw, groups,
         None if offsets is None else _dense(offsets, "offsets", (groups + 1,), torch.int32), N, 2 * half,
         _dense(y, "y", (rows, N), y.dtype), _dtype(y, "y"), workspace.data_ptr(), workspace.numel(),
-        _raw_stream(stream)), "moe_mxfp4_matmul")
+        _raw_stream(stream, x)), "moe_mxfp4_matmul")
 
 
 def moe_mxfp4_workspace_size(cfg: MoeConfig, max_tokens: int) -> int:
@@ -461,7 +469,7 @@ def moe_mxfp4_expert_ffn(cfg, x, weights: Dict[str, torch.Tensor], y_pairs, work
         None if offsets is None else _dense(offsets, "offsets", (E + 1,), torch.int32),
         None if tok is None else _dense(tok, "tok", (P,), torch.int32),
         _dense(y_pairs, "y_pairs", (P, H), y_pairs.dtype), _dtype(y_pairs, "y_pairs"),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(stream)), "moe_mxfp4_expert_ffn")
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x)), "moe_mxfp4_expert_ffn")
 
 
 def moe_gated_workspace_size(T: int, H: int, F: int, train: bool) -> int:
@@ -487,7 +495,7 @@ def moe_gated_forward(x, w_gate, w_up, h, workspace, g=None, u=None, stream=None
         x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt), _dense(w_up, "w_up", (F, H), dt),
         _dtype(x, "x"), T, H, F, _dense(h, "h", (T, F), dt),
         None if g is None else _dense(g, "g", (T, F), dt), None if u is None else _dense(u, "u", (T, F), dt),
-        _ptr(workspace), workspace.numel(), _raw_stream(stream)), "moe_gated_forward")
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x)), "moe_gated_forward")
 
 
 def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace, stream=None):
@@ -500,5 +508,5 @@ def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace,
         _dense(dh, "dh", (T, F), dt), x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt),
         _dense(w_up, "w_up", (F, H), dt), _dense(g, "g", (T, F), dt), _dense(u, "u", (T, F), dt),
         _dtype(x, "x"), T, H, F, opt(dx, "dx", (T, H)), opt(dw_gate, "dw_gate", (F, H)),
-        opt(dw_up, "dw_up", (F, H)), _ptr(workspace), workspace.numel(), _raw_stream(stream)),
-        "moe_gated_backward")
+        opt(dw_up, "dw_up", (F, H)), workspace.data_ptr(), workspace.numel(),
+        _raw_stream(stream, x)), "moe_gated_backward")
