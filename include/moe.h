@@ -234,6 +234,8 @@ int moe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, long long 
  *   out of order or past the rows is skipped and recorded (moe_check_errors).
  *   1 <= groups <= 512, 1 <= N <= 2^20, groups * N <= 2^27.
  *   workspace: 256 bytes (the error word), zeroed once before its first use.
+ *   Scales are read in aligned 16-byte pieces: an array whose size is not a multiple
+ *   of 16 must be readable up to the next one (cudaMalloc'ed memory is).
  * A NaN block (scale 255) makes the outputs that read it NaN and no others. */
 int moe_mxfp4_matmul(const uint8_t *x, const uint8_t *x_scales, int rows, const uint8_t *w,
                      const uint8_t *w_scales, int groups, const int32_t *offsets, int N, int K,
@@ -248,6 +250,7 @@ int moe_mxfp4_matmul(const uint8_t *x, const uint8_t *x_scales, int rows, const 
  *   offsets, tok as moe_permute writes them; both NULL (n_experts = top_k = 1)
  *   runs every token through the one expert: a shared expert or a dense layer.
  *   A token index outside [0, T) makes its pair NaN and is recorded.
+ *   Scales are read as moe_mxfp4_matmul reads them.
  *   workspace: moe_mxfp4_workspace_size(cfg, T) bytes, first 256 zeroed once. */
 int moe_mxfp4_expert_ffn(const moe_config *cfg, const void *x, int x_dtype, int T,
                          const moe_expert_mxfp4 *w, const int32_t *offsets, const int32_t *tok,

@@ -494,27 +494,58 @@ __device__ __forceinline__ void emit1(const Args &a, float g, float u, int m, in
 }
 
 // 16 scale bytes (blocks 16 kc .. 16 kc + 15) of a row of K / 32; past the end: 0 (2^-127, on
-// codes that are zero there).  WHOLE: K is a multiple of 512, every row's 16 are one aligned load;
-// a kernel of its own, since the other form's code beside it cost one-token calls a microsecond.
+// codes that are zero there).  load() only starts the loads, get() uses them, so that a chunk's
+// loads run beside the stores of the one before.
 template <bool WHOLE>
-__device__ __forceinline__ uint4 load_scales(const uint8_t *base, long long row, long long rows, int ld, int kc)
-{
-    if (row >= rows) return make_uint4(0, 0, 0, 0);
-    const uint8_t *p = base + row * ld + 16 * kc;
-    if constexpr (WHOLE) return __ldg(reinterpret_cast<const uint4 *>(p));
-    const int left = min(16, ld - 16 * kc);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if ((ld & 3) == 0) {   // K a multiple of 128: whole words
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (4 * i < left) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < left) w[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+struct Scales;
+
+// K is a multiple of 512: every row's 16 bytes are one aligned load.  A kernel of its own, since the
+// other form's code beside it cost one-token calls a microsecond.
+template <>
+struct Scales<true> {
+    uint4 v;
+    __device__ __forceinline__ void load(const uint8_t *base, long long row, long long rows, int ld, int kc)
+    {
+        v = make_uint4(0, 0, 0, 0);
+        if (row < rows) v = __ldg(reinterpret_cast<const uint4 *>(base + row * ld + 16 * kc));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
+    __device__ __forceinline__ uint4 get() const { return v; }
+};
+
+// Otherwise the two aligned 16 bytes around them, shifted into place (2000 x 4000 x 2528 in 20 us;
+// byte loads 35).  The last row's may pass the array's end by up to 15 bytes, never a 16-byte
+// boundary: the entry points ask for arrays that are readable up to the next one.
+template <>
+struct Scales<false> {
+    uint4 lo, hi;
+    int sh, left;   // bytes before them in lo, bytes of the row from here on
+    __device__ __forceinline__ void load(const uint8_t *base, long long row, long long rows, int ld, int kc)
+    {
+        const long long o = row * ld + 16 * kc;
+        sh = (int)o & 15;
+        left = row < rows ? ld - 16 * kc : 0;
+        lo = hi = make_uint4(0, 0, 0, 0);
+        const uint4 *p = reinterpret_cast<const uint4 *>(base + (o - sh));
+        if (left > 0) lo = __ldg(p);
+        if (sh + min(left, 16) > 16) hi = __ldg(p + 1);
+    }
+    __device__ __forceinline__ uint4 get() const
+    {
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        uint32_t x[6], y[5], r[4];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) x[i] = sh & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) y[i] = sh & 4 ? x[i + 1] : x[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r[i] = __funnelshift_r(y[i], y[i + 1], 8 * (sh & 3));
+            const int keep = left - 4 * i;   // valid bytes of this word
+            if (keep < 4) r[i] &= keep > 0 ? (1u << (8 * keep)) - 1u : 0u;
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+};
 
 template <Mode MODE, int BN, bool WHOLE>
 __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
@@ -822,7 +853,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         // Chunks of 512 inputs (16 scale bytes of a row, two stages), one ahead in registers, over
         // the tiles' ends too.  The next chunk is loaded before this one is stored where the MMAs
         // set the pace (prompt 1255 us, after: 1276), after it where the weights' stream does (decode
-        // batch 486 us, before: 502); two or four chunks ahead were slower in both.
+        // batch 486 us, before: 502), but for rows off the 16-byte grid, which have more to load
+        // (decode batch of 4160 x 1088 75 us, after: 80); two or four chunks ahead were slower.
         const int u = warp - C::SF_WARP;
         if (u >= C::NA && a.early) pdl_wait();
         const uint8_t *base = u < C::NA ? a.sfa[u] : a.sfb;
@@ -831,7 +863,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         const int chunks = tile0 < total ? (total - tile0 + tstep - 1) / tstep * (kc1 - kc0) : 0;
         int lt = tile0 - tstep, lk = kc1;   // the next load: tile, chunk
         long long lrow = 0;
-        uint4 v[4];
+        Scales<WHOLE> v[4];
         auto load = [&] {
             if (lk == kc1) {
                 lt += tstep;
@@ -843,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             }
             if (lt < total) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = load_scales<WHOLE>(base, lrow + lane + 32 * i, rows, a.sf_ld, lk);
+                for (int i = 0; i < 4; ++i) v[i].load(base, lrow + lane + 32 * i, rows, a.sf_ld, lk);
                 ++lk;
             }
         };
@@ -854,8 +886,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         for (int i = 0; i < chunks && ok; ++i) {
             uint4 now[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) now[j] = v[j];
-            if (!C::FEW || i == 0) load();
+            for (int j = 0; j < 4; ++j) now[j] = v[j].get();
+            if (!C::FEW || !WHOLE || i == 0) load();
             for (int ks = max(ks0, 2 * kc); ks < min(ks1, 2 * kc + 2); ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (a.early && it == C::STAGES) pdl_wait();
@@ -868,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(C::PAIR ? &c->sfull[s] : &c->full[s]);
             }
-            if (C::FEW && i > 0) load();
+            if (C::FEW && WHOLE && i > 0) load();
             if (++kc == kc1) kc = kc0;
         }
     }
