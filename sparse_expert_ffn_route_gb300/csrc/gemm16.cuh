@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     }
 }
 
-// Column chunks: the count whose waves of SM pairs take least, by what a tile costs in cycles:
+// Column chunks: the width whose waves of SM pairs take least, by what a tile costs in cycles:
 // its reduction at the tensor pipe's rate or at the 50 bytes a cycle that reach an SM from L2,
 // whichever is more, and a fixed start and end.
 template <Mode MODE>
@@ -332,10 +332,8 @@ void plan(Args &a)
     a.mtiles = (a.rows + 2 * kLanes - 1) / (2 * kLanes);
     a.rbox = std::min(kLanes, (a.rows + 15) / 16 * 16);
     double best = 0;
-    for (int nt = (a.cols + kMaxCols - 1) / kMaxCols; nt <= (a.cols + 31) / 32; ++nt) {
-        const int w = ((a.cols + nt - 1) / nt + 31) & ~31;
+    for (int w = kMaxCols; w >= 32; w -= 32) {
         const long long tiles = (long long)a.groups * a.mtiles * ((a.cols + w - 1) / w);
-        if (best > 0 && tiles > 8 * pairs) break;
         const double stage = std::max(2.0 * w * NB, (16384.0 + 64.0 * w * NB) / 50);
         const double cost = (double)((tiles + pairs - 1) / pairs) * (a.ksteps * stage + 3000.0 + 4.0 * w * NB);
         if (best == 0 || cost < best) {

@@ -1,7 +1,8 @@
 // gemm_tc.cuh -- the tcgen05 matrix-product kernel behind the MXFP4 operators and the 16-bit
-// gated block for few tokens.  One kernel template, three uses:
+// gated block for few tokens.  One kernel template, four uses:
 //   kMxGate   h = q(silu(x Wg^T) * (x Wu^T)), x and W in MXFP4, h requantised to MXFP4
 //   kMxMul    y = x W^T, x and W in MXFP4
+//   kMxMul2   the same on twice the weight rows a tile (two lanes operands of one matrix)
 //   kGate     h = silu(x Wg^T) * (x Wu^T) in 16 bits (g and u kept on request)
 //
 // Orientation.  The accumulator's 128 lanes are weight rows (the output's contiguous dimension)
@@ -56,14 +57,14 @@
 namespace moe {
 namespace gemm {
 
-enum Mode { kMxGate, kMxMul, kGate };
+enum Mode { kMxGate, kMxMul, kGate, kMxMul2 };
 
 constexpr int kM = 128;          // lanes of a tile
 constexpr int kBoxMaps = 7;      // column-operand maps with boxes of 16 (k + 1) rows
 constexpr int kMaxGroups = 512;
 constexpr int kSplitCols = 16;   // columns of a tile that CTAs share
 
-constexpr bool is_mx(Mode m) { return m == kMxGate || m == kMxMul; }
+constexpr bool is_mx(Mode m) { return m != kGate; }
 constexpr bool is_gated(Mode m) { return m == kMxGate || m == kGate; }
 
 // the kernel's parameters (tensor maps apart)
@@ -95,12 +96,12 @@ struct Maps {
 template <Mode MODE, int BN>
 struct Cfg {
     static constexpr bool MX = is_mx(MODE), GATED = is_gated(MODE);
-    static constexpr int NA = GATED ? 2 : 1;               // lanes operands (accumulators) of a tile
+    static constexpr int NA = GATED || MODE == kMxMul2 ? 2 : 1;   // lanes operands (accumulators) of a tile
     static constexpr bool FEW = BN <= 32;                  // clusters may share a tile
     static constexpr bool PAIR = !FEW;                     // two SMs a tile: 256 lanes, each half of the columns' operand
-    static constexpr int LANES = PAIR ? 2 * kM : kM;       // of a tile
+    static constexpr int LANES = (MODE == kMxMul2 ? 2 : 1) * (PAIR ? 2 * kM : kM);   // of a tile
     static constexpr int STEP = PAIR ? 32 : 16;            // the MMA's column count is a multiple
-    static constexpr int EPI = FEW ? 4 : MX && GATED ? 16 : 8;   // epilogue warps
+    static constexpr int EPI = FEW ? 4 : NA == 2 ? 16 : 8;   // epilogue warps
     // TMEM: two halves of accumulators.  A tile takes one half, so that its epilogue runs beside
     // the next tile's MMAs; two accumulators of more than HALF / 2 columns take both.
     static constexpr int HALF = FEW ? NA * BN : 224;
@@ -452,11 +453,15 @@ __device__ __forceinline__ void emit16(const Args &a, const float (&g)[16], cons
             emit_mx8(a, v, m, lane, [&](int j) { return col(j0 + j); });
         }
     } else {
-        if (m >= a.M) return;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int r = col(j);
-            if (r >= 0) store(a.out[0], a.dtype, (size_t)r * a.ld + m, g[j]);
+        for (int o = 0; o < (MODE == kMxMul2 ? 2 : 1); ++o) {
+            const int n = m + 2 * kM * o;
+            if (n >= a.M) return;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int r = col(j);
+                if (r >= 0) store(a.out[0], a.dtype, (size_t)r * a.ld + n, o ? u[j] : g[j]);
+            }
         }
     }
 }
@@ -652,8 +657,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             const Tile q = get_tile<C>(a, c, t);
             const int cols = C::PAIR ? q.np >> 1 : q.np;   // this CTA's
             const uint32_t bytes = (C::PAIR ? 2u : 1u) * (C::NA * C::A_BYTES + (uint32_t)cols * 128u);
-            const CUtensorMap *map = col ? &maps.b[(cols >> 4) - 1] : &maps.a[o];
-            const int y = col ? q.row0 + (C::PAIR ? rank * cols : 0) : q.e * a.M + q.m0 + lane0;
+            const CUtensorMap *map = col ? &maps.b[(cols >> 4) - 1] : &maps.a[MODE == kMxMul2 ? 0 : o];
+            const int y = col ? q.row0 + (C::PAIR ? rank * cols : 0) : q.e * a.M + q.m0 + lane0 + (MODE == kMxMul2 ? 2 * kM * o : 0);
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (a.early && it == C::STAGES) pdl_wait();
@@ -848,6 +853,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 }
             }
         }
+        // sums still in flight (after a wait that gave up) land before the cluster ends
+        if (C::FEW && S > 1 && !ok) mbar_wait(&c->rfull, red_parity);
     } else if (C::MX && warp >= C::SF_WARP) {
         // ---------------- scales: this warp's operand, 128 rows -----------------------------
         // Chunks of 512 inputs (16 scale bytes of a row, two stages), one ahead in registers, over
@@ -857,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         // (decode batch of 4160 x 1088 75 us, after: 80); two or four chunks ahead were slower.
         const int u = warp - C::SF_WARP;
         if (u >= C::NA && a.early) pdl_wait();
-        const uint8_t *base = u < C::NA ? a.sfa[u] : a.sfb;
+        const uint8_t *base = u < C::NA ? a.sfa[MODE == kMxMul2 ? 0 : u] : a.sfb;
         const long long rows = u < C::NA ? a.sfa_rows : a.rows;
         const int kc0 = ks0 >> 1, kc1 = (ks1 + 1) >> 1;
         const int chunks = tile0 < total ? (total - tile0 + tstep - 1) / tstep * (kc1 - kc0) : 0;
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 lk = kc0;
                 if (lt < total) {
                     const Tile q = get_tile<C>(a, c, lt);
-                    lrow = u < C::NA ? (long long)q.e * a.M + q.m0 + lane0 : (long long)q.row0 + (u - C::NA) * 128;
+                    lrow = u < C::NA ? (long long)q.e * a.M + q.m0 + lane0 + (MODE == kMxMul2 ? 2 * kM * u : 0) : (long long)q.row0 + (u - C::NA) * 128;
                 }
             }
             if (lt < total) {

@@ -45,26 +45,34 @@ cudaError_t run_as(Args &a, const Maps &m, bool few, cudaStream_t st)
         a.width = a.split > 1 ? kSplitCols : kFew;
         return launch<MODE, kFew, WHOLE>(a, m, (int)std::min<long long>(tiles(mtiles), 2 * sms / a.split) * a.split, st);
     }
-    const int mtiles = (a.M + 2 * kM - 1) / (2 * kM), pairs = sms / 2;
+    const int pairs = sms / 2;
     a.idesc |= (uint32_t)(2 * kM >> 4) << 24;
     a.split = 1;
     a.width = kMany;
+    int lanes = 2 * kM;
     if (a.E == 1) {
-        // one group: the chunk width whose waves of pairs take least (a stage costs the pipe
-        // 2 cycles a column and sum, or what L2 feeds: 50 bytes a cycle; a tile 1500 more)
+        // One group: the tile whose waves of pairs take least.  A stage costs the pipe 2 cycles a
+        // column and sum, or what L2 feeds: 50 bytes a cycle; a tile 1500 cycles more, and its epilogue
+        // where its sums take both halves of TMEM.  A product may hold twice the weight rows: 46 KB
+        // a stage for 896 cycles of the pipe in place of 33 KB for 448.
         double best = 0;
-        for (int w = kMany; w >= 32; w -= 32) {
-            const long long t = (long long)mtiles * ((a.rows + w - 1) / w);
-            const int na = MODE == kMxGate ? 2 : 1;
-            const double stage = std::max(2.0 * na * w, (16384.0 * na + 64.0 * w) / 50);
-            const double cost = (double)((t + pairs - 1) / pairs) * (a.ksteps * stage + 1500);
-            if (best == 0 || cost < best) {
-                best = cost;
-                a.width = w;
+        for (int two = MODE == kMxGate; two < 2; ++two)
+            for (int w = kMany; w >= 32; w -= 32) {
+                const int na = two ? 2 : 1, l = MODE == kMxMul && two ? 4 * kM : 2 * kM;
+                const long long t = (long long)((a.M + l - 1) / l) * ((a.rows + w - 1) / w);
+                const double stage = std::max(2.0 * na * w, (16384.0 * na + 64.0 * w) / 50);
+                const double cost = (double)((t + pairs - 1) / pairs) * (a.ksteps * stage + 1500 + (na * w > 224 ? 20.0 * w : 0.0));
+                if (best == 0 || cost < best) {
+                    best = cost;
+                    a.width = w;
+                    lanes = l;
+                }
             }
-        }
     }
-    return launch<MODE, kMany, WHOLE>(a, m, 2 * (int)std::min<long long>(tiles(mtiles), pairs), st);
+    const int grid = 2 * (int)std::min<long long>(tiles((a.M + lanes - 1) / lanes), pairs);
+    if constexpr (MODE == kMxMul)
+        if (lanes > 2 * kM) return launch<kMxMul2, kMany, WHOLE>(a, m, grid, st);
+    return launch<MODE, kMany, WHOLE>(a, m, grid, st);
 }
 
 template <Mode MODE>

@@ -356,3 +356,12 @@ def test_routed_layer_on_mxfp4_experts():
             e = int(ids[t, k])
             want[t] += float(wt[t, k]) * (pm.held(pm.gate(q[t:t + 1], val["gate"][e], val["up"][e])[2])[0] @ val["down"][e].T)
     assert np.linalg.norm(y.cpu().double().numpy() - want) <= 0.02 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("rows,N,K", [(300, 1500, 2048), (2048, 2100, 512), (1000, 4000, 96), (900, 513, 1120)])
+def test_matmul_large_tiles(rows, N, K):
+    """Sizes at which tiles hold 256 and 512 weight rows, with ragged last tiles of either side."""
+    rng = np.random.default_rng(rows + N)
+    _, sx, px, vx = random_mx(rng, rows, K)
+    _, sw, pw, vw = random_mx(rng, N, K)
+    check_matmul(matmul(px, sx, pw, sw, torch.bfloat16), vx, vw, torch.bfloat16)
