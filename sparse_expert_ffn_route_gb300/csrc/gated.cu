@@ -78,8 +78,13 @@ __global__ void __launch_bounds__(256)
     reinterpret_cast<uint4 *>(du)[i] = q.v;
 }
 
-// T <= kFewTokens: the weights' rows on the lanes, the tokens on the columns
-constexpr int kFewTokens = 32;
+// Few tokens take the kernel with the weights' rows on the lanes, tokens in columns of up to 32: it
+// spreads the reduction over clusters, where a pair of SMs walks all of it (about 0.17 us a 64
+// inputs); a longer list of columns and short reductions favour the pairs.  Microseconds, few and
+// pairs: 6144 x 2048, 1 token 8.0, 18.9, 64 tokens 17.1, 18.9; 2048 x 512, 1 token 4.6, 8.0, 64
+// tokens 6.9, 8.0; 1000 x 520, 1 token 4.5, 5.4, 32 tokens 5.9, 5.5; 512 x 512, 8 tokens 4.5, 4.1.
+bool few_tokens(int T, int H) { return T <= 16 ? H > 512 : T <= 64 && H >= 2048; }
+constexpr int kFewCols = 32;
 
 cudaError_t forward_few(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,
                         void *h, void *g, void *u, int32_t *err, cudaStream_t st)
@@ -87,7 +92,7 @@ cudaError_t forward_few(const void *x, long long ldx, const void *wg, const void
     gemm::Maps m;
     cudaError_t e = rows_map(&m.a[0], wg, 16, H, H, F, gemm::kM);
     if (e == cudaSuccess) e = rows_map(&m.a[1], wu, 16, H, H, F, gemm::kM);
-    for (int k = 0; 16 * (k + 1) <= kFewTokens && e == cudaSuccess; ++k) e = rows_map(&m.b[k], x, 16, H, ldx, T, 16 * (k + 1));
+    for (int k = 0; 16 * (k + 1) <= kFewCols && e == cudaSuccess; ++k) e = rows_map(&m.b[k], x, 16, H, ldx, T, 16 * (k + 1));
     if (e != cudaSuccess) return e;
     gemm::Args a = {};
     a.E = 1;
@@ -102,16 +107,16 @@ cudaError_t forward_few(const void *x, long long ldx, const void *wg, const void
     a.idesc = idesc16(dtype, gemm::kM, false, false);
     a.err = err;
     const int mtiles = (F + gemm::kM - 1) / gemm::kM;
-    a.split = gemm::choose_split<gemm::kGate, kFewTokens, true>(mtiles * ((T + gemm::kSplitCols - 1) / gemm::kSplitCols), a.ksteps);
-    a.width = a.split > 1 ? gemm::kSplitCols : kFewTokens;
+    a.split = gemm::choose_split<gemm::kGate, kFewCols, true>(mtiles * ((T + gemm::kSplitCols - 1) / gemm::kSplitCols), a.ksteps);
+    a.width = a.split > 1 ? gemm::kSplitCols : kFewCols;
     const int tiles = mtiles * ((T + a.width - 1) / a.width);
-    return gemm::launch<gemm::kGate, kFewTokens, true>(a, m, std::min(tiles, num_sms() / a.split) * a.split, st);
+    return gemm::launch<gemm::kGate, kFewCols, true>(a, m, std::min(tiles, num_sms() / a.split) * a.split, st);
 }
 
 cudaError_t forward(const void *x, long long ldx, const void *wg, const void *wu, int dtype, int T, int H, int F,
                     void *h, void *g, void *u, int32_t *err, cudaStream_t st)
 {
-    if (T <= kFewTokens) return forward_few(x, ldx, wg, wu, dtype, T, H, F, h, g, u, err, st);
+    if (few_tokens(T, H)) return forward_few(x, ldx, wg, wu, dtype, T, H, F, h, g, u, err, st);
     gemm16::Args a = {};
     a.rows = T;
     a.cols = F;

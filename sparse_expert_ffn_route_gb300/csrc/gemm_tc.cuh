@@ -956,17 +956,17 @@ int max_clusters(int size)
     return n;
 }
 
-// CTAs that share a tile when `tiles` of them would leave SMs idle.  Each keeps at least 8 stages
-// of the reduction: below that the exchange of the sums costs what the shorter stream saves
-// (one token, microseconds with 1, 2, 4, 8 CTAs a tile: 48 tiles of 8 stages 6.0, 6.6, 6.1, 10.4;
-// 16 tiles of 96 stages 32.7, 18.7, 11.7, 9.3).  All clusters run at once: the query counts one CTA
-// an SM, two fit.
+// CTAs that share a tile when `tiles` of them would leave SMs idle: each with two stages of the
+// reduction at least, with eight where a quarter of the SMs has a tile anyway (48 tiles of 8 stages
+// 5.4 us alone, 5.9 by threes; one token, microseconds with at least 8, 4, 2 stages a CTA: 16-bit block of
+// 1000 x 520 6.6, 5.1, 4.5, of 2048 x 512 5.4, 4.6, 4.6; MXFP4 product of 16 rows, 1000 x 4096 7.8,
+// 5.8, 5.1).  All clusters run at once: the query counts one CTA an SM, PER_SM fit.
 template <Mode MODE, int BN, bool WHOLE>
 int choose_split(long long tiles, int ksteps)
 {
     int best = 1;
     if (Cfg<MODE, BN>::FEW)
-        for (int s = 2; s <= 8 && 8 * s <= ksteps && s * tiles <= num_sms(); ++s)
+        for (int s = 2; s <= 8 && (4 * tiles > num_sms() ? 8 : 2) * s <= ksteps && s * tiles <= num_sms(); ++s)
             if (Cfg<MODE, BN>::PER_SM * max_clusters<MODE, BN, WHOLE>(s) >= tiles) best = s;
     return best;
 }
