@@ -265,16 +265,18 @@ size_t moe_mxfp4_workspace_size(const moe_config *cfg, int max_tokens);
  * expert ["MoE 路由与专家流式加载" §1.4, §2: dense layers before the sparse ones]:
  *   g = x w_gate^T, u = x w_up^T, h = silu(g) * u      (sums and silu in fp32)
  *   x [T][H] with ldx elements between rows, w_gate, w_up [F][H], h [T][F], all
- *   bf16 or all fp16 (dtype).  g, u [T][F]: kept for moe_gated_backward, rounded
- *   to dtype; both NULL when no gradient is wanted.
+ *   bf16 or all fp16 (dtype).  g, u: two arrays of T * F 16-bit words that keep,
+ *   together, the factors of dh of each element for moe_gated_backward (not the
+ *   values of g and u: 12 or 13 bits of each factor and a shared exponent); both
+ *   NULL when no gradient is wanted.
  *   H, F multiples of 8 in [8, 65536], T in [0, 2^24], rows of x 16-byte aligned.
  *   workspace: moe_gated_workspace_size(T, H, F, 0) bytes, first 256 zeroed once. */
 int moe_gated_forward(const void *x, long long ldx, const void *w_gate, const void *w_up, int dtype,
                       int T, int H, int F, void *h, void *g, void *u, void *workspace,
                       size_t workspace_bytes, void *stream);
 
-/* Gradients of the gated block from dh [T][F] and the g, u that the forward pass
- * kept: with s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s (rounded to
+/* Gradients of the gated block from dh [T][F] and what the forward pass kept in g
+ * and u: with s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s (rounded to
  * dtype as the products' operands),
  *   dx = dg w_gate + du w_up [T][H],  dw_gate = dg^T x, dw_up = du^T x [F][H]
  * written in full (not accumulated).  dx, or both weight gradients, may be NULL.

@@ -487,8 +487,8 @@ def alloc_gated_workspace(T: int, H: int, F: int, train: bool, device="cuda") ->
 
 
 def moe_gated_forward(x, w_gate, w_up, h, workspace, g=None, u=None, stream=None):
-    """h [T][F] = silu(x w_gate^T) * (x w_up^T), all bfloat16 or all float16; g, u [T][F] keep the
-    two products for moe_gated_backward.  Rows of x [T][H] may be strided."""
+    """h [T][F] = silu(x w_gate^T) * (x w_up^T), all bfloat16 or all float16; g, u [T][F] (of
+    the same type, as storage) keep what moe_gated_backward needs.  Rows of x [T][H] may be strided."""
     T, H, ld = _rows(x, "x")
     F, dt = w_gate.shape[0], x.dtype
     _check(load_library().moe_gated_forward(

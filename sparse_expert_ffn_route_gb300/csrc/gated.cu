@@ -5,10 +5,10 @@
 // With s = sigmoid(g):  dg = dh u s (1 + g (1 - s)),  du = dh g s,
 //   dx = dg Wg + du Wu,   dWg = dg^T x,   dWu = du^T x.
 //
-// Roundings to 16 bits besides the outputs': g and u, kept by the forward pass for the
-// backward one (their half step is the outputs' own; keeping fp32 would double what both
-// passes move), and dg and du, the operands of the tensor-core products.  Everything else is
-// fp32.
+// Of an element the forward pass keeps A = u s (1 + g (1 - s)) and B = g s for the backward one, so
+// that dg = dh A and du = dh B, in one word of 32 bits (gated_kept.cuh), its low half in `g`, its
+// high half in `u`.  The one rounding to 16 bits besides the outputs' is that of dg and du, the
+// operands of the tensor-core products.  Everything else is fp32.
 #include <algorithm>
 
 #include "gemm16.cuh"
@@ -25,36 +25,17 @@ uint32_t idesc16(int dtype, int lanes, bool a_mn, bool b_mn)
     return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(lanes >> 4) << 24);
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v)
-{
-    return __bfloat162float(v);
-}
-template <>
-__device__ __forceinline__ float to_f<__half>(__half v)
-{
-    return __half2float(v);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v)
-{
-    return __float2bfloat16_rn(v);
-}
-template <>
-__device__ __forceinline__ __half from_f<__half>(float v)
-{
-    return __float2half_rn(v);
-}
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ void set(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void set(__half &d, float v) { d = __float2half_rn(v); }
 
-// dg, du from dh, g, u, 8 values a thread (F is a multiple of 8, so the rows laid end to end are)
-template <typename T>
+// dg, du from dh and the kept words, 8 values a thread (F is a multiple of 8, so the rows laid end
+// to end are).  Bound by memory: 10 bytes a value.
+template <typename T, bool FP16>
 __global__ void __launch_bounds__(256)
-    gated_grad_kernel(const T *__restrict__ dh, const T *__restrict__ g, const T *__restrict__ u, long long units,
-                      T *__restrict__ dg, T *__restrict__ du)
+    gated_grad_kernel(const T *__restrict__ dh, const uint16_t *__restrict__ lo, const uint16_t *__restrict__ hi,
+                      long long units, T *__restrict__ dg, T *__restrict__ du)
 {
     pdl_wait();
     pdl_launch_dependents();
@@ -63,16 +44,17 @@ __global__ void __launch_bounds__(256)
     union Pack {
         uint4 v;
         T t[8];
-    } a, b, c, p, q;
+    } a, p, q;
     a.v = ld_stream_v4(reinterpret_cast<const uint4 *>(dh) + i);
-    b.v = ld_stream_v4(reinterpret_cast<const uint4 *>(g) + i);
-    c.v = ld_stream_v4(reinterpret_cast<const uint4 *>(u) + i);
+    const uint4 l4 = ld_stream_v4(reinterpret_cast<const uint4 *>(lo) + i), h4 = ld_stream_v4(reinterpret_cast<const uint4 *>(hi) + i);
+    const uint32_t l[4] = {l4.x, l4.y, l4.z, l4.w}, h[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float d = to_f(a.t[j]), gg = to_f(b.t[j]), uu = to_f(c.t[j]);
-        const float s = 1.0f / (1.0f + expf(-gg));
-        p.t[j] = from_f<T>(d * uu * s * (1.0f + gg * (1.0f - s)));
-        q.t[j] = from_f<T>(d * gg * s);
+        float A, B;
+        Kept<FP16>::unpack(__byte_perm(l[j >> 1], h[j >> 1], j & 1 ? 0x7632 : 0x5410), A, B);
+        const float d = to_f(a.t[j]);
+        set(p.t[j], d * A);
+        set(q.t[j], d * B);
     }
     reinterpret_cast<uint4 *>(dg)[i] = p.v;
     reinterpret_cast<uint4 *>(du)[i] = q.v;
@@ -282,10 +264,10 @@ int moe_gated_backward(const void *dh, const void *x, long long ldx, const void 
     const dim3 grid((unsigned)((units + 255) / 256));
     cudaError_t e =
         dtype == MOE_DTYPE_BF16
-            ? launch_kernel(gated_grad_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, 1, (const __nv_bfloat16 *)dh,
-                            (const __nv_bfloat16 *)g, (const __nv_bfloat16 *)u, units, (__nv_bfloat16 *)dg, (__nv_bfloat16 *)du)
-            : launch_kernel(gated_grad_kernel<__half>, grid, dim3(256), 0, st, 1, (const __half *)dh, (const __half *)g,
-                            (const __half *)u, units, (__half *)dg, (__half *)du);
+            ? launch_kernel(gated_grad_kernel<__nv_bfloat16, false>, grid, dim3(256), 0, st, 1, (const __nv_bfloat16 *)dh,
+                            (const uint16_t *)g, (const uint16_t *)u, units, (__nv_bfloat16 *)dg, (__nv_bfloat16 *)du)
+            : launch_kernel(gated_grad_kernel<__half, true>, grid, dim3(256), 0, st, 1, (const __half *)dh, (const uint16_t *)g,
+                            (const uint16_t *)u, units, (__half *)dg, (__half *)du);
     if (e == cudaSuccess && dx) e = grad_x(dg, du, w_gate, w_up, dtype, T, H, F, dx, err, st);
     if (e == cudaSuccess && dw_gate) e = grad_w(dg, du, x, ldx, dtype, T, H, F, dw_gate, dw_up, err, st);
     return done(e, "gated backward launch");

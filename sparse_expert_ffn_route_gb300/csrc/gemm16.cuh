@@ -54,7 +54,7 @@ struct Args {
     int rbox;                // rows of the rows operand's box: 128, or what a call of fewer has (the
                              // lanes after them hold whatever was there; none of them is stored)
     int ksteps, kphase;      // stages of 64; kDx: stages of the first phase
-    void *out[3];            // (h, g, u) | dx | (dWg, dWu)
+    void *out[3];            // (h, kept low, high halves) | dx | (dWg, dWu)
     int stages, stage_bytes; // of the ring: a tile of few rows and columns has more and smaller ones
     int rows_bytes;          // the rows operand's part of a stage
     int cols_bytes;          // one columns operand's
@@ -118,37 +118,50 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// 8 consecutive columns -> 16 bytes
-__device__ __forceinline__ uint4 pack8(const float *v, int dtype)
+// two consecutive columns
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int dtype)
 {
-    uint4 o;
-    uint32_t *w = &o.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (dtype == MOE_DTYPE_BF16) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&p);
-        } else {
-            const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&p);
-        }
+    if (dtype == MOE_DTYPE_BF16) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
     }
-    return o;
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// 16 columns of a row, those below `n`: one 32-byte store where rows allow it (a whole sector a
-// lane: 16-byte stores of 32 rows each are as many requests), else 16 bytes at a time
-__device__ __forceinline__ void put16(void *out, size_t at, const float *v, int n, const Args &a)
+// 16 columns of a row (32 bytes), those below `n`: one 32-byte store where rows allow it (a whole
+// sector a lane: 16-byte stores of 32 rows each are as many requests), else 16 bytes at a time
+__device__ __forceinline__ void put32(void *out, size_t at, const uint32_t (&w)[8], int n, const Args &a)
 {
-    const uint4 lo = pack8(v, a.dtype), hi = pack8(v + 8, a.dtype);
     char *p = static_cast<char *>(out) + at * 2;
     if (a.wide && n >= 16) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
-                     "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
     } else {
-        *reinterpret_cast<uint4 *>(p) = lo;
-        if (n >= 16) *reinterpret_cast<uint4 *>(p + 16) = hi;
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (n >= 16) *reinterpret_cast<uint4 *>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// h and the kept words of 16 columns
+template <bool FP16>
+__device__ __forceinline__ void put_gated(const float (&g)[16], const float (&u)[16], size_t at, int n, const Args &a)
+{
+    uint32_t h[8], lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float A[2], B[2];
+        const float h0 = gated(g[2 * i], u[2 * i], A[0], B[0]), h1 = gated(g[2 * i + 1], u[2 * i + 1], A[1], B[1]);
+        h[i] = pack2(h0, h1, a.dtype);
+        const uint32_t w0 = Kept<FP16>::pack(A[0], B[0]), w1 = Kept<FP16>::pack(A[1], B[1]);
+        lo[i] = __byte_perm(w0, w1, 0x5410);
+        hi[i] = __byte_perm(w0, w1, 0x7632);
+    }
+    put32(a.out[0], at, h, n, a);
+    if (a.out[1]) {
+        put32(a.out[1], at, lo, n, a);
+        put32(a.out[2], at, hi, n, a);
     }
 }
 
@@ -292,20 +305,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                     for (int j = 0; j < 32; j += 16) {
                         if (c0 + j >= n) break;
                         const int left = n - c0 - j;   // 8, or 16 and more
-                        float x[16], y[16];
+                        float x[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[0][j + i]);
                         if constexpr (MODE == kGate2) {
+                            float y[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[1][j + i]);
-                            if (a.out[1]) {
-                                put16(a.out[1], at + c0 + j, x, left, a);
-                                put16(a.out[2], at + c0 + j, y, left, a);
-                            }
+                            if (a.dtype == MOE_DTYPE_F16) put_gated<true>(x, y, at + c0 + j, left, a);
+                            else put_gated<false>(x, y, at + c0 + j, left, a);
+                        } else {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] = gemm::silu(x[i]) * y[i];
+                            for (int i = 0; i < 8; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1], a.dtype);
+                            put32(out, at + c0 + j, w, left, a);
                         }
-                        put16(out, at + c0 + j, x, left, a);
                     }
                 }
             }

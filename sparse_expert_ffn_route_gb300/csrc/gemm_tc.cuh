@@ -3,7 +3,7 @@
 //   kMxGate   h = q(silu(x Wg^T) * (x Wu^T)), x and W in MXFP4, h requantised to MXFP4
 //   kMxMul    y = x W^T, x and W in MXFP4
 //   kMxMul2   the same on twice the weight rows a tile (two lanes operands of one matrix)
-//   kGate     h = silu(x Wg^T) * (x Wu^T) in 16 bits (g and u kept on request)
+//   kGate     h = silu(x Wg^T) * (x Wu^T) in 16 bits (its factors kept on request)
 //
 // Orientation.  The accumulator's 128 lanes are weight rows (the output's contiguous dimension)
 // and its columns tokens.  A weight tile is then always a full 128-lane operand, however few tokens there
@@ -49,6 +49,7 @@
 #include <atomic>
 
 #include "device_util.cuh"
+#include "gated_kept.cuh"
 #include "launch.cuh"
 #include "moe_internal.cuh"
 #include "mx_util.cuh"
@@ -81,7 +82,7 @@ struct Args {
     const uint8_t *sfa[2], *sfb;
     int sf_ld;                 // K / 32
     long long sfa_rows;        // E * M
-    void *out[3];              // y | (h, g, u) | (codes, scales)
+    void *out[3];              // y | (h, kept low, high halves) | (codes, scales)
     int ld;                    // row stride of out, in elements (codes: of M)
     int dtype;                 // MOE_DTYPE_* of out
     uint32_t idesc;            // instruction descriptor without N and the scale ids
@@ -487,10 +488,12 @@ __device__ __forceinline__ void emit1(const Args &a, float g, float u, int m, in
     } else if (m < a.M) {
         const size_t at = (size_t)r * a.ld + m;
         if constexpr (MODE == kGate) {
-            store(a.out[0], a.dtype, at, silu(g) * u);
+            float A, B;
+            store(a.out[0], a.dtype, at, gated(g, u, A, B));
             if (a.out[1]) {
-                store(a.out[1], a.dtype, at, g);
-                store(a.out[2], a.dtype, at, u);
+                const uint32_t w = a.dtype == MOE_DTYPE_F16 ? Kept<true>::pack(A, B) : Kept<false>::pack(A, B);
+                static_cast<uint16_t *>(a.out[1])[at] = (uint16_t)w;
+                static_cast<uint16_t *>(a.out[2])[at] = (uint16_t)(w >> 16);
             }
         } else {
             store(a.out[0], a.dtype, at, g);

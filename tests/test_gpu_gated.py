@@ -40,11 +40,10 @@ def subnormal(dtype):
 @pytest.mark.parametrize("T,H,F", SIZES)
 def test_forward(dtype, T, H, F):
     x, wg, wu, _ = make(T, H, F, dtype)
-    h, g, u = (f64(t) for t in forward(x.cuda(), wg.cuda(), wu.cuda()))
-    G, U, Hh, eh, eg, eu = pm.gate(f64(x), f64(wg), f64(wu))
+    h = f64(forward(x.cuda(), wg.cuda(), wu.cuda())[0])
+    _, _, want, bound, _, _ = pm.gate(f64(x), f64(wg), f64(wu))
     r, z = pm.HALF_STEP[dtype], subnormal(dtype)
-    for got, want, bound in ((h, Hh, eh), (g, G, eg), (u, U, eu)):
-        assert (np.abs(got - want) <= bound + r * (np.abs(want) + bound) + z).all()
+    assert (np.abs(h - want) <= bound + r * (np.abs(want) + bound) + z).all()
     h2 = f64(forward(x.cuda(), wg.cuda(), wu.cuda(), keep=False)[0])
     assert (h2 == h).all()
 
@@ -59,22 +58,34 @@ def backward(dh, x, wg, wu, g, u):
     return out
 
 
+# what one kept factor is off by at most, relative to the larger of the element's two, and absolutely
+KEPT = {torch.bfloat16: 1 / 2047, torch.float16: 1 / 5792}
+KEPT_LEAST = {torch.bfloat16: 2.0 ** -103 * 2 / 2047, torch.float16: 2.0 ** -13 * 2 / 5792}
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,H,F", SIZES)
 def test_backward(dtype, T, H, F):
-    """From the kept (rounded) g and u, taken as inputs: dg and du carry 10 fp32 roundings and one
-    to the type, the products fp32 sums, the gradients one rounding."""
+    """The factors A = u s (1 + g (1 - s)) and B = g s of fp32 sums, 10 fp32 roundings and the kept
+    form's step; dg and du one rounding to the type, the products fp32 sums, the gradients one
+    rounding."""
     x, wg, wu, dh = make(T, H, F, dtype)
     _, g, u = forward(x.cuda(), wg.cuda(), wu.cuda())
     dx, dwg, dwu = (f64(t) for t in backward(dh.cuda(), x.cuda(), wg.cuda(), wu.cuda(), g, u))
-    X, WG, WU, DH, G, U = (f64(t) for t in (x, wg, wu, dh, g, u))
+    X, WG, WU, DH = (f64(t) for t in (x, wg, wu, dh))
+    G, U, _, _, eg, eu = pm.gate(X, WG, WU)
     s = pm.sigmoid(G)
     r, z = pm.HALF_STEP[dtype], subnormal(dtype)
-    dg, du = DH * U * s * (1 + G * (1 - s)), DH * G * s
+    A, B = U * s * (1 + G * (1 - s)), G * s
     e32 = 10 * 2.0 ** -24
-    # 1 + g (1 - s) is a sum: its roundings are relative to its terms
-    edg = np.abs(DH * U) * s * (1 + np.abs(G) * (1 + s)) * e32 + r * np.abs(dg) + z
-    edu = (e32 + r) * np.abs(du) + z
+    # |silu'| <= 1.1 and |silu''| <= 0.5; 1 + g (1 - s) is a sum: its roundings are relative to its terms
+    kept = KEPT[dtype] * np.maximum(np.abs(A), np.abs(B)) + KEPT_LEAST[dtype]
+    eA = 1.1 * eu + 0.5 * (np.abs(U) + eu) * eg + e32 * np.abs(U) * s * (1 + np.abs(G) * (1 + s))
+    eB = 1.1 * eg + e32 * np.abs(B)
+    eA, eB = eA + kept + KEPT[dtype] * (eA + eB), eB + kept + KEPT[dtype] * (eA + eB)
+    dg, du = DH * A, DH * B
+    edg = np.abs(DH) * eA * (1 + r) + r * np.abs(dg) + z
+    edu = np.abs(DH) * eB * (1 + r) + r * np.abs(du) + z
 
     def check(got, pairs):
         want = sum(a @ b for a, b, _ in pairs)
@@ -106,11 +117,16 @@ def test_gradient_against_differences():
         d[at] = a
         e = 1e-5
         want = (loss(X + e * d[0], WG + e * d[1], WU + e * d[2]) - loss(X - e * d[0], WG - e * d[1], WU - e * d[2])) / (2 * e)
-        # five roundings to fp16 (g, u, dg or du, the operands' products, the gradient), each at most
+        # two roundings to fp16 (dg or du, the gradient) and the kept factors' step, each at most
         # half a step of its value: sum over the entries in the worst case is far above; in the
         # mean of n independent entries it is the norm's
         bound = 5 * pm.HALF_STEP[torch.float16] * np.linalg.norm(grad) * 6 + 1e-6 * abs(want)
         assert abs((grad * a).sum() - want) <= bound
+
+
+def same(a, b):
+    """The same bits (what the forward pass keeps is words, not numbers of the type)."""
+    return all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(a, b))
 
 
 def test_strided_rows_of_x():
@@ -119,9 +135,9 @@ def test_strided_rows_of_x():
     wide[:, 24:152] = x
     part = wide[:, 24:152]
     a, b = forward(x, wg, wu), forward(part, wg, wu)
-    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert same(a, b)
     ga, gb = backward(dh, x, wg, wu, a[1], a[2]), backward(dh, part, wg, wu, a[1], a[2])
-    assert all(torch.equal(p, q) for p, q in zip(ga, gb))
+    assert same(ga, gb)
 
 
 def test_each_gradient_alone_and_repeats():
@@ -151,7 +167,7 @@ def test_saturated_gates_and_infinities():
     x, wg, wu, dh = make(T, H, F, torch.bfloat16)
     big = (x * 200).cuda()
     h, g, u = forward(big, wg.cuda(), wu.cuda())
-    assert torch.isfinite(h).all() and g.float().abs().max() > 200
+    assert torch.isfinite(h).all()
     out = backward(dh.cuda(), big, wg.cuda(), wu.cuda(), g, u)
     assert all(torch.isfinite(t).all() for t in out)
     x[3, 5] = float("inf")
@@ -175,4 +191,39 @@ def test_step_in_a_graph():
         graph.replay()
     torch.cuda.synchronize()
     moe.moe_check_errors(ws)
-    assert all(torch.equal(p, q) for p, q in zip(want + grads, b + o))
+    assert same(want + grads, b + o)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [0.0, 1e-6, 1e-3, 1.0, 30.0])
+def test_kept_factors_over_the_range(dtype, scale):
+    """One input and identity-like weights: g and u are chosen freely, dh = 1, x' = 1, so that dwg and
+    dwu are the rounded factors themselves, down to the least kept step and at zero."""
+    F = 256
+    rng = np.random.default_rng(17)
+    x = torch.zeros(1, 8, dtype=dtype)
+    x[0, 0] = 1
+    wg, wu = torch.zeros(F, 8, dtype=dtype), torch.zeros(F, 8, dtype=dtype)
+    wg[:, 0] = torch.from_numpy(rng.standard_normal(F) * min(scale, 5.0)).to(dtype)
+    wu[:, 0] = torch.from_numpy(rng.standard_normal(F) * scale * 10.0 ** rng.uniform(-3, 0, F)).to(dtype)
+    dh = torch.ones(1, F, dtype=dtype)
+    _, g, u = forward(x.cuda(), wg.cuda(), wu.cuda())
+    _, dwg, dwu = (f64(t) for t in backward(dh.cuda(), x.cuda(), wg.cuda(), wu.cuda(), g, u))
+    G, U = f64(wg)[:, 0], f64(wu)[:, 0]
+    s = pm.sigmoid(G)
+    A, B = U * s * (1 + G * (1 - s)), G * s
+    kept = KEPT[dtype] * np.maximum(np.abs(A), np.abs(B)) + KEPT_LEAST[dtype] + 10 * 2.0 ** -24 * np.maximum(np.abs(U), np.abs(G)) * (1 + np.abs(G))
+    r, z = pm.HALF_STEP[dtype], subnormal(dtype)
+    for got, want in ((dwg[:, 0], A), (dwu[:, 0], B)):
+        # the rounding to dg or du, then the gradient's (of a value that the type holds: none)
+        assert (np.abs(got - want) <= kept * (1 + r) + r * np.abs(want) + z).all()
+
+
+def test_factors_that_are_not_finite():
+    """An infinite g or u makes its row's dg and du NaN and no other row's."""
+    x, wg, wu, dh = make(40, 64, 64, torch.bfloat16)
+    x[3, 5] = float("inf")
+    _, g, u = forward(x.cuda(), wg.cuda(), wu.cuda())
+    dx = backward(dh.cuda(), x.cuda(), wg.cuda(), wu.cuda(), g, u)[0]
+    rows = torch.isfinite(dx).all(1)
+    assert not rows[3] and rows.sum() == 39
