@@ -16,7 +16,8 @@
 // fill whole waves of SM pairs).  Warps of each CTA: 0-7 its operand loads, one TMA box
 // of every second stage each (a box costs the warp that issues it about 270 cycles beside its 1.8
 // a row, and boxes of different warps overlap: three boxes of a stage from one warp held the stage
-// at 700 cycles), 8-15 the epilogue, two for each quarter of the lanes, 16 of the leader the MMAs.
+// at 700 cycles), then the epilogue, two or four for each quarter of the lanes, then one that issues
+// the leader's MMAs.
 // Barriers: `full` lives in
 // the leader (both CTAs' copies complete on it); `empty` and `dfull` are in both (multicast
 // commits); `dempty` in the leader (both epilogues arrive).  Waits are bounded as in gemm_tc.cuh.
@@ -38,10 +39,8 @@ enum Mode { kGate2, kDx, kDw };
 
 constexpr int kLanes = 128;   // rows of a CTA (a pair: 256)
 constexpr int kMaxCols = 256;
-constexpr int kThreads = 544;
 constexpr int kBoxes = 4;                     // TMA boxes of a stage, at most
-constexpr int kWarpEpi = 2 * kBoxes, kWarpMma = 16;
-constexpr int kEpiWarps = 8;
+constexpr int kWarpEpi = 2 * kBoxes;
 
 constexpr bool rows_mn(Mode m) { return m == kDw; }    // rows operand stored reduction-major
 constexpr bool cols_mn(Mode m) { return m != kGate2; }
@@ -73,6 +72,13 @@ template <Mode MODE>
 struct Cfg {
     static constexpr int NB = MODE == kGate2 ? 2 : 1;
     static constexpr int NBUF = MODE == kGate2 ? 1 : 2;
+    // Epilogue warps, and columns that one reads at a time.  The gate's two sums fill TMEM, so no MMA
+    // runs beside its epilogue: twice the warps on half the columns each (4096 x 6144 x 2048 with
+    // what it keeps 122.6 us, with eight warps 128.4).
+    static constexpr int EPI = MODE == kGate2 ? 16 : 8;
+    static constexpr int READ = MODE == kGate2 ? 16 : 32;
+    static constexpr int MMA_WARP = kWarpEpi + EPI;
+    static constexpr int THREADS = 32 * (MMA_WARP + 1);
 };
 
 constexpr int kMaxStages = 16;
@@ -118,6 +124,9 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tc::ld16(taddr, v); }
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tc::ld32(taddr, v); }
+
 // two consecutive columns
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, int dtype)
 {
@@ -144,11 +153,18 @@ __device__ __forceinline__ void put32(void *out, size_t at, const uint32_t (&w)[
     }
 }
 
-// h and the kept words of 16 columns
+// h, and the kept words where they are asked for, of 16 columns
 template <bool FP16>
 __device__ __forceinline__ void put_gated(const float (&g)[16], const float (&u)[16], size_t at, int n, const Args &a)
 {
-    uint32_t h[8], lo[8], hi[8];
+    uint32_t h[8];
+    if (!a.out[1]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = pack2(gemm::silu(g[2 * i]) * u[2 * i], gemm::silu(g[2 * i + 1]) * u[2 * i + 1], a.dtype);
+        put32(a.out[0], at, h, n, a);
+        return;
+    }
+    uint32_t lo[8], hi[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float A[2], B[2];
@@ -159,14 +175,12 @@ __device__ __forceinline__ void put_gated(const float (&g)[16], const float (&u)
         hi[i] = __byte_perm(w0, w1, 0x7632);
     }
     put32(a.out[0], at, h, n, a);
-    if (a.out[1]) {
-        put32(a.out[1], at, lo, n, a);
-        put32(a.out[2], at, hi, n, a);
-    }
+    put32(a.out[1], at, lo, n, a);
+    put32(a.out[2], at, hi, n, a);
 }
 
 template <Mode MODE>
-__global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
+__global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
     using C = Cfg<MODE>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -181,14 +195,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
             mbar_init(&c->empty[tid], 1);
         } else if (tid < kMaxStages + 2) {
             mbar_init(&c->dfull[tid - kMaxStages], 1);
-            mbar_init(&c->dempty[tid - kMaxStages], 2 * kEpiWarps);
+            mbar_init(&c->dempty[tid - kMaxStages], 2 * C::EPI);
         } else if (tid == 31) {
             mbar_init(&c->fin, 1);
             c->abort = 0;
         }
         fence_mbar_init();
     }
-    if (warp == kWarpMma) {
+    if (warp == C::MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -239,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
             for (uint32_t j = it > (uint32_t)a.stages ? it - a.stages : 0; j < it; ++j)
                 mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1);
         __syncwarp();
-    } else if (warp == kWarpMma && rank == 0) {
+    } else if (warp == C::MMA_WARP && rank == 0) {
         // ---------------- MMA issue, for both CTAs ------------------------------------------
         const uint32_t r0 = smem_u32(ring);
         uint32_t s = 0, phase = 0, nt = 0;
@@ -267,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
         }
         commit_pair(&c->fin);   // every MMA is done before TMEM is freed
         wait_warp(&c->fin, 0, c, a.err);
-    } else if (warp >= kWarpEpi && warp < kWarpMma) {
+    } else if (warp >= kWarpEpi && warp < C::MMA_WARP) {
         // ---------------- epilogue ----------------------------------------------------------
         const int qd = warp & 3, part = (warp - kWarpEpi) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
@@ -287,22 +301,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) gemm::arrive_cluster_relaxed(map_rank(smem_u32(&c->dempty[buf]), 0));
             };
-            if (part * 32 >= n) give_back();
-            // 32 columns at a time, alternately to the two warps of these lanes; the width is a
+            if (part * C::READ >= n) give_back();
+            // READ columns at a time, in turns of the warps of these lanes; the width is a
             // multiple of 32, the columns of 8
-            for (int c0 = part * 32; c0 < n; c0 += 64) {
-                uint32_t v[2][32];
+            for (int c0 = part * C::READ; c0 < n; c0 += C::EPI / 4 * C::READ) {
+                uint32_t v[2][C::READ];
 #pragma unroll
-                for (int o = 0; o < C::NB; ++o) tc::ld32(tl + buf * kMaxCols + o * kMaxCols + c0, v[o]);
+                for (int o = 0; o < C::NB; ++o) ld_cols(tl + buf * kMaxCols + o * kMaxCols + c0, v[o]);
                 tc::wait_ld();
 #pragma unroll
                 for (int o = 0; o < C::NB; ++o)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[o][j]));   // read after the wait
-                if (c0 + 64 >= n) give_back();
+                    for (int j = 0; j < C::READ; ++j) asm volatile("" : "+r"(v[o][j]));   // read after the wait
+                if (c0 + C::EPI / 4 * C::READ >= n) give_back();
                 if (row < a.rows) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 16) {
+                    for (int j = 0; j < C::READ; j += 16) {
                         if (c0 + j >= n) break;
                         const int left = n - c0 - j;   // 8, or 16 and more
                         float x[16];
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm16_kernel(const __grid_consta
     tc::fence_before_sync();
     __syncthreads();
     cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
-    if (warp == kWarpMma) {
+    if (warp == C::MMA_WARP) {
         tc::fence_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -371,7 +385,7 @@ cudaError_t launch(Args a, const Maps &m, cudaStream_t st)
     a.wide = bits % 32 == 0;
     const long long tiles = (long long)a.groups * a.mtiles * a.ntiles;
     const int grid = 2 * (int)std::min<long long>(tiles, num_sms() / 2);
-    return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, 2, a, m);
+    return launch_kernel(gemm16_kernel<MODE>, dim3(grid), dim3(Cfg<MODE>::THREADS), kSmemBytes, st, 2, a, m);
 }
 
 }  // namespace gemm16
