@@ -410,20 +410,21 @@ __device__ __forceinline__ void store(void *p, int dtype, size_t i, float v)
 template <class Col>
 __device__ __forceinline__ void emit_mx8(const Args &a, const float (&v)[8], int m, int lane, Col col)
 {
-    uint32_t w = 0, mine = 0;
+    // (of a block with a NaN or an infinity the codes do not matter: its scale is NaN)
+    uint32_t w = 0, sbs[2] = {0, 0};   // the columns' scale bytes, the same in all lanes
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         float s[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint32_t bits = __float_as_uint(v[j + k]) & 0x7fffffffu;
             float f;
-            const uint32_t sb = mx_scale(__reduce_max_sync(0xffffffffu, bits), f);
-            s[k] = f == 0.0f ? 0.0f : v[j + k] * f;
-            if ((lane & 7) == j + k) mine = sb;
+            const uint32_t sb = mx_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j + k]) & 0x7fffffffu), f);
+            s[k] = v[j + k] * f;
+            sbs[j >> 2] |= sb << (8 * ((j + k) & 3));
         }
         w |= e2m1x2(s[0], s[1]) << (4 * j);
     }
+    const uint32_t mine = (lane & 4 ? sbs[1] : sbs[0]) >> (8 * (lane & 3));
     // lane 8a + i holds column j's nibble of row 8a + i at nibble j: transpose within 8 lanes,
     // so that lane 8a + j holds rows 8a .. 8a + 7 of column j
 #pragma unroll
