@@ -865,7 +865,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
         // the tiles' ends too.  The next chunk is loaded before this one is stored where the MMAs
         // set the pace (prompt 1255 us, after: 1276), after it where the weights' stream does (decode
         // batch 486 us, before: 502), but for rows off the 16-byte grid, which have more to load
-        // (decode batch of 4160 x 1088 75 us, after: 80); two or four chunks ahead were slower.
+        // (decode batch of 4160 x 1088 75 us, after: 80).  Further ahead is slower (prompt block 969 us,
+        // two chunks 980, four 1133): the fence before the arrival waits for a warp's loads in flight.
         const int u = warp - C::SF_WARP;
         if (u >= C::NA && a.early) pdl_wait();
         const uint8_t *base = u < C::NA ? a.sfa[MODE == kMxMul2 ? 0 : u] : a.sfb;
