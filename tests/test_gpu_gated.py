@@ -9,7 +9,8 @@ import sparse_expert_ffn_route_gb300 as moe
 pytestmark = pytest.mark.gpu
 TYPES = [torch.bfloat16, torch.float16]
 SIZES = [(1, 64, 64), (1, 1000, 520), (2, 8, 8), (16, 256, 136), (32, 6144, 256), (33, 264, 128), (70, 136, 1000),
-         (256, 128, 256), (300, 520, 264), (513, 72, 328)]
+         (256, 128, 256), (300, 520, 264), (513, 72, 328), (50, 2048, 136), (17, 1032, 72),
+         (64, 2056, 392)]
 
 
 def make(T, H, F, dtype, seed=0):
