@@ -201,14 +201,12 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
             c->abort = 0;
         }
         fence_mbar_init();
+        __syncwarp();
     }
-    if (warp == C::MMA_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
+    cluster_sync();   // both CTAs run and their barriers are ready
+    if (warp == C::MMA_WARP) gemm::tmem_alloc<true>(&c->tmem, 512);
     tc::fence_before_sync();
-    __syncthreads();
-    cluster_sync();   // the pair's barriers and TMEM are ready
+    __syncthreads();   // (a stage is full only with the peer's copies, which follow its own allocation)
     tc::fence_after_sync();
     pdl_wait();
     pdl_launch_dependents();
@@ -345,8 +343,10 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
     cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
     if (warp == C::MMA_WARP) {
         tc::fence_after_sync();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        gemm::tmem_dealloc<true>(tmem, 512);
+        __syncwarp();
     }
+    cluster_sync();
 }
 
 // Column chunks: the width whose waves of SM pairs take least, by what a tile costs in cycles:

@@ -346,6 +346,9 @@ __device__ __forceinline__ void commit(uint64_t *bar)
     else tc::commit_elect(bar);
 }
 
+// TMEM of a CTA, or of both CTAs of a pair.  The pair's forms are issued by a warp of each CTA, and
+// neither may issue while the other CTA has not started or has ended: a cluster barrier of all
+// threads stands before the allocation and one after the freeing.
 template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols)
 {
@@ -592,10 +595,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             c->abort = 0;
         }
         fence_mbar_init();
+        __syncwarp();
     }
-    if (warp == 1) {
-        tmem_alloc<C::PAIR>(&c->tmem, C::TMEM_COLS);
-    }
+    if constexpr (C::PAIR) cluster_sync();   // both CTAs run and their barriers are ready
+    if (warp == 1) tmem_alloc<C::PAIR>(&c->tmem, C::TMEM_COLS);
     if (!a.early) pdl_wait();
     pdl_launch_dependents();
     // tiles before each group: thread e (in rounds of the block) has group e, a scan within each
@@ -642,10 +645,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    // Every rank's barriers are ready: a pair's loads need that; where ranks share a tile only the
-    // sums' exchange does, and the other warps pass the barrier at the end.
-    if (C::PAIR) cluster_sync();
-    else if (S > 1) cluster_arrive();
+    // Where ranks share a tile only the sums' exchange needs the others' barriers ready; the other
+    // warps pass the cluster's barrier at the end.  (A pair's is behind it, and its stages are full only
+    // with the peer's copies, which follow the peer's allocation.)
+    if (!C::PAIR && S > 1) cluster_arrive();
     const uint32_t tmem = uniform(c->tmem);
     const int total = uniform(c->tiles);
 
@@ -926,7 +929,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     if (warp == 1) {
         tc::fence_after_sync();
         tmem_dealloc<C::PAIR>(tmem, C::TMEM_COLS);
+        __syncwarp();
     }
+    if (C::PAIR) cluster_sync();
 }
 
 // Clusters of `size` CTAs of this kernel that the current device holds at once (0 if unknown); a
