@@ -246,10 +246,17 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
                     tma_2d_pair(to + s * a.stage_bytes, map, mn ? o : k, mn ? k : o, bar);
                 }
             }
-        // copies still in flight (after a wait that gave up) land before the pair ends
-        if (warp == 0 && rank == 0)
-            for (uint32_t j = it > (uint32_t)a.stages ? it - a.stages : 0; j < it; ++j)
-                mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1);
+        if (b == 0) {
+            // the leader's commits on the last stages' `empty`, which no load waits for, land before
+            // this CTA ends and its shared memory is another kernel's (each warp waits for its own
+            // stages: it has seen the phase before)
+            const uint32_t j0 = it > (uint32_t)a.stages ? it - a.stages : 0;
+            for (uint32_t j = j0; j < it && ok; ++j)
+                if ((j & 1) == turn) ok = wait_warp(&c->empty[j % a.stages], (j / a.stages) & 1, c, a.err);
+            // after a wait that gave up: so do the copies still in flight
+            if (!ok && rank == 0)
+                for (uint32_t j = j0; j < it; ++j) mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1);
+        }
         __syncwarp();
     } else if (warp == C::MMA_WARP && rank == 0) {
         // ---------------- MMA issue, for both CTAs ------------------------------------------
@@ -340,6 +347,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
 
     tc::fence_before_sync();
     __syncthreads();
+    if (warp == C::MMA_WARP && rank == 1) wait_warp(&c->fin, 0, c, a.err);   // the leader's last commit, here too
     cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
     if (warp == C::MMA_WARP) {
         tc::fence_after_sync();

@@ -676,11 +676,17 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 else tma_2d(dst, map, ks * (C::MX ? 128 : 64), y, bar);
             }
         }
-        // copies still in flight (after a wait that gave up) land before the CTA ends
         if (a.early) pdl_wait();
-        if (warp == 0 && (!C::PAIR || rank == 0))
-            for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+        if (warp == 0) {
+            const uint32_t j0 = it > (uint32_t)C::STAGES ? it - C::STAGES : 0;
+            // a pair: the leader's commits on the last stages' `empty`, which no load waits for, land
+            // before this CTA ends and its shared memory is another kernel's
+            for (uint32_t j = j0; C::PAIR && j < it && ok; ++j)
+                ok = wait_warp(&c->empty[j % C::STAGES], (j / C::STAGES) & 1, c, a.err);
+            // copies still in flight (after a wait that gave up) land before the CTA ends
+            if ((!C::PAIR || !ok) && (!C::PAIR || rank == 0))
+                for (uint32_t j = j0; j < it; ++j) mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+        }
         __syncwarp();
     } else if (warp == 1 && !(C::PAIR && rank == 1)) {
         // ---------------- MMA issue ---------------------------------------------------------
@@ -924,6 +930,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     if (a.early) pdl_wait();   // a CTA without tiles too: this grid ends after the one before it
     tc::fence_before_sync();
     __syncthreads();
+    if (C::PAIR && rank == 1 && warp == 1) wait_warp(&c->fin, 0, c, a.err);   // the leader's last commit, here too
     // no CTA of a cluster frees its TMEM or leaves while another may still use its memory
     if (CS > 1) cluster_sync();
     if (warp == 1) {
