@@ -291,13 +291,14 @@ int moe_gated_backward(const void *dh, const void *x, long long ldx, const void 
  * for sizes outside the limits. */
 size_t moe_gated_workspace_size(int T, int H, int F, int train);
 
-/* Diagnostic of the error path of the kernels' bounded device-side waits:
- * one CTA polls, `polls` times (1 .. 2^24), an mbarrier that nothing arrives
- * at, gives up and records the timeout in the workspace's error word exactly
- * as the tcgen05 pipeline's waits do.  Nothing faults or hangs; the next
- * moe_check_errors on the workspace returns MOE_ERR_TIMEOUT and clears the
- * word.  workspace: any workspace of the library (>= 256 bytes, 256-byte
- * aligned).  Asynchronous on stream. */
+/* Diagnostic of the error path of the kernels' bounded device-side waits: a
+ * pair of CTAs waits on mbarriers that nothing arrives at.  One warp polls
+ * `polls` times (1 .. 2^24), gives up, records the timeout in the workspace's
+ * error word exactly as the tcgen05 pipeline's waits do, and tells the others,
+ * which end with it.  Nothing faults or hangs; the next moe_check_errors on the
+ * workspace returns MOE_ERR_TIMEOUT and clears the word.  workspace: any
+ * workspace of the library (>= 256 bytes, 256-byte aligned).  Asynchronous on
+ * stream. */
 int moe_selftest_wait_timeout(void *workspace, size_t workspace_bytes, int polls, void *stream);
 
 /* Which grouped expert-FFN kernels a call with T tokens runs (host-side, no

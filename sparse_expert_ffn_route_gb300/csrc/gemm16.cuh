@@ -28,10 +28,8 @@
 namespace moe {
 namespace gemm16 {
 
-using gemm::cluster_sync;
 using gemm::commit_pair;
 using gemm::expect_tx;
-using gemm::map_rank;
 using gemm::tma_2d_pair;
 using gemm::uniform;
 
@@ -99,20 +97,11 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr)
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// (a vote, so that loops on it are uniform across the warp for the compiler too)
-__device__ __forceinline__ bool stopped(const Ctrl *c)
-{
-    return __any_sync(0xffffffffu, *(volatile const int *)&c->abort != 0);
-}
+__device__ __forceinline__ bool stopped(const Ctrl *c) { return aborted(&c->abort); }
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
 {
-    const bool ok = mbar_wait(bar, parity);
-    if (!ok) {
-        atomicOr(err, kErrTimeout);
-        atomicExch(&c->abort, 1);
-    }
-    return __all_sync(0xffffffffu, ok);
+    return wait_or_abort(bar, parity, &c->abort, err);
 }
 
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
@@ -254,8 +243,9 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
             for (uint32_t j = j0; j < it && ok; ++j)
                 if ((j & 1) == turn) ok = wait_warp(&c->empty[j % a.stages], (j / a.stages) & 1, c, a.err);
             // after a wait that gave up: so do the copies still in flight
+            int polls = kDrainLimit;
             if (!ok && rank == 0)
-                for (uint32_t j = j0; j < it; ++j) mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1);
+                for (uint32_t j = j0; j < it; ++j) drain(&c->full[j % a.stages], (j / a.stages) & 1, polls);
         }
         __syncwarp();
     } else if (warp == C::MMA_WARP && rank == 0) {
@@ -285,7 +275,9 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
             commit_pair(&c->dfull[buf]);
         }
         commit_pair(&c->fin);   // every MMA is done before TMEM is freed
-        wait_warp(&c->fin, 0, c, a.err);
+        int polls = kDrainLimit;
+        drain(&c->fin, 0, polls);
+        __syncwarp();
     } else if (warp >= kWarpEpi && warp < C::MMA_WARP) {
         // ---------------- epilogue ----------------------------------------------------------
         const int qd = warp & 3, part = (warp - kWarpEpi) >> 2;
@@ -347,7 +339,11 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
 
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == C::MMA_WARP && rank == 1) wait_warp(&c->fin, 0, c, a.err);   // the leader's last commit, here too
+    if (warp == C::MMA_WARP && rank == 1) {   // the leader's last commit, here too
+        int polls = kDrainLimit;
+        drain(&c->fin, 0, polls);
+        __syncwarp();
+    }
     cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
     if (warp == C::MMA_WARP) {
         tc::fence_after_sync();

@@ -38,8 +38,9 @@
 // complete before it began.  No bounded wait then starts before that kernel's end: the waits of
 // this file measure this kernel's own progress.
 //
-// Every wait is bounded: one that gives up sets the workspace's error word and ends the CTA's
-// loops; its copies in flight and MMAs are waited for and TMEM is freed.
+// Every wait is bounded: one that gives up sets the workspace's error word and ends the loops of
+// every CTA of the cluster (cluster_wait.cuh); copies in flight and MMAs are waited for and TMEM is
+// freed.
 #pragma once
 
 #include <cuda.h>
@@ -48,6 +49,7 @@
 
 #include <atomic>
 
+#include "cluster_wait.cuh"
 #include "device_util.cuh"
 #include "gated_kept.cuh"
 #include "launch.cuh"
@@ -147,39 +149,17 @@ struct Ctrl {
     int32_t prefix[kMaxGroups + 1], off[kMaxGroups + 1];
 };
 
-// (a vote, so that loops on it are uniform across the warp for the compiler too)
-__device__ __forceinline__ bool stopped(const Ctrl *c)
-{
-    return __any_sync(0xffffffffu, *(volatile const int *)&c->abort != 0);
-}
+__device__ __forceinline__ bool stopped(const Ctrl *c) { return aborted(&c->abort); }
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
 {
-    bool ok = mbar_wait(bar, parity);
-    if (!ok) {
-        atomicOr(err, kErrTimeout);
-        atomicExch(&c->abort, 1);
-    }
-    return __all_sync(0xffffffffu, ok);
+    return wait_or_abort(bar, parity, &c->abort, err);
 }
 
 // the same on a barrier that other CTAs of the cluster arrive at (their writes become visible)
 __device__ __forceinline__ bool wait_warp_cluster(uint64_t *bar, uint32_t parity, Ctrl *c, int32_t *err)
 {
-    uint32_t ok = 0;
-    for (int n = 0; n < kWaitLimit && !ok; ++n)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-    if (!ok) {
-        atomicOr(err, kErrTimeout);
-        atomicExch(&c->abort, 1);
-    }
-    return __all_sync(0xffffffffu, ok != 0);
+    return wait_or_abort<true>(bar, parity, &c->abort, err);
 }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
@@ -257,12 +237,6 @@ __device__ __forceinline__ void ld1(uint32_t taddr, uint32_t step, uint32_t (&v)
 }
 
 // --- cluster ----------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, int rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
-}
 // asynchronous 4-byte store into another CTA's shared memory that counts on a barrier there
 __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar)
 {
@@ -281,10 +255,6 @@ __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar)
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // --- pairs of SMs (cta_group::2) ---------------------------------------------------------
 // TMA into this CTA's shared memory, completing on a barrier of either CTA of the pair
@@ -684,8 +654,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             for (uint32_t j = j0; C::PAIR && j < it && ok; ++j)
                 ok = wait_warp(&c->empty[j % C::STAGES], (j / C::STAGES) & 1, c, a.err);
             // copies still in flight (after a wait that gave up) land before the CTA ends
+            int polls = kDrainLimit;
             if ((!C::PAIR || !ok) && (!C::PAIR || rank == 0))
-                for (uint32_t j = j0; j < it; ++j) mbar_wait(&c->full[j % C::STAGES], (j / C::STAGES) & 1);
+                for (uint32_t j = j0; j < it; ++j) drain(&c->full[j % C::STAGES], (j / C::STAGES) & 1, polls);
         }
         __syncwarp();
     } else if (warp == 1 && !(C::PAIR && rank == 1)) {
@@ -755,7 +726,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             else h ^= 1;
         }
         commit<C::PAIR>(&c->fin);   // every MMA issued here is done before TMEM is freed
-        wait_warp(&c->fin, 0, c, a.err);
+        int polls = kDrainLimit;
+        drain(&c->fin, 0, polls);
+        __syncwarp();
     } else if (C::PAIR && warp == 1) {
         // ---------------- the peer's scales: one word a stage to the leader ------------------
         // The warps that wrote the scales have made them visible to the tensor unit (the async proxy)
@@ -867,7 +840,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             }
         }
         // sums still in flight (after a wait that gave up) land before the cluster ends
-        if (C::FEW && S > 1 && !ok) mbar_wait(&c->rfull, red_parity);
+        int polls = kDrainLimit;
+        if (C::FEW && S > 1 && !ok) drain(&c->rfull, red_parity, polls);
+        __syncwarp();
     } else if (C::MX && warp >= C::SF_WARP) {
         // ---------------- scales: this warp's operand, 128 rows -----------------------------
         // Chunks of 512 inputs (16 scale bytes of a row, two stages), one ahead in registers, over
@@ -930,7 +905,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     if (a.early) pdl_wait();   // a CTA without tiles too: this grid ends after the one before it
     tc::fence_before_sync();
     __syncthreads();
-    if (C::PAIR && rank == 1 && warp == 1) wait_warp(&c->fin, 0, c, a.err);   // the leader's last commit, here too
+    if (C::PAIR && rank == 1 && warp == 1) {   // the leader's last commit, here too
+        int polls = kDrainLimit;
+        drain(&c->fin, 0, polls);
+        __syncwarp();
+    }
     // no CTA of a cluster frees its TMEM or leaves while another may still use its memory
     if (CS > 1) cluster_sync();
     if (warp == 1) {
