@@ -265,26 +265,31 @@ size_t moe_mxfp4_workspace_size(const moe_config *cfg, int max_tokens);
  * expert ["MoE 路由与专家流式加载" §1.4, §2: dense layers before the sparse ones]:
  *   g = x w_gate^T, u = x w_up^T, h = silu(g) * u      (sums and silu in fp32)
  *   x [T][H] with ldx elements between rows, w_gate, w_up [F][H], h [T][F], all
- *   bf16 or all fp16 (dtype).  g, u: two arrays of T * F 16-bit words that keep,
- *   together, the factors of dh of each element for moe_gated_backward (not the
- *   values of g and u: 12 or 13 bits of each factor and a shared exponent); both
- *   NULL when no gradient is wanted.
+ *   bf16 or all fp16 (dtype).
+ *   kept_g, kept_u: two arrays of T * F 16-bit words in which the forward pass
+ *   leaves the factors of dh for moe_gated_backward, s = sigmoid(g):
+ *   u s (1 + g (1 - s)) in kept_g, g s in kept_u.  Words to be handed on, not g and
+ *   u themselves.  Each factor is held with its own exponent: fp16 as that number
+ *   (off by at most 2^-11 of it, or 2^-25, infinite from 65520 up); bf16 as a 15-bit magnitude
+ *   code and a sign, off by at most 2^-11 of it from 2^-12 to 16, by at most 2^-8
+ *   from 2^-84 to 2^60, by at most 2^-92 below, NaN above.  Both NULL when no gradient is
+ *   wanted.
  *   H, F multiples of 8 in [8, 65536], T in [0, 2^24], rows of x 16-byte aligned.
  *   workspace: moe_gated_workspace_size(T, H, F, 0) bytes, first 256 zeroed once. */
 int moe_gated_forward(const void *x, long long ldx, const void *w_gate, const void *w_up, int dtype,
-                      int T, int H, int F, void *h, void *g, void *u, void *workspace,
+                      int T, int H, int F, void *h, void *kept_g, void *kept_u, void *workspace,
                       size_t workspace_bytes, void *stream);
 
-/* Gradients of the gated block from dh [T][F] and what the forward pass kept in g
- * and u: with s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s (rounded to
+/* Gradients of the gated block from dh [T][F] and what the forward pass kept in
+ * kept_g and kept_u: with s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s (rounded to
  * dtype as the products' operands),
  *   dx = dg w_gate + du w_up [T][H],  dw_gate = dg^T x, dw_up = du^T x [F][H]
  * written in full (not accumulated).  dx, or both weight gradients, may be NULL.
  * T = 0 zeroes the weight gradients.  workspace: moe_gated_workspace_size(T, H,
  * F, 1) bytes, first 256 zeroed once. */
 int moe_gated_backward(const void *dh, const void *x, long long ldx, const void *w_gate,
-                       const void *w_up, const void *g, const void *u, int dtype, int T, int H,
-                       int F, void *dx, void *dw_gate, void *dw_up, void *workspace,
+                       const void *w_up, const void *kept_g, const void *kept_u, int dtype,
+                       int T, int H, int F, void *dx, void *dw_gate, void *dw_up, void *workspace,
                        size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of the gated block's calls (train = 0: forward alone); 0

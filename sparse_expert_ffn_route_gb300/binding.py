@@ -487,8 +487,9 @@ def alloc_gated_workspace(T: int, H: int, F: int, train: bool, device="cuda") ->
 
 
 def moe_gated_forward(x, w_gate, w_up, h, workspace, g=None, u=None, stream=None):
-    """h [T][F] = silu(x w_gate^T) * (x w_up^T), all bfloat16 or all float16; g, u [T][F] (of
-    the same type, as storage) keep what moe_gated_backward needs.  Rows of x [T][H] may be strided."""
+    """h [T][F] = silu(x w_gate^T) * (x w_up^T), all bfloat16 or all float16.  Rows of x [T][H]
+    may be strided.  g, u [T][F] of the same type are filled for moe_gated_backward with the factors of dh that
+    give dg and du, as 16-bit words to be handed on: they are not the values of x w_gate^T and x w_up^T."""
     T, H, ld = _rows(x, "x")
     F, dt = w_gate.shape[0], x.dtype
     _check(load_library().moe_gated_forward(
@@ -499,7 +500,7 @@ def moe_gated_forward(x, w_gate, w_up, h, workspace, g=None, u=None, stream=None
 
 
 def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace, stream=None):
-    """Gradients of moe_gated_forward from dh [T][F] and the kept g, u: dx [T][H] (or None) and
+    """Gradients of moe_gated_forward from dh [T][F] and the g, u that it filled: dx [T][H] (or None) and
     dw_gate, dw_up [F][H] (or both None), written in full."""
     T, H, ld = _rows(x, "x")
     F, dt = w_gate.shape[0], x.dtype

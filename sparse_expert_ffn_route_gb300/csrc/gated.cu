@@ -6,9 +6,9 @@
 //   dx = dg Wg + du Wu,   dWg = dg^T x,   dWu = du^T x.
 //
 // Of an element the forward pass keeps A = u s (1 + g (1 - s)) and B = g s for the backward one, so
-// that dg = dh A and du = dh B, in one word of 32 bits (gated_kept.cuh), its low half in `g`, its
-// high half in `u`.  The one rounding to 16 bits besides the outputs' is that of dg and du, the
-// operands of the tensor-core products.  Everything else is fp32.
+// that dg = dh A and du = dh B, in 16 bits each (gated_kept.cuh), A in `kept_g` and B in `kept_u`.  The
+// other rounding to 16 bits besides the outputs' is that of dg and du, the operands of the
+// tensor-core products.  Everything else is fp32.
 #include <algorithm>
 
 #include "gemm16.cuh"
@@ -30,11 +30,11 @@ __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ void set(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void set(__half &d, float v) { d = __float2half_rn(v); }
 
-// dg, du from dh and the kept words, 8 values a thread (F is a multiple of 8, so the rows laid end
+// dg, du from dh and the kept factors, 8 values a thread (F is a multiple of 8, so the rows laid end
 // to end are).  Bound by memory: 10 bytes a value.
 template <typename T, bool FP16>
 __global__ void __launch_bounds__(256)
-    gated_grad_kernel(const T *__restrict__ dh, const uint16_t *__restrict__ lo, const uint16_t *__restrict__ hi,
+    gated_grad_kernel(const T *__restrict__ dh, const uint16_t *__restrict__ kept_g, const uint16_t *__restrict__ kept_u,
                       long long units, T *__restrict__ dg, T *__restrict__ du)
 {
     pdl_wait();
@@ -46,15 +46,13 @@ __global__ void __launch_bounds__(256)
         T t[8];
     } a, p, q;
     a.v = ld_stream_v4(reinterpret_cast<const uint4 *>(dh) + i);
-    const uint4 l4 = ld_stream_v4(reinterpret_cast<const uint4 *>(lo) + i), h4 = ld_stream_v4(reinterpret_cast<const uint4 *>(hi) + i);
-    const uint32_t l[4] = {l4.x, l4.y, l4.z, l4.w}, h[4] = {h4.x, h4.y, h4.z, h4.w};
+    const uint4 a4 = ld_stream_v4(reinterpret_cast<const uint4 *>(kept_g) + i), b4 = ld_stream_v4(reinterpret_cast<const uint4 *>(kept_u) + i);
+    const uint32_t A[4] = {a4.x, a4.y, a4.z, a4.w}, B[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        float A, B;
-        Kept<FP16>::unpack(__byte_perm(l[j >> 1], h[j >> 1], j & 1 ? 0x7632 : 0x5410), A, B);
         const float d = to_f(a.t[j]);
-        set(p.t[j], d * A);
-        set(q.t[j], d * B);
+        set(p.t[j], d * Kept<FP16>::value(j & 1 ? A[j >> 1] : A[j >> 1] << 16));
+        set(q.t[j], d * Kept<FP16>::value(j & 1 ? B[j >> 1] : B[j >> 1] << 16));
     }
     reinterpret_cast<uint4 *>(dg)[i] = p.v;
     reinterpret_cast<uint4 *>(du)[i] = q.v;
@@ -216,7 +214,7 @@ size_t moe_gated_workspace_size(int T, int H, int F, int train)
 }
 
 int moe_gated_forward(const void *x, long long ldx, const void *w_gate, const void *w_up, int dtype, int T, int H, int F,
-                      void *h, void *g, void *u, void *workspace, size_t workspace_bytes, void *stream)
+                      void *h, void *kept_g, void *kept_u, void *workspace, size_t workspace_bytes, void *stream)
 {
     int rc;
     if ((rc = check_shape(dtype, T, H, F, ldx))) return rc;
@@ -225,16 +223,16 @@ int moe_gated_forward(const void *x, long long ldx, const void *w_gate, const vo
     GATED_PTR(w_gate);
     GATED_PTR(w_up);
     GATED_PTR(h);
-    if (!g != !u) return set_error(MOE_ERR_ARG, "g and u go together");
-    if (off(g, 16) || off(u, 16)) return set_error(MOE_ERR_ALIGN, "g or u is not 16-byte aligned");
+    if (!kept_g != !kept_u) return set_error(MOE_ERR_ARG, "kept_g and kept_u go together");
+    if (off(kept_g, 16) || off(kept_u, 16)) return set_error(MOE_ERR_ALIGN, "kept_g or kept_u is not 16-byte aligned");
     if ((rc = check_workspace(workspace, workspace_bytes, 256)) || (rc = require_device())) return rc;
-    return done(forward(x, ldx, w_gate, w_up, dtype, T, H, F, h, g, u, static_cast<int32_t *>(workspace),
+    return done(forward(x, ldx, w_gate, w_up, dtype, T, H, F, h, kept_g, kept_u, static_cast<int32_t *>(workspace),
                         (cudaStream_t)stream),
                 "gated forward launch");
 }
 
-int moe_gated_backward(const void *dh, const void *x, long long ldx, const void *w_gate, const void *w_up, const void *g,
-                       const void *u, int dtype, int T, int H, int F, void *dx, void *dw_gate, void *dw_up,
+int moe_gated_backward(const void *dh, const void *x, long long ldx, const void *w_gate, const void *w_up, const void *kept_g,
+                       const void *kept_u, int dtype, int T, int H, int F, void *dx, void *dw_gate, void *dw_up,
                        void *workspace, size_t workspace_bytes, void *stream)
 {
     int rc;
@@ -253,8 +251,8 @@ int moe_gated_backward(const void *dh, const void *x, long long ldx, const void 
     GATED_PTR(x);
     GATED_PTR(w_gate);
     GATED_PTR(w_up);
-    GATED_PTR(g);
-    GATED_PTR(u);
+    GATED_PTR(kept_g);
+    GATED_PTR(kept_u);
     if ((rc = check_workspace(workspace, workspace_bytes, moe_gated_workspace_size(T, H, F, 1))) || (rc = require_device()))
         return rc;
     if (!dx && !dw_gate) return done(cudaSuccess, "");
@@ -265,9 +263,9 @@ int moe_gated_backward(const void *dh, const void *x, long long ldx, const void 
     cudaError_t e =
         dtype == MOE_DTYPE_BF16
             ? launch_kernel(gated_grad_kernel<__nv_bfloat16, false>, grid, dim3(256), 0, st, 1, (const __nv_bfloat16 *)dh,
-                            (const uint16_t *)g, (const uint16_t *)u, units, (__nv_bfloat16 *)dg, (__nv_bfloat16 *)du)
-            : launch_kernel(gated_grad_kernel<__half, true>, grid, dim3(256), 0, st, 1, (const __half *)dh, (const uint16_t *)g,
-                            (const uint16_t *)u, units, (__half *)dg, (__half *)du);
+                            (const uint16_t *)kept_g, (const uint16_t *)kept_u, units, (__nv_bfloat16 *)dg, (__nv_bfloat16 *)du)
+            : launch_kernel(gated_grad_kernel<__half, true>, grid, dim3(256), 0, st, 1, (const __half *)dh, (const uint16_t *)kept_g,
+                            (const uint16_t *)kept_u, units, (__half *)dg, (__half *)du);
     if (e == cudaSuccess && dx) e = grad_x(dg, du, w_gate, w_up, dtype, T, H, F, dx, err, st);
     if (e == cudaSuccess && dw_gate) e = grad_w(dg, du, x, ldx, dtype, T, H, F, dw_gate, dw_up, err, st);
     return done(e, "gated backward launch");

@@ -51,7 +51,7 @@ struct Args {
     int rbox;                // rows of the rows operand's box: 128, or what a call of fewer has (the
                              // lanes after them hold whatever was there; none of them is stored)
     int ksteps, kphase;      // stages of 64; kDx: stages of the first phase
-    void *out[3];            // (h, kept low, high halves) | dx | (dWg, dWu)
+    void *out[3];            // (h, kept dh/dg, dh/du) | dx | (dWg, dWu)
     int stages, stage_bytes; // of the ring: a tile of few rows and columns has more and smaller ones
     int rows_bytes;          // the rows operand's part of a stage
     int cols_bytes;          // one columns operand's
@@ -142,7 +142,7 @@ __device__ __forceinline__ void put32(void *out, size_t at, const uint32_t (&w)[
     }
 }
 
-// h, and the kept words where they are asked for, of 16 columns
+// h, and the kept factors where they are asked for, of 16 columns
 template <bool FP16>
 __device__ __forceinline__ void put_gated(const float (&g)[16], const float (&u)[16], size_t at, int n, const Args &a)
 {
@@ -153,19 +153,18 @@ __device__ __forceinline__ void put_gated(const float (&g)[16], const float (&u)
         put32(a.out[0], at, h, n, a);
         return;
     }
-    uint32_t lo[8], hi[8];
+    uint32_t ka[8], kb[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float A[2], B[2];
         const float h0 = gated(g[2 * i], u[2 * i], A[0], B[0]), h1 = gated(g[2 * i + 1], u[2 * i + 1], A[1], B[1]);
         h[i] = pack2(h0, h1, a.dtype);
-        const uint32_t w0 = Kept<FP16>::pack(A[0], B[0]), w1 = Kept<FP16>::pack(A[1], B[1]);
-        lo[i] = __byte_perm(w0, w1, 0x5410);
-        hi[i] = __byte_perm(w0, w1, 0x7632);
+        ka[i] = Kept<FP16>::code(A[0]) | Kept<FP16>::code(A[1]) << 16;
+        kb[i] = Kept<FP16>::code(B[0]) | Kept<FP16>::code(B[1]) << 16;
     }
     put32(a.out[0], at, h, n, a);
-    put32(a.out[1], at, lo, n, a);
-    put32(a.out[2], at, hi, n, a);
+    put32(a.out[1], at, ka, n, a);
+    put32(a.out[2], at, kb, n, a);
 }
 
 template <Mode MODE>

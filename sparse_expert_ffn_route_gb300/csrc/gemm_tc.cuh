@@ -84,7 +84,7 @@ struct Args {
     const uint8_t *sfa[2], *sfb;
     int sf_ld;                 // K / 32
     long long sfa_rows;        // E * M
-    void *out[3];              // y | (h, kept low, high halves) | (codes, scales)
+    void *out[3];              // y | (h, kept dh/dg, dh/du) | (codes, scales)
     int ld;                    // row stride of out, in elements (codes: of M)
     int dtype;                 // MOE_DTYPE_* of out
     uint32_t idesc;            // instruction descriptor without N and the scale ids
@@ -465,9 +465,9 @@ __device__ __forceinline__ void emit1(const Args &a, float g, float u, int m, in
             float A, B;
             store(a.out[0], a.dtype, at, gated(g, u, A, B));
             if (a.out[1]) {
-                const uint32_t w = a.dtype == MOE_DTYPE_F16 ? Kept<true>::pack(A, B) : Kept<false>::pack(A, B);
-                static_cast<uint16_t *>(a.out[1])[at] = (uint16_t)w;
-                static_cast<uint16_t *>(a.out[2])[at] = (uint16_t)(w >> 16);
+                const bool f16 = a.dtype == MOE_DTYPE_F16;
+                static_cast<uint16_t *>(a.out[1])[at] = (uint16_t)(f16 ? Kept<true>::code(A) : Kept<false>::code(A));
+                static_cast<uint16_t *>(a.out[2])[at] = (uint16_t)(f16 ? Kept<true>::code(B) : Kept<false>::code(B));
             }
         } else {
             store(a.out[0], a.dtype, at, g);
