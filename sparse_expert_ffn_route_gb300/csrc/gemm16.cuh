@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
             // READ columns at a time, in turns of the warps of these lanes; the width is a
             // multiple of 32, the columns of 8
             for (int c0 = part * C::READ; c0 < n; c0 += C::EPI / 4 * C::READ) {
+                __syncwarp();   // lanes past the last row come from another branch, the loads want the whole warp
                 uint32_t v[2][C::READ];
 #pragma unroll
                 for (int o = 0; o < C::NB; ++o) ld_cols(tl + buf * kMaxCols + o * kMaxCols + c0, v[o]);

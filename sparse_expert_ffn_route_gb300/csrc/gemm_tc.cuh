@@ -804,6 +804,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 if (more && lane < S) arrive_cluster(map_rank(smem_u32(&c->rempty), lane));
             } else if (C::FEW) {
                 for (int k = 0; k < q.n; ++k) {
+                    __syncwarp();   // lanes past M come from another branch, the load wants the whole warp
                     uint32_t v[2];
                     ld1<C::NA>(d0 + k, dstep, v);
                     emit1<MODE>(a, __uint_as_float(v[0]), __uint_as_float(v[1]), m, lane, q.row0 + k);
@@ -821,6 +822,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 };
                 if (part * 16 >= q.np) give_back();
                 for (int c0 = part * 16; c0 < q.np; c0 += 4 * C::EPI) {
+                    __syncwarp();   // as above
                     uint32_t v[2][16];
 #pragma unroll
                     for (int o = 0; o < C::NA; ++o) tc::ld16(d0 + o * dstep + c0, v[o]);
