@@ -341,14 +341,17 @@ def moe_stage_times(reset: bool = True):
 
 
 # --- MXFP4 and the 16-bit gated block ----------------------------------------------------
-# These check what the C entry points cannot see: types, shapes and strides of the tensors.
+# These check what the C entry points cannot see: types, shapes, strides and devices of the tensors.
+# Each of them takes its first tensor's device, which has to be the current one (the library launches
+# there), and asks for the others, the workspace among them, on the same.
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
 
 
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    """The handle of `stream`, or of the current stream of t's device, without the Stream object that
+def _raw_stream(stream, device: int) -> int:
+    """The handle of `stream`, or of the current stream of the device, without the Stream object that
     torch.cuda.current_stream makes (2.9 us against 0.1 us a call, where a one-token call takes 5)."""
-    return _current_stream(t.get_device()) if stream is None else stream.cuda_stream
+    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
@@ -361,25 +364,44 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _dense(t: torch.Tensor, name: str, shape, dtype) -> int:
-    """Device pointer of a contiguous CUDA tensor of the given shape and type."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+def _dense(t: torch.Tensor, name: str, shape, dtype, device: int) -> int:
+    """Device pointer of a contiguous tensor of the given shape and type on `device`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
         return t.data_ptr()
-    raise ValueError("%s must be a contiguous CUDA tensor %s of %s (got %s of %s%s)" % (
-        name, tuple(shape), dtype, tuple(t.shape), t.dtype, "" if t.is_contiguous() else ", strided"))
+    raise ValueError("%s must be a contiguous CUDA tensor %s of %s on device %d (got %s of %s on %s%s)" % (
+        name, tuple(shape), dtype, device, tuple(t.shape), t.dtype, t.device, "" if t.is_contiguous() else ", strided"))
+
+
+def _space(t: torch.Tensor, device: int) -> int:
+    """Device pointer of a workspace: contiguous bytes on `device`."""
+    if t.dtype is torch.uint8 and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    raise ValueError("the workspace must be a contiguous CUDA tensor of torch.uint8 on device %d (got %s on %s%s)" % (
+        device, t.dtype, t.device, "" if t.is_contiguous() else ", strided"))
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of t's device, which has to be the current CUDA device."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("%s must be a contiguous CUDA tensor (got one on %s)" % (name, t.device))
+    if device != _current_device():
+        raise ValueError("%s is on device %d, the current device is %d" % (name, device, _current_device()))
+    return device
 
 
 def _rows(t: torch.Tensor, name: str):
-    """(rows, width, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    """(device, rows, width, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
     shape = t.shape
-    if len(shape) != 2 or not t.is_cuda:
+    if len(shape) != 2:
         raise ValueError("%s must be a 2-D CUDA tensor" % name)
+    device = _device(t, name)
     rows, width = shape
     if t.is_contiguous():
-        return rows, width, width
+        return device, rows, width, width
     if width > 1 and t.stride(1) != 1:
         raise ValueError("rows of %s must be contiguous" % name)
-    return rows, width, t.stride(0)
+    return device, rows, width, t.stride(0)
 
 
 def moe_quantize_mxfp4(x, codes, scales, stream=None):
@@ -389,17 +411,17 @@ def moe_quantize_mxfp4(x, codes, scales, stream=None):
     if len(x.shape) > 2 and x.is_contiguous():
         x = x.view(-1, x.shape[-1])
         codes, scales = codes.view(-1, codes.shape[-1]), scales.view(-1, scales.shape[-1])
-    rows, K, ld = _rows(x, "x")
+    dev, rows, K, ld = _rows(x, "x")
     rc = load_library().moe_quantize_mxfp4(
-        x.data_ptr(), _dtype(x, "x"), ld, rows, K, _dense(codes, "codes", (rows, K // 2), torch.uint8),
-        _dense(scales, "scales", (rows, K // 32), torch.uint8), _raw_stream(stream, x))
+        x.data_ptr(), _dtype(x, "x"), ld, rows, K, _dense(codes, "codes", (rows, K // 2), torch.uint8, dev),
+        _dense(scales, "scales", (rows, K // 32), torch.uint8, dev), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_quantize_mxfp4")
 
 
 def moe_dequantize_mxfp4(codes, scales, y, stream=None):
     """The values that MXFP4 codes [..][K/2] and scales [..][K/32] stand for, into y [..][K]."""
-    shape = y.shape
+    shape, dev = y.shape, _device(y, "y")
     if len(shape) == 2:
         rows, K = shape
         c, sc = (rows, K // 2), (rows, K // 32)
@@ -407,8 +429,8 @@ def moe_dequantize_mxfp4(codes, scales, y, stream=None):
         K, lead = shape[-1], tuple(shape[:-1])
         rows, c, sc = (y.numel() // K if K else 0), lead + (K // 2,), lead + (K // 32,)
     rc = load_library().moe_dequantize_mxfp4(
-        _dense(codes, "codes", c, torch.uint8), _dense(scales, "scales", sc, torch.uint8), rows, K,
-        _dense(y, "y", shape, y.dtype), _dtype(y, "y"), _raw_stream(stream, y))
+        _dense(codes, "codes", c, torch.uint8, dev), _dense(scales, "scales", sc, torch.uint8, dev), rows, K,
+        _dense(y, "y", shape, y.dtype, dev), _dtype(y, "y"), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_dequantize_mxfp4")
 
@@ -422,18 +444,18 @@ def moe_mxfp4_matmul(x, x_scales, w, w_scales, y, workspace, offsets=None, strea
     """y [rows][N] = x w^T by group: x [rows][K/2], x_scales [rows][K/32]; w [groups][N][K/2] (or
     [N][K/2]), w_scales alike; offsets [groups + 1] int32 (None: one group, all rows)."""
     rows, half = x.shape
-    K32, u8 = half // 16, torch.uint8
+    K32, u8, dev = half // 16, torch.uint8, _device(x, "x")
     if w.dim() == 2:
         groups, N = 1, w.shape[0]
-        pw, psw = _dense(w, "w", (N, half), u8), _dense(w_scales, "w_scales", (N, K32), u8)
+        pw, psw = _dense(w, "w", (N, half), u8, dev), _dense(w_scales, "w_scales", (N, K32), u8, dev)
     else:
         groups, N = w.shape[0], w.shape[1]
-        pw, psw = _dense(w, "w", (groups, N, half), u8), _dense(w_scales, "w_scales", (groups, N, K32), u8)
+        pw, psw = _dense(w, "w", (groups, N, half), u8, dev), _dense(w_scales, "w_scales", (groups, N, K32), u8, dev)
     _check(load_library().moe_mxfp4_matmul(
-        _dense(x, "x", (rows, half), u8), _dense(x_scales, "x_scales", (rows, K32), u8), rows, pw, psw, groups,
-        None if offsets is None else _dense(offsets, "offsets", (groups + 1,), torch.int32), N, 2 * half,
-        _dense(y, "y", (rows, N), y.dtype), _dtype(y, "y"), workspace.data_ptr(), workspace.numel(),
-        _raw_stream(stream, x)), "moe_mxfp4_matmul")
+        _dense(x, "x", (rows, half), u8, dev), _dense(x_scales, "x_scales", (rows, K32), u8, dev), rows, pw, psw, groups,
+        None if offsets is None else _dense(offsets, "offsets", (groups + 1,), torch.int32, dev), N, 2 * half,
+        _dense(y, "y", (rows, N), y.dtype, dev), _dtype(y, "y"), _space(workspace, dev), workspace.numel(),
+        _raw_stream(stream, dev)), "moe_mxfp4_matmul")
 
 
 def moe_mxfp4_workspace_size(cfg: MoeConfig, max_tokens: int) -> int:
@@ -457,19 +479,18 @@ def moe_mxfp4_expert_ffn(cfg, x, weights: Dict[str, torch.Tensor], y_pairs, work
     w_gate, w_up [E][F][H/2], w_down [E][H][F/2] and s_gate, s_up [E][F][H/32],
     s_down [E][H][F/32], uint8."""
     T, H, F, E, P = x.shape[0], cfg.hidden, cfg.d_ff, cfg.n_experts, y_pairs.shape[0]
-    u8, up, down = torch.uint8, (E, F, H // 2), (E, H, F // 2)
+    u8, up, down, dev = torch.uint8, (E, F, H // 2), (E, H, F // 2), _device(x, "x")
     s_up, s_down = (E, F, H // 32), (E, H, F // 32)
-    w = ExpertMxfp4(_dense(weights["w_gate"], "w_gate", up, u8), _dense(weights["s_gate"], "s_gate", s_up, u8),
-                    _dense(weights["w_up"], "w_up", up, u8), _dense(weights["s_up"], "s_up", s_up, u8),
-                    _dense(weights["w_down"], "w_down", down, u8), _dense(weights["s_down"], "s_down", s_down, u8))
+    w = ExpertMxfp4(*[_dense(weights[k], k, shape, u8, dev) for k, shape in (
+        ("w_gate", up), ("s_gate", s_up), ("w_up", up), ("s_up", s_up), ("w_down", down), ("s_down", s_down))])
     if P != T * cfg.top_k:
         raise ValueError("y_pairs must have T * top_k = %d rows (got %d)" % (T * cfg.top_k, P))
     _check(load_library().moe_mxfp4_expert_ffn(
-        ctypes.byref(cfg), _dense(x, "x", (T, H), x.dtype), _dtype(x, "x"), T, ctypes.byref(w),
-        None if offsets is None else _dense(offsets, "offsets", (E + 1,), torch.int32),
-        None if tok is None else _dense(tok, "tok", (P,), torch.int32),
-        _dense(y_pairs, "y_pairs", (P, H), y_pairs.dtype), _dtype(y_pairs, "y_pairs"),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x)), "moe_mxfp4_expert_ffn")
+        ctypes.byref(cfg), _dense(x, "x", (T, H), x.dtype, dev), _dtype(x, "x"), T, ctypes.byref(w),
+        None if offsets is None else _dense(offsets, "offsets", (E + 1,), torch.int32, dev),
+        None if tok is None else _dense(tok, "tok", (P,), torch.int32, dev),
+        _dense(y_pairs, "y_pairs", (P, H), y_pairs.dtype, dev), _dtype(y_pairs, "y_pairs"),
+        _space(workspace, dev), workspace.numel(), _raw_stream(stream, dev)), "moe_mxfp4_expert_ffn")
 
 
 def moe_gated_workspace_size(T: int, H: int, F: int, train: bool) -> int:
@@ -490,24 +511,24 @@ def moe_gated_forward(x, w_gate, w_up, h, workspace, g=None, u=None, stream=None
     """h [T][F] = silu(x w_gate^T) * (x w_up^T), all bfloat16 or all float16.  Rows of x [T][H]
     may be strided.  g, u [T][F] of the same type are filled for moe_gated_backward with the factors of dh that
     give dg and du, as 16-bit words to be handed on: they are not the values of x w_gate^T and x w_up^T."""
-    T, H, ld = _rows(x, "x")
+    dev, T, H, ld = _rows(x, "x")
     F, dt = w_gate.shape[0], x.dtype
     _check(load_library().moe_gated_forward(
-        x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt), _dense(w_up, "w_up", (F, H), dt),
-        _dtype(x, "x"), T, H, F, _dense(h, "h", (T, F), dt),
-        None if g is None else _dense(g, "g", (T, F), dt), None if u is None else _dense(u, "u", (T, F), dt),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x)), "moe_gated_forward")
+        x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt, dev), _dense(w_up, "w_up", (F, H), dt, dev),
+        _dtype(x, "x"), T, H, F, _dense(h, "h", (T, F), dt, dev),
+        None if g is None else _dense(g, "g", (T, F), dt, dev), None if u is None else _dense(u, "u", (T, F), dt, dev),
+        _space(workspace, dev), workspace.numel(), _raw_stream(stream, dev)), "moe_gated_forward")
 
 
 def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace, stream=None):
     """Gradients of moe_gated_forward from dh [T][F] and the g, u that it filled: dx [T][H] (or None) and
     dw_gate, dw_up [F][H] (or both None), written in full."""
-    T, H, ld = _rows(x, "x")
+    dev, T, H, ld = _rows(x, "x")
     F, dt = w_gate.shape[0], x.dtype
-    opt = lambda t, name, shape: None if t is None else _dense(t, name, shape, dt)  # noqa: E731
+    opt = lambda t, name, shape: None if t is None else _dense(t, name, shape, dt, dev)  # noqa: E731
     _check(load_library().moe_gated_backward(
-        _dense(dh, "dh", (T, F), dt), x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt),
-        _dense(w_up, "w_up", (F, H), dt), _dense(g, "g", (T, F), dt), _dense(u, "u", (T, F), dt),
+        _dense(dh, "dh", (T, F), dt, dev), x.data_ptr(), ld, _dense(w_gate, "w_gate", (F, H), dt, dev),
+        _dense(w_up, "w_up", (F, H), dt, dev), _dense(g, "g", (T, F), dt, dev), _dense(u, "u", (T, F), dt, dev),
         _dtype(x, "x"), T, H, F, opt(dx, "dx", (T, H)), opt(dw_gate, "dw_gate", (F, H)),
-        opt(dw_up, "dw_up", (F, H)), workspace.data_ptr(), workspace.numel(),
-        _raw_stream(stream, x)), "moe_gated_backward")
+        opt(dw_up, "dw_up", (F, H)), _space(workspace, dev), workspace.numel(),
+        _raw_stream(stream, dev)), "moe_gated_backward")
