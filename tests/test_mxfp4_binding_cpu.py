@@ -1,5 +1,8 @@
 """What the binding of the MXFP4 and gated calls refuses before the library is called: workspaces and
 tensors that the library cannot see to be wrong.  With stand-ins for tensors on CUDA devices."""
+import importlib.util
+import sys
+
 import pytest
 import torch
 
@@ -119,3 +122,18 @@ def test_the_device_is_the_current_one(bound, monkeypatch, name):
     call, tensors = calls()[name]
     with pytest.raises(ValueError, match="current device"):
         call(**tensors)
+
+
+def test_import_without_torchs_private_stream_call(monkeypatch):
+    """The binding imports on a torch that lacks it, and asks for the stream the public way."""
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("binding_without", binding.__file__)
+    copy = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(sys.modules, spec.name, copy)
+    spec.loader.exec_module(copy)
+    asked = []
+
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: asked.append(device) or Stream)
+    assert copy._raw_stream(None, 3) == 77 and asked == [3]
