@@ -767,7 +767,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             if (C::FEW && S > 1) {
                 // send the partial sums to their columns' owners (column k to rank k % S), then
                 // add up the own columns in rank order
-                const bool more = t + tstep < total;   // the buffers are used again
+                // the buffers are used again: the host gives every tile a cluster of its own, but lists
+                // out of order can name rows more than once and hold more tiles than it counts
+                const bool more = t + tstep < total;
                 const int per = (kSplitCols + S - 1) / S, own = q.n > rank ? (q.n - rank + S - 1) / S : 0;
                 if (warp == 4 && lane == 0 && own > 0)
                     mbar_arrive_expect_tx(&c->rfull, (uint32_t)(S * own * C::NA * kM * 4));

@@ -153,6 +153,22 @@ def test_product_of_few_rows_and_many_tiles(K):
         check_product(y[off[e]:off[e + 1]], x[off[e]:off[e + 1]], w[e], torch.float32)
 
 
+def test_product_of_lists_that_name_rows_again():
+    """Groups out of order are recorded and left out; the others here name every row five times, more
+    tiles of the few-row form than the host counts on, so that a cluster which shares a tile's
+    reduction takes a second one.  (All groups' weights are alike: it does not matter whose row it is.)"""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    E, rows, N, K = 9, 64, 100, 4096
+    (px, sx), (pw, sw) = random_gpu(g, rows, K), random_gpu(g, 1, N, K)
+    off = torch.tensor([0, rows] * 5, dtype=torch.int32, device="cuda")
+    y, ws = torch.full((rows, N), 7.0, dtype=torch.float32, device="cuda"), moe.alloc_mxfp4_matmul_workspace()
+    moe.moe_mxfp4_matmul(px, sx, pw.repeat(E, 1, 1), sw.repeat(E, 1, 1), y, ws, offsets=off)
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_check_errors(ws)
+    assert e.value.code == moe.MOE_ERR_DEVICE          # the lists, and no wait that gave up
+    check_product(y, values64(px, sx), values64(pw[0], sw[0]), torch.float32)
+
+
 @pytest.mark.parametrize("counts,H,F", [([1500, 0, 1, 800, 299], 128, 1984), ([17, 24, 3, 0, 31, 22, 8, 1] * 10, 256, 960)])
 def test_expert_ffn_of_many_tiles(counts, H, F):
     """The gate/up form on pairs with more tiles than pairs (first), and the few-row form with more
