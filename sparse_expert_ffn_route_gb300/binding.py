@@ -9,6 +9,7 @@ If libmoe.so is missing, loading raises ``ImportError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -348,6 +349,7 @@ def moe_stage_times(reset: bool = True):
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 _current_device = torch.cuda.current_device
+_device_count = functools.lru_cache(maxsize=None)(torch.cuda.device_count)
 
 
 def _raw_stream(stream, device: int) -> int:
@@ -387,7 +389,7 @@ def _device(t: torch.Tensor, name: str) -> int:
     device = t.get_device()
     if device < 0:
         raise ValueError("%s must be a contiguous CUDA tensor (got one on %s)" % (name, t.device))
-    if device != _current_device():
+    if _device_count() > 1 and device != _current_device():
         raise ValueError("%s is on device %d, the current device is %d" % (name, device, _current_device()))
     return device
 

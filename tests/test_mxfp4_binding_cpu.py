@@ -57,9 +57,10 @@ class Library:
 
 @pytest.fixture
 def bound(monkeypatch):
-    """The binding over a library that only says that it was called; the current device is 0."""
+    """The binding over a library that only says that it was called; the current device of two is 0."""
     monkeypatch.setattr(binding, "load_library", lambda: Library())
     monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_device_count", lambda: 2)
 
 
 def calls():
