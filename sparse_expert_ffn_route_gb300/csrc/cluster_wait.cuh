@@ -12,8 +12,9 @@
 // The poll loop does not look at `abort`: its few instructions lie on the path from one stage to the
 // next, and a look between polls cost a prompt's product 60 -> 72 us and its expert block 953 -> 1146.
 //
-// What a kernel has still in flight then (copies into its shared memory, MMAs on its tensor
-// memory) completes by itself in microseconds; drain() gives it that time, whatever `abort` says.
+// What a kernel has in flight when it stops like that (copies and other CTAs' stores into its shared
+// memory, MMAs on its tensor memory) completes by itself in microseconds, but nothing says when: settle()
+// has every CTA wait 15 ms before it goes to the barrier behind which they end.
 #pragma once
 
 #include "device_util.cuh"
@@ -22,7 +23,7 @@
 namespace moe {
 
 constexpr int kClusterWaitLimit = 1 << 18;
-constexpr int kDrainLimit = 1 << 12;   // polls, for all that one warp drains
+constexpr int kSettleLimit = 1 << 12;   // polls
 
 __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, int rank)
 {
@@ -78,10 +79,20 @@ __device__ __forceinline__ bool aborted(const int *abort)
     return __any_sync(0xffffffffu, *(volatile const int *)abort != 0);
 }
 
-// waits for a phase without recording anything; `polls` is what is left of the warp's limit
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, int &polls)
+// waits for a phase without recording anything; `polls` is what is left of the limit
+__device__ __forceinline__ void poll(uint64_t *bar, uint32_t parity, int &polls)
 {
     while (polls > 0 && !mbar_try_wait(bar, parity)) --polls;
+}
+
+// By one warp of each CTA at its end: waits for the first phase of `fin`, the commit of all MMAs, and
+// after a stop for the rest of the limit too (no second phase follows).
+__device__ __forceinline__ void settle(uint64_t *fin, const int *abort)
+{
+    int polls = kSettleLimit;
+    poll(fin, 0, polls);
+    if (aborted(abort)) poll(fin, 1, polls);
+    __syncwarp();
 }
 
 }  // namespace moe

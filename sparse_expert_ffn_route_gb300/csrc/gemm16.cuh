@@ -238,13 +238,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
             // the leader's commits on the last stages' `empty`, which no load waits for, land before
             // this CTA ends and its shared memory is another kernel's (each warp waits for its own
             // stages: it has seen the phase before)
-            const uint32_t j0 = it > (uint32_t)a.stages ? it - a.stages : 0;
-            for (uint32_t j = j0; j < it && ok; ++j)
+            for (uint32_t j = it > (uint32_t)a.stages ? it - a.stages : 0; j < it && ok; ++j)
                 if ((j & 1) == turn) ok = wait_warp(&c->empty[j % a.stages], (j / a.stages) & 1, c, a.err);
-            // after a wait that gave up: so do the copies still in flight
-            int polls = kDrainLimit;
-            if (!ok && rank == 0)
-                for (uint32_t j = j0; j < it; ++j) drain(&c->full[j % a.stages], (j / a.stages) & 1, polls);
         }
         __syncwarp();
     } else if (warp == C::MMA_WARP && rank == 0) {
@@ -274,9 +269,6 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
             commit_pair(&c->dfull[buf]);
         }
         commit_pair(&c->fin);   // every MMA is done before TMEM is freed
-        int polls = kDrainLimit;
-        drain(&c->fin, 0, polls);
-        __syncwarp();
     } else if (warp >= kWarpEpi && warp < C::MMA_WARP) {
         // ---------------- epilogue ----------------------------------------------------------
         const int qd = warp & 3, part = (warp - kWarpEpi) >> 2;
@@ -339,11 +331,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) gemm16_kernel(const __g
 
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == C::MMA_WARP && rank == 1) {   // the leader's last commit, here too
-        int polls = kDrainLimit;
-        drain(&c->fin, 0, polls);
-        __syncwarp();
-    }
+    if (warp == C::MMA_WARP) settle(&c->fin, &c->abort);   // the leader's last commit, in both CTAs
     cluster_sync();   // neither CTA frees its TMEM or leaves while the other still uses the pair's
     if (warp == C::MMA_WARP) {
         tc::fence_after_sync();

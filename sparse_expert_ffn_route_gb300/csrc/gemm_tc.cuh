@@ -39,8 +39,7 @@
 // this file measure this kernel's own progress.
 //
 // Every wait is bounded: one that gives up sets the workspace's error word and ends the loops of
-// every CTA of the cluster (cluster_wait.cuh); copies in flight and MMAs are waited for and TMEM is
-// freed.
+// every CTA of the cluster (cluster_wait.cuh); what is in flight gets its time and TMEM is freed.
 #pragma once
 
 #include <cuda.h>
@@ -647,17 +646,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             }
         }
         if (a.early) pdl_wait();
-        if (warp == 0) {
-            const uint32_t j0 = it > (uint32_t)C::STAGES ? it - C::STAGES : 0;
-            // a pair: the leader's commits on the last stages' `empty`, which no load waits for, land
-            // before this CTA ends and its shared memory is another kernel's
-            for (uint32_t j = j0; C::PAIR && j < it && ok; ++j)
+        // a pair: the leader's commits on the last stages' `empty`, which no load waits for, land before
+        // this CTA ends and its shared memory is another kernel's
+        if (C::PAIR && warp == 0)
+            for (uint32_t j = it > (uint32_t)C::STAGES ? it - C::STAGES : 0; j < it && ok; ++j)
                 ok = wait_warp(&c->empty[j % C::STAGES], (j / C::STAGES) & 1, c, a.err);
-            // copies still in flight (after a wait that gave up) land before the CTA ends
-            int polls = kDrainLimit;
-            if ((!C::PAIR || !ok) && (!C::PAIR || rank == 0))
-                for (uint32_t j = j0; j < it; ++j) drain(&c->full[j % C::STAGES], (j / C::STAGES) & 1, polls);
-        }
         __syncwarp();
     } else if (warp == 1 && !(C::PAIR && rank == 1)) {
         // ---------------- MMA issue ---------------------------------------------------------
@@ -726,9 +719,6 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
             else h ^= 1;
         }
         commit<C::PAIR>(&c->fin);   // every MMA issued here is done before TMEM is freed
-        int polls = kDrainLimit;
-        drain(&c->fin, 0, polls);
-        __syncwarp();
     } else if (C::PAIR && warp == 1) {
         // ---------------- the peer's scales: one word a stage to the leader ------------------
         // The warps that wrote the scales have made them visible to the tensor unit (the async proxy)
@@ -843,10 +833,6 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
                 }
             }
         }
-        // sums still in flight (after a wait that gave up) land before the cluster ends
-        int polls = kDrainLimit;
-        if (C::FEW && S > 1 && !ok) drain(&c->rfull, red_parity, polls);
-        __syncwarp();
     } else if (C::MX && warp >= C::SF_WARP) {
         // ---------------- scales: this warp's operand, 128 rows -----------------------------
         // Chunks of 512 inputs (16 scale bytes of a row, two stages), one ahead in registers, over
@@ -909,11 +895,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN>::THREADS, Cfg<MODE, BN>::PER_SM)
     if (a.early) pdl_wait();   // a CTA without tiles too: this grid ends after the one before it
     tc::fence_before_sync();
     __syncthreads();
-    if (C::PAIR && rank == 1 && warp == 1) {   // the leader's last commit, here too
-        int polls = kDrainLimit;
-        drain(&c->fin, 0, polls);
-        __syncwarp();
-    }
+    if (warp == 1) settle(&c->fin, &c->abort);   // (a pair: the leader's last commit, in both CTAs)
     // no CTA of a cluster frees its TMEM or leaves while another may still use its memory
     if (CS > 1) cluster_sync();
     if (warp == 1) {

@@ -31,7 +31,7 @@ __global__ void selftest_wait_kernel(int32_t *err, int polls)
     } else {
         for (int left = polls / 4 + 64; left > 0 && !aborted(&abort); --left) {
             int turn = 64;
-            drain(&bar, 0, turn);
+            poll(&bar, 0, turn);
         }
     }
     __syncthreads();
