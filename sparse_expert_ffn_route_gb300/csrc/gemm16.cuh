@@ -72,7 +72,7 @@ struct Cfg {
     static constexpr int NBUF = MODE == kGate2 ? 1 : 2;
     // Epilogue warps, and columns that one reads at a time.  The gate's two sums fill TMEM, so no MMA
     // runs beside its epilogue: twice the warps on half the columns each (4096 x 6144 x 2048 with
-    // what it keeps 122.6 us, with eight warps 128.4).
+    // what it kept then 122.6 us, with eight warps 128.4; with what it keeps now 124).
     static constexpr int EPI = MODE == kGate2 ? 16 : 8;
     static constexpr int READ = MODE == kGate2 ? 16 : 32;
     static constexpr int MMA_WARP = kWarpEpi + EPI;
