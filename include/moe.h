@@ -296,6 +296,106 @@ int moe_gated_backward(const void *dh, const void *x, long long ldx, const void 
  * for sizes outside the limits. */
 size_t moe_gated_workspace_size(int T, int H, int F, int train);
 
+/* The step between two blocks of the residual stream: a norm behind a block, its gate and
+ * scales, the residual sum, and the norm ahead of the next block, in one pass:
+ *   z = post_w ? y / sqrt(mean(y^2) + eps) * post_w : y
+ *   out = residual_scale * x + branch_scale * gate * z
+ *   n = out / sqrt(mean(out^2) + eps) * pre_w          (of out before it is rounded)
+ *   x, out [T][H] of x_dtype (the stream); y, n [T][H] and the gate of dtype; fp32, bf16 or fp16
+ *   each.  post_w, pre_w [H] fp32.  Rows of x and y ldx and ldy elements apart, 16-byte aligned.
+ *   gate, by gate_kind: MOE_GATE_NONE (gate NULL), MOE_GATE_CHANNEL [H], MOE_GATE_TOKEN [T],
+ *   MOE_GATE_FULL [T][H].
+ *   Without y (NULL; then no gate and no post_w) out = residual_scale * x: a first block's norm.
+ *   out may be NULL (not written), pre_w and n both NULL (no norm), not all three.  post_w may be
+ *   NULL.  out may be x itself and n may be y itself.
+ *   kept [T][2] fp32 or NULL: the rows' two inverse norms, for moe_block_norm_backward.
+ *   A row with mean square + eps = 0 normalises to zeros.  Sums and norms are in fp32.
+ *   H a multiple of 8 in [8, 8192], T in [0, 2^24], eps finite and >= 0.
+ * No workspace; asynchronous on stream. */
+#define MOE_GATE_NONE    0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN   2
+#define MOE_GATE_FULL    3
+int moe_block_norm_forward(const void *x, long long ldx, int x_dtype, const void *y, long long ldy,
+                           const void *gate, int gate_kind, int dtype, const float *post_w,
+                           const float *pre_w, float eps, float residual_scale, float branch_scale,
+                           int T, int H, void *out, void *n, float *kept, void *stream);
+
+/* Its gradients from dout [T][H] (x_dtype) and dn [T][H] (dtype), the operands of the forward
+ * call and what it kept.  Either of dout and dn may be NULL (zero; dn goes with pre_w).  Each of
+ * these may be NULL and is written in full otherwise:
+ *   dx [T][H] x_dtype;  dy [T][H] dtype;  dpost, dpre [H] fp32, summed over the rows;
+ *   dgate: [H] fp32 (MOE_GATE_CHANNEL), [T] fp32 (MOE_GATE_TOKEN), [T][H] dtype (MOE_GATE_FULL).
+ * dx may be dout itself and dy may be dn itself.  T = 0 zeroes the sums over rows.
+ *   workspace: moe_block_norm_workspace_size(T, H) bytes, first 256 zeroed once. */
+int moe_block_norm_backward(const void *x, long long ldx, int x_dtype, const void *y, long long ldy,
+                            const void *gate, int gate_kind, int dtype, const float *post_w,
+                            const float *pre_w, const float *kept, float residual_scale,
+                            float branch_scale, int T, int H, const void *dout, const void *dn,
+                            void *dx, void *dy, void *dgate, float *dpost, float *dpre,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of moe_block_norm_backward; 0 for sizes outside the limits. */
+size_t moe_block_norm_workspace_size(int T, int H);
+
+/* Low-rank adapters of many requests beside a projection that they share:
+ *   y[p] = base[p] + scale[a] * (x[p] down[a]^T) up[a]^T,  a = ids[s],
+ *   for the rows p of segment s, offsets[s] <= p < offsets[s+1].
+ *   x [T][K] with ldx elements between rows, down [adapters][rank][K], up [adapters][N][rank], all
+ *   bf16 or all fp16 (dtype); scale [adapters] fp32 or NULL (1); sums in fp32.
+ *   base, y [T][N] of y_dtype (fp32, bf16 or fp16), rounded once.  base: the shared projection's
+ *   output; y itself (added in place) or NULL (zero).
+ *   offsets [segments+1] int32 in order within [0, T] and ids [segments] int32, on the device: one
+ *   segment a request, of any length, an adapter any number of times.  ids -1: no adapter,
+ *   y = base.  Rows in no segment are left untouched.
+ *   A segment whose offsets are out of order or past the rows is skipped, and recorded; one whose id is
+ *   no adapter becomes NaN, and is recorded (moe_check_errors).
+ *   K, N multiples of 8 in [8, 65536], rank a multiple of 8 in [8, 128] (smaller ones padded with
+ *   zeros), adapters in [1, 2^16], segments in [1, 2^20], T in [0, 2^24], rows of x 16-byte aligned.
+ *   workspace: 256 bytes (the error word), zeroed once before its first use. */
+int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, const void *down,
+                       const void *up, const float *scale, int adapters, int rank, int N,
+                       const int32_t *offsets, const int32_t *ids, int segments, const void *base,
+                       void *y, int y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* How evenly a batch's routing loads the experts.  For each of n_seq sequences s (tokens
+ * seq_offsets[s] <= t < seq_offsets[s+1]) with sig = sigmoid(logits):
+ *   counts [n_seq][E] int32: kept pairs (t, i < keff[t]) of each expert,
+ *   tokens [n_seq] int32: counted tokens,
+ *   loss [1] fp32: the mean over the sequences with tokens of sum_e f_e P_e,
+ *     f_e = E counts[s][e] / sum counts[s],  P_e = mean over its tokens of sig_e / sum sig.
+ * 1 for an even load, E where one expert takes everything; 0 without any token.
+ *   logits [T][E] of dtype (fp32, bf16, fp16), ld elements between rows: the router's, before the
+ *   bias.  -inf scores 0; a token of nothing but -inf adds nothing to P.
+ *   ids [T][K], keff [T] as moe_route writes them.  valid [T] uint8 or NULL: tokens with 0 (padding)
+ *   are not counted and their logits not read.  Tokens in no sequence are not counted.
+ *   cfg gives n_experts and top_k.  A kept id outside [0, E) is left out, a keff outside [0, K] clamped,
+ *   and recorded.  Offsets out of order or outside [0, T] make the loss NaN, and are recorded.
+ *   n_seq in [1, 2^20].  workspace: moe_balance_workspace_size(cfg, T, n_seq) bytes, first 256 zeroed
+ *   once; for one call at a time. */
+int moe_balance_forward(const moe_config *cfg, const void *logits, int dtype, long long ld,
+                        const int32_t *ids, const int32_t *keff, int T, const int32_t *seq_offsets,
+                        int n_seq, const uint8_t *valid, float *loss, int32_t *counts,
+                        int32_t *tokens, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of the logits from the balance loss and from the applied weights:
+ *   dloss [1] fp32 (device) or NULL: the loss's gradient (its coefficient);
+ *   dw [T][K] fp32 or NULL: the gradient of the weights w that moe_route writes, with
+ *   cfg's norm_topk_prob and routed_scaling_factor; slots >= keff are not read.
+ *   The other operands as moe_balance_forward took them, counts and tokens as it wrote them (read with
+ *   dloss).  The counts are constants and the choice has no gradient.
+ *   dlogits [T][E] (dense) of grad_dtype, dtype or fp32, written in full: zero for tokens that are
+ *   not valid or in no sequence. */
+int moe_balance_backward(const moe_config *cfg, const void *logits, int dtype, long long ld,
+                         const int32_t *ids, const int32_t *keff, int T, const int32_t *seq_offsets,
+                         int n_seq, const uint8_t *valid, const int32_t *counts,
+                         const int32_t *tokens, const float *dloss, const float *dw, void *dlogits,
+                         int grad_dtype, void *stream);
+
+/* Bytes of workspace of moe_balance_forward for up to max_tokens tokens in up to max_seq
+ * sequences; 0 for an invalid config or count. */
+size_t moe_balance_workspace_size(const moe_config *cfg, int max_tokens, int max_seq);
+
 /* Diagnostic of the error path of the kernels' bounded device-side waits: a
  * pair of CTAs waits on mbarriers that nothing arrives at.  One warp polls
  * `polls` times (1 .. 2^24), gives up, records the timeout in the workspace's

@@ -35,6 +35,10 @@ MOE_FFN_ROW_GEMV = 2
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 MOE_DTYPE_F16 = 2
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
 STAGES = ("router", "select", "permute", "plan", "quant", "gate_up", "quant_h", "down", "combine")
 
 # every symbol include/moe.h declares
@@ -46,7 +50,9 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_expert_ffn", "
            "moe_layer_forward_host", "moe_ffn_path", "moe_ffn_path_down",
            "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_mxfp4_matmul", "moe_mxfp4_expert_ffn",
            "moe_mxfp4_workspace_size", "moe_gated_forward", "moe_gated_backward",
-           "moe_gated_workspace_size")
+           "moe_gated_workspace_size", "moe_block_norm_forward", "moe_block_norm_backward",
+           "moe_block_norm_workspace_size", "moe_balance_forward", "moe_balance_backward",
+           "moe_balance_workspace_size", "moe_adapter_matmul")
 
 
 class MoeError(RuntimeError):
@@ -142,6 +148,17 @@ def load_library():
                                      sz, vp]
     L.moe_gated_workspace_size.argtypes = [i32, i32, i32, i32]
     L.moe_gated_workspace_size.restype = sz
+    f32 = ctypes.c_float
+    L.moe_block_norm_forward.argtypes = [vp, i64, i32, vp, i64, vp, i32, i32, vp, vp, f32, f32, f32, i32, i32, vp, vp, vp, vp]
+    L.moe_block_norm_backward.argtypes = [vp, i64, i32, vp, i64, vp, i32, i32, vp, vp, vp, f32, f32, i32, i32, vp, vp, vp, vp,
+                                          vp, vp, vp, vp, sz, vp]
+    L.moe_block_norm_workspace_size.argtypes = [i32, i32]
+    L.moe_block_norm_workspace_size.restype = sz
+    L.moe_balance_forward.argtypes = [vp, vp, i32, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_balance_backward.argtypes = [vp, vp, i32, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp]
+    L.moe_balance_workspace_size.argtypes = [vp, i32, i32]
+    L.moe_balance_workspace_size.restype = sz
+    L.moe_adapter_matmul.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, i32, vp, sz, vp]
     L.moe_last_error_string.argtypes = []
     L.moe_last_error_string.restype = ctypes.c_char_p
     _lib = L
@@ -536,3 +553,171 @@ def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace,
         _dtype(x, "x"), T, H, F, opt(dx, "dx", (T, H)), opt(dw_gate, "dw_gate", (F, H)),
         opt(dw_up, "dw_up", (F, H)), _space(workspace, dev), workspace.numel(),
         _raw_stream(stream, dev)), "moe_gated_backward")
+
+
+# --- Around the expert layer: norms between blocks, the routing's balance, adapters ---------------------
+def _opt(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> Optional[int]:
+    return None if t is None else _dense(t, name, shape, dtype, device)
+
+
+def _strided(t: torch.Tensor, name: str, rows: int, width: int, device: int):
+    """(pointer, row stride) of a 2-D tensor [rows][width] on `device` whose rows are contiguous."""
+    dev, r, w, ld = _rows(t, name)
+    if (r, w) != (rows, width) or dev != device:
+        raise ValueError("%s must be [%d][%d] on device %d (got %s on %s)" % (name, rows, width, device, tuple(t.shape), t.device))
+    return t.data_ptr(), ld
+
+
+def _gate(gate, dgate, T: int, H: int, dtype, device: int):
+    """(pointer, kind) of a gate [H] or [1][H], [T][1] or [T], or [T][H].  Of [1][H] for one token the
+    gradient's type tells: a channel's is float32."""
+    if gate is None:
+        return None, MOE_GATE_NONE
+    shape = tuple(gate.shape)
+    if shape == (T, H) and not (T == 1 and dgate is not None and dgate.dtype is torch.float32 and dtype is not torch.float32):
+        kind = MOE_GATE_FULL
+    elif shape in ((H,), (1, H)):
+        kind = MOE_GATE_CHANNEL
+    elif shape in ((T, 1), (T,)):
+        kind = MOE_GATE_TOKEN
+    else:
+        raise ValueError("gate must be [H], [T][1] or [T][H] for T %d, H %d (got %s)" % (T, H, shape))
+    return _dense(gate, "gate", shape, dtype, device), kind
+
+
+def moe_block_norm_workspace_size(T: int, H: int) -> int:
+    return int(load_library().moe_block_norm_workspace_size(T, H))
+
+
+def alloc_block_norm_workspace(T: int, H: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_block_norm_backward for T rows of H, its head zeroed."""
+    n = moe_block_norm_workspace_size(T, H)
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_block_norm_workspace_size", "sizes outside the limits")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_block_norm_forward(x, eps, y=None, post_w=None, gate=None, pre_w=None, out=None, n=None, residual_scale=1.0,
+                           branch_scale=1.0, kept=None, stream=None):
+    """The step between two blocks: out [T][H] = residual_scale * x + branch_scale * gate * z, z = y or, with
+    post_w, its RMSNorm times post_w; n = the RMSNorm of out times pre_w.  x and out are of the residual
+    stream's type, y, gate and n of the blocks', each float32, bfloat16 or float16; post_w, pre_w [H] and
+    kept [T][2] (for moe_block_norm_backward) float32.  gate: [H], [T][1] or [T][H].  Rows of x and y may be
+    strided.  Without y, a first block's norm."""
+    dev, T, H, ld = _rows(x, "x")
+    f32 = torch.float32
+    like = y if y is not None else n if n is not None else x
+    dt = like.dtype
+    py, ldy = (None, 0) if y is None else _strided(y, "y", T, H, dev)
+    pg, kind = _gate(gate, None, T, H, dt, dev)
+    rc = load_library().moe_block_norm_forward(
+        x.data_ptr(), ld, _dtype(x, "x"), py, ldy, pg, kind, _dtype(like, "y"), _opt(post_w, "post_w", (H,), f32, dev),
+        _opt(pre_w, "pre_w", (H,), f32, dev), eps, residual_scale, branch_scale, T, H, _opt(out, "out", (T, H), x.dtype, dev),
+        _opt(n, "n", (T, H), dt, dev), _opt(kept, "kept", (T, 2), f32, dev), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_block_norm_forward")
+
+
+def moe_block_norm_backward(x, kept, workspace, y=None, post_w=None, gate=None, pre_w=None, dout=None, dn=None, dx=None, dy=None,
+                            dgate=None, dpost=None, dpre=None, residual_scale=1.0, branch_scale=1.0, stream=None):
+    """Gradients of moe_block_norm_forward from dout [T][H] (x's type) and dn [T][H] (y's), either None: dx (x's
+    type), dy (y's), dpost, dpre [H] float32, and dgate, float32 in the gate's shape or for a gate [T][H] of its
+    type.  A gradient that is None is not formed."""
+    dev, T, H, ld = _rows(x, "x")
+    f32 = torch.float32
+    like = y if y is not None else dn if dn is not None else x
+    dt = like.dtype
+    py, ldy = (None, 0) if y is None else _strided(y, "y", T, H, dev)
+    pg, kind = _gate(gate, dgate, T, H, dt, dev)
+    pdg = None
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        pdg = _dense(dgate, "dgate", tuple(gate.shape), dt if kind == MOE_GATE_FULL else f32, dev)
+    rc = load_library().moe_block_norm_backward(
+        x.data_ptr(), ld, _dtype(x, "x"), py, ldy, pg, kind, _dtype(like, "y"), _opt(post_w, "post_w", (H,), f32, dev),
+        _opt(pre_w, "pre_w", (H,), f32, dev), _dense(kept, "kept", (T, 2), f32, dev), residual_scale, branch_scale, T, H,
+        _opt(dout, "dout", (T, H), x.dtype, dev), _opt(dn, "dn", (T, H), dt, dev), _opt(dx, "dx", (T, H), x.dtype, dev),
+        _opt(dy, "dy", (T, H), dt, dev), pdg, _opt(dpost, "dpost", (H,), f32, dev), _opt(dpre, "dpre", (H,), f32, dev),
+        _space(workspace, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_block_norm_backward")
+
+
+def moe_balance_workspace_size(cfg: MoeConfig, max_tokens: int, max_seq: int) -> int:
+    return int(load_library().moe_balance_workspace_size(ctypes.byref(cfg), max_tokens, max_seq))
+
+
+def alloc_balance_workspace(cfg: MoeConfig, max_tokens: int, max_seq: int, device="cuda") -> torch.Tensor:
+    """Workspace of moe_balance_forward for up to ``max_tokens`` tokens in up to ``max_seq`` sequences, its head zeroed."""
+    n = moe_balance_workspace_size(cfg, max_tokens, max_seq)
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_balance_workspace_size", "invalid config or count")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _balance(cfg, logits, ids, keff, seq_offsets, counts, tokens, valid):
+    """The operands that both directions take: (device, T, the first arguments, counts and tokens)."""
+    dev, T, E, ld = _rows(logits, "logits")
+    S, K, i32 = seq_offsets.numel() - 1, cfg.top_k, torch.int32
+    if E != cfg.n_experts:
+        raise ValueError("logits must have n_experts = %d columns (got %d)" % (cfg.n_experts, E))
+    return (dev, T, [ctypes.byref(cfg), logits.data_ptr(), _dtype(logits, "logits"), ld, _dense(ids, "ids", (T, K), i32, dev),
+                     _dense(keff, "keff", (T,), i32, dev), T, _dense(seq_offsets, "seq_offsets", (S + 1,), i32, dev), S,
+                     _opt(valid, "valid", (T,), torch.uint8, dev)],
+            [_dense(counts, "counts", (S, E), i32, dev), _dense(tokens, "tokens", (S,), i32, dev)])
+
+
+def moe_balance_forward(cfg, logits, ids, keff, seq_offsets, loss, counts, tokens, workspace, valid=None, stream=None):
+    """How evenly a routing loads the experts: counts [S][E] int32 (kept pairs of each sequence and expert),
+    tokens [S] int32 (counted tokens) and loss [1] float32, from the router's logits [T][E] (float32, bfloat16 or
+    float16; rows may be strided) and moe_route's ids [T][K], keff [T].  seq_offsets [S + 1] int32; valid [T] uint8
+    (None: all): tokens with 0 are left out."""
+    dev, _, args, kept = _balance(cfg, logits, ids, keff, seq_offsets, counts, tokens, valid)
+    rc = load_library().moe_balance_forward(*args, _dense(loss, "loss", (1,), torch.float32, dev), *kept, _space(workspace, dev),
+                                            workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_balance_forward")
+
+
+def moe_balance_backward(cfg, logits, ids, keff, seq_offsets, counts, tokens, dlogits, dloss=None, dw=None, valid=None,
+                         stream=None):
+    """dlogits [T][E] (float32 or the logits' type) from dloss [1] float32, the balance loss's gradient, and dw [T][K]
+    float32, that of the weights moe_route applies (either may be None).  counts and tokens as
+    moe_balance_forward wrote them."""
+    dev, T, args, kept = _balance(cfg, logits, ids, keff, seq_offsets, counts, tokens, valid)
+    f32 = torch.float32
+    rc = load_library().moe_balance_backward(
+        *args, *kept, _opt(dloss, "dloss", (1,), f32, dev), _opt(dw, "dw", (T, cfg.top_k), f32, dev),
+        _dense(dlogits, "dlogits", (T, cfg.n_experts), dlogits.dtype, dev), _dtype(dlogits, "dlogits"), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_balance_backward")
+
+
+def alloc_adapter_workspace(device="cuda") -> torch.Tensor:
+    """Zeroed workspace of moe_adapter_matmul (the error word)."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def moe_adapter_matmul(x, down, up, scale, offsets, ids, y, workspace, base=None, stream=None):
+    """y = base + scale[a] * (x down[a]^T) up[a]^T with a = ids[s] for the rows of segment s: x [T][K] (rows may be
+    strided), down [A][R][K], up [A][N][R], all bfloat16 or all float16; scale [A] float32 or None; offsets [S + 1],
+    ids [S] int32 (-1: no adapter); base, y [T][N] of one type, base y itself or None (zero)."""
+    dev, T, K, ld = _rows(x, "x")
+    dt = x.dtype
+    if down.dim() != 3 or up.dim() != 3:
+        raise ValueError("down must be [A][R][K] and up [A][N][R]")
+    A, R, N = down.shape[0], down.shape[1], up.shape[1]
+    S = ids.numel()
+    rc = load_library().moe_adapter_matmul(
+        x.data_ptr(), ld, _dtype(x, "x"), T, K, _dense(down, "down", (A, R, K), dt, dev), _dense(up, "up", (A, N, R), dt, dev),
+        _opt(scale, "scale", (A,), torch.float32, dev), A, R, N, _dense(offsets, "offsets", (S + 1,), torch.int32, dev),
+        _dense(ids, "ids", (S,), torch.int32, dev), S, _opt(base, "base", (T, N), y.dtype, dev),
+        _dense(y, "y", (T, N), y.dtype, dev), _dtype(y, "y"), _space(workspace, dev), workspace.numel(),
+        _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_adapter_matmul")

@@ -1,0 +1,307 @@
+// adapter.cu -- low-rank adapters of many requests beside a projection they share:
+//   y[p] = base[p] + scale[a] (x[p] down[a]^T) up[a]^T,  a = ids[s], for the rows p of segment s.
+//
+// Few rows a segment (a decode batch).  A cluster of 8 CTAs takes up to 8 rows of one segment: each CTA
+// forms the rows' R numbers over its eighth of the inputs, the eighths are added in rank order through
+// distributed shared memory, and each CTA writes its eighth of the outputs.  One launch, nothing goes
+// through global memory in between.
+#include <algorithm>
+
+#include "cluster_wait.cuh"
+#include "launch.cuh"
+#include "moe_internal.cuh"
+#include "vec8.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxRank = 128, kMaxAdapterDim = 65536, kMaxAdapters = 1 << 16, kMaxSegments = 1 << 20;
+constexpr int kFewRows = 8;       // rows of a tile
+constexpr int kFewCluster = 8;
+constexpr int kFewThreads = 256;
+
+struct AdapterArgs {
+    const void *x;
+    long long ldx;
+    const void *down, *up;
+    const float *scale;
+    const int32_t *offsets, *ids;
+    const void *base;
+    void *y;
+    int T, S, K, N, R, A;
+    int32_t *err;
+};
+
+// Tiles of `rows` rows on a fixed grid over the batch, cut by the segments: the part of grid cell c that is
+// segment s's is tile c + s.  (A later part has a later cell or a later segment, so no two share a number.)
+struct Tile {
+    int lo, hi;      // rows; empty where the number is not used
+    int adapter;     // -1: none
+    bool bad;        // not an adapter: the rows become NaN
+};
+
+// by one warp
+__device__ __forceinline__ Tile find_tile(const AdapterArgs &p, int tile, int rows, int lane)
+{
+    Tile t = {0, 0, -1, false};
+    int s = 0, n = p.S;      // the last segment whose first tile is `tile` or before it lies in [s, s + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const bool before = at < n && p.offsets[s + at] / rows + s + at <= tile;
+        const int got = __popc(__ballot_sync(0xffffffffu, before));
+        if (got == 0) return t;
+        n = min(step, n - (got - 1) * step);
+        s += (got - 1) * step;
+    }
+    const int cell = tile - s, from = p.offsets[s], to = p.offsets[s + 1];
+    if (cell < 0 || from < 0 || from > to || to > p.T) return t;
+    t.lo = max(from, cell * rows);
+    t.hi = (int)min((long long)to, ((long long)cell + 1) * rows);
+    t.adapter = p.ids[s];
+    t.bad = t.adapter < -1 || t.adapter >= p.A;
+    return t;
+}
+
+// what is wrong with segment s, recorded
+__device__ __forceinline__ void check_segment(const AdapterArgs &p, int s)
+{
+    const int from = p.offsets[s], to = p.offsets[s + 1], id = p.ids[s];
+    if (from < 0 || from > to || to > p.T) atomicOr(p.err, kErrBadOffsets);
+    if (id < -1 || id >= p.A) atomicOr(p.err, kErrBadAdapter);
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// part[m][r] = sum over this CTA's inputs of x[m] down[r], M rows, four r of a warp at a time
+template <typename T, int M>
+__device__ __forceinline__ void few_down(const T *xs, int width, const T *down, long long ldd, int R, float *part, int warp, int lane)
+{
+    constexpr int U = 4;
+    for (int r0 = warp * U; r0 < R; r0 += kFewThreads / 32 * U) {
+        float acc[U * M];
+#pragma unroll
+        for (int i = 0; i < U * M; ++i) acc[i] = 0.0f;
+        for (int k = lane * 8; k < width; k += 256) {
+            Vec8<T> d[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) d[u].load(down + (r0 + u) * ldd + k);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                Vec8<T> x;
+                x.load(xs + (size_t)m * width + k);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[u * M + m] = fmaf(x.get(i), d[u].get(i), acc[u * M + m]);
+            }
+        }
+        constexpr int V = U * M;   // a power of two, at most 32
+        ReduceScatter<V, 16>::run(acc, lane);
+        constexpr int shift = 5 - ilog2(V);
+        const int i = lane >> shift;
+        if ((lane & ((1 << shift) - 1)) == 0) part[(i % M) * kMaxRank + r0 + i / M] = acc[0];
+    }
+}
+
+template <typename T, typename Y, int M>
+__device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, const float *u, const T *up, float scale, int n0, int n1)
+{
+    const int rows = t.hi - t.lo;
+    for (int n = n0 + threadIdx.x; n < n1; n += kFewThreads) {
+        float acc[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[m] = 0.0f;
+        const T *b = up + (size_t)n * p.R;
+        for (int r = 0; r < p.R; r += 8) {
+            Vec8<T> v;
+            v.load(b + r);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                Vec8<float> w;
+                w.load(u + m * kMaxRank + r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[m] = fmaf(w.get(i), v.get(i), acc[m]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            if (m < rows) {
+                const size_t at = (size_t)(t.lo + m) * p.N + n;
+                const float had = p.base ? to_f32(static_cast<const Y *>(p.base)[at]) : 0.0f;
+                from_f32(static_cast<Y *>(p.y)[at], fmaf(scale, acc[m], had));
+            }
+    }
+}
+
+template <typename T, typename Y>
+__global__ void __launch_bounds__(kFewThreads) adapter_few_kernel(const AdapterArgs p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float s_part[kFewRows * kMaxRank], s_u[kFewRows * kMaxRank];
+    __shared__ Tile s_tile;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tile = blockIdx.x / kFewCluster, rank = blockIdx.x % kFewCluster;
+    if (warp == 0) {
+        const Tile t = find_tile(p, tile, kFewRows, lane);
+        if (lane == 0) s_tile = t;
+        if (lane == 0 && rank == 0 && tile < p.S) check_segment(p, tile);
+    }
+    __syncthreads();
+    const Tile t = s_tile;
+    const int rows = t.hi - t.lo;
+    if (rows <= 0) return;                       // (the same for the whole cluster)
+    const int nslice = (p.N / 8 + kFewCluster - 1) / kFewCluster * 8;
+    const int n0 = min(p.N, rank * nslice), n1 = min(p.N, n0 + nslice);
+    if (t.adapter < 0 || t.bad) {
+        for (int m = t.lo; m < t.hi; ++m)
+            for (int n = n0 + tid; n < n1; n += kFewThreads) {
+                const size_t at = (size_t)m * p.N + n;
+                Y v;
+                if (t.bad) from_f32(v, __int_as_float(0x7fc00000));
+                else if (p.base) v = static_cast<const Y *>(p.base)[at];
+                else from_f32(v, 0.0f);
+                static_cast<Y *>(p.y)[at] = v;
+            }
+        return;
+    }
+    const int kslice = (p.K / 8 + kFewCluster - 1) / kFewCluster * 8;
+    const int k0 = min(p.K, rank * kslice), width = min(p.K, k0 + kslice) - k0;
+    const int m_up = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
+    T *xs = reinterpret_cast<T *>(smem);
+    for (int i = tid * 8; i < m_up * width; i += kFewThreads * 8) {
+        const int m = i / width, k = i - m * width;
+        Vec8<T> v;
+        if (m < rows) v.load(static_cast<const T *>(p.x) + (size_t)(t.lo + m) * p.ldx + k0 + k);
+        else v.zero();
+        v.store(xs + i);
+    }
+    __syncthreads();
+    const T *down = static_cast<const T *>(p.down) + (size_t)t.adapter * p.R * p.K + k0;
+    switch (m_up) {
+    case 1: few_down<T, 1>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
+    case 2: few_down<T, 2>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
+    case 4: few_down<T, 4>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
+    default: few_down<T, 8>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
+    }
+    cluster_sync();
+    for (int i = tid; i < m_up * p.R; i += kFewThreads) {
+        const int at = i / p.R * kMaxRank + i % p.R;
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kFewCluster; ++c) sum += ld_cluster_f32(map_rank(smem_u32(s_part + at), c));
+        s_u[at] = sum;
+    }
+    __syncthreads();
+    const T *up = static_cast<const T *>(p.up) + (size_t)t.adapter * p.N * p.R;
+    const float scale = p.scale ? p.scale[t.adapter] : 1.0f;
+    switch (m_up) {
+    case 1: few_up<T, Y, 1>(p, t, s_u, up, scale, n0, n1); break;
+    case 2: few_up<T, Y, 2>(p, t, s_u, up, scale, n0, n1); break;
+    case 4: few_up<T, Y, 4>(p, t, s_u, up, scale, n0, n1); break;
+    default: few_up<T, Y, 8>(p, t, s_u, up, scale, n0, n1); break;
+    }
+    cluster_sync();   // no CTA leaves while another reads its sums
+}
+
+// f(T()) of the two 16-bit types
+template <typename F>
+auto with_half(int dtype, F &&f)
+{
+    return dtype == MOE_DTYPE_BF16 ? f(__nv_bfloat16()) : f(__half());
+}
+
+cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_t st)
+{
+    const long long tiles = (p.T + kFewRows - 1) / kFewRows + p.S;
+    const size_t smem = (size_t)kFewRows * ((p.K / 8 + kFewCluster - 1) / kFewCluster * 8) * 2;
+    return with_half(dtype, [&](auto t) {
+        return with_dtype(y_dtype, [&](auto y) {
+            return launch_kernel(adapter_few_kernel<decltype(t), decltype(y)>, dim3((unsigned)(tiles * kFewCluster)), dim3(kFewThreads),
+                                 smem, st, kFewCluster, p);
+        });
+    });
+}
+
+bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
+
+int done(cudaError_t e, const char *what)
+{
+    if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return set_error(MOE_OK, "%s", "");
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+#define ADAPTER_PTR(p, a)                                                                               \
+    do {                                                                                                \
+        if (!(p)) return set_error(MOE_ERR_ARG, "%s is NULL", #p);                                      \
+        if (off((p), (a))) return set_error(MOE_ERR_ALIGN, "%s is not %d-byte aligned", #p, (int)(a));  \
+    } while (0)
+
+extern "C" {
+
+int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, const void *down, const void *up, const float *scale,
+                       int adapters, int rank, int N, const int32_t *offsets, const int32_t *ids, int segments, const void *base,
+                       void *y, int y_dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) return set_error(MOE_ERR_ARG, "dtype must be bf16 or fp16 (got %d)", dtype);
+    if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16 && y_dtype != MOE_DTYPE_F16)
+        return set_error(MOE_ERR_ARG, "unknown dtype %d", y_dtype);
+    if (T < 0 || T > 1 << 24) return set_error(MOE_ERR_SHAPE, "T must be in [0, 2^24] (got %d)", T);
+    if (K < 8 || K > kMaxAdapterDim || K % 8)
+        return set_error(MOE_ERR_SHAPE, "K must be a multiple of 8 in [8, %d] (got %d)", kMaxAdapterDim, K);
+    if (N < 8 || N > kMaxAdapterDim || N % 8)
+        return set_error(MOE_ERR_SHAPE, "N must be a multiple of 8 in [8, %d] (got %d)", kMaxAdapterDim, N);
+    if (rank < 8 || rank > kMaxRank || rank % 8)
+        return set_error(MOE_ERR_SHAPE, "rank must be a multiple of 8 in [8, %d] (got %d)", kMaxRank, rank);
+    if (adapters < 1 || adapters > kMaxAdapters) return set_error(MOE_ERR_SHAPE, "adapters must be in [1, 2^16] (got %d)", adapters);
+    if (segments < 1 || segments > kMaxSegments) return set_error(MOE_ERR_SHAPE, "segments must be in [1, 2^20] (got %d)", segments);
+    if (ldx < K) return set_error(MOE_ERR_SHAPE, "ldx must be at least K (got %lld)", ldx);
+    if (ldx % 8) return set_error(MOE_ERR_ALIGN, "rows of x are not 16-byte aligned (ldx %lld)", ldx);
+    if (T == 0) return done(cudaSuccess, "");
+    ADAPTER_PTR(x, 16);
+    ADAPTER_PTR(down, 16);
+    ADAPTER_PTR(up, 16);
+    ADAPTER_PTR(offsets, 4);
+    ADAPTER_PTR(ids, 4);
+    ADAPTER_PTR(y, 16);
+    if (off(base, 16)) return set_error(MOE_ERR_ALIGN, "base is not 16-byte aligned");
+    if (off(scale, 4)) return set_error(MOE_ERR_ALIGN, "scale is not 4-byte aligned");
+    if (!workspace) return set_error(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (off(workspace, 256)) return set_error(MOE_ERR_ALIGN, "workspace is not 256-byte aligned");
+    if (workspace_bytes < 256) return set_error(MOE_ERR_WORKSPACE, "workspace has %zu bytes; 256 needed", workspace_bytes);
+    if ((rc = require_device())) return rc;
+    AdapterArgs p = {};
+    p.x = x;
+    p.ldx = ldx;
+    p.down = down;
+    p.up = up;
+    p.scale = scale;
+    p.offsets = offsets;
+    p.ids = ids;
+    p.base = base;
+    p.y = y;
+    p.T = T;
+    p.S = segments;
+    p.K = K;
+    p.N = N;
+    p.R = rank;
+    p.A = adapters;
+    p.err = static_cast<int32_t *>(workspace);
+    return done(launch_adapter(p, dtype, y_dtype, (cudaStream_t)stream), "adapter launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,605 @@
+// balance.cu -- how evenly a batch's routing loads the experts, and the gradient of the router's logits.
+//
+// Of sequence s with L counted tokens and c[s][e] kept pairs of expert e, C = sum_e c, and the router's scores
+// sig = 1 / (1 + exp(-l)) normalised to p = sig / sum_e sig:
+//   f[s][e] = E c[s][e] / C,  P[s][e] = sum_t p / L,  loss = mean over sequences with L > 0 of sum_e f P.
+// (One for an even load; f counts and has no gradient.)  Backward, with G_e = dloss f / (L n) and the
+// applied weights w_i = scale g_i / sum_j g_j, g_i = sig of the kept expert i:
+//   dl_e  = (G_e - sum_j G_j p_j) p_e (1 - sig_e)
+//   dl_i += scale h_i (1 - sig_i) (dw_i - sum_j h_j dw_j),  h = g / sum g
+//           (without norm_topk_prob: scale sig_i (1 - sig_i) dw_i).
+//
+// Scores far below zero are taken relative to the largest, t = exp(l - m) / (1 + exp(l)), so that p keeps its
+// digits where every sig is a denormal number or zero.
+//
+// A warp holds a token's row, E / 32 logits a lane.  Both directions are one read of the logits: bound by
+// memory for the widths of a router (256 fp32 logits are 1 KB a token).
+#include <algorithm>
+
+#include "launch.cuh"
+#include "moe_internal.cuh"
+#include "vec8.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kMaxChunks = 608;      // four CTAs an SM
+constexpr int kMinChunk = kWarps;    // tokens: one a warp
+constexpr int kMaxSequences = 1 << 20;
+
+struct BalanceArgs {
+    const void *logits;
+    long long ld;
+    const int32_t *ids, *keff, *offsets;
+    const uint8_t *valid;
+    int T, E, K, S, chunk;
+    // sums of a chunk's part of a sequence, in slot (chunk + sequence): a later part has a later chunk or
+    // a later sequence, so no two share a slot and a sequence's are consecutive
+    float *psum;       // [slots][E]
+    int32_t *pcount;   // [slots][E]
+    int32_t *pmeta;    // [slots][2] counted tokens, kept pairs
+    float *ploss;      // [S][blocks of 32 experts]
+    float *loss;
+    int32_t *counts, *tokens;
+    int32_t *err, *ticket;
+    // backward
+    const float *dloss, *dw;
+    void *dlogits;
+    float scale;
+    int norm;
+};
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// A lane's part of a row: VEC 4 takes groups of four consecutive logits, VEC 1 every 32nd one.
+template <int VEC>
+__device__ __forceinline__ int expert_of(int j, int lane)
+{
+    return VEC == 4 ? ((j >> 2) * 32 + lane) * 4 + (j & 3) : j * 32 + lane;
+}
+
+template <typename T, int PER, int VEC>
+__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&l)[PER])
+{
+    if constexpr (VEC == 4) {
+#pragma unroll
+        for (int j = 0; j < PER; j += 4) {
+            const int e = expert_of<4>(j, lane);
+            union {
+                uint2 w[sizeof(T) / 2];
+                T t[4];
+            } u;
+            if (e < E) {
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(&u) = *reinterpret_cast<const uint4 *>(row + e);
+                else u.w[0] = *reinterpret_cast<const uint2 *>(row + e);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[j + i] = e < E ? to_f32(u.t[i]) : kNegInf;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = expert_of<1>(j, lane);
+            l[j] = e < E ? to_f32(row[e]) : kNegInf;
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+constexpr float kLow = -60.0f;   // sums of scores above exp(-60) are far from fp32's smallest numbers
+
+// t: scores of this lane's N logits up to a common factor; rest: 1 - sig.  A row of nothing but -inf has t = 0.
+template <int N>
+__device__ __forceinline__ void scores(const float (&l)[N], float (&t)[N], float (&rest)[N])
+{
+    bool high = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float q = __expf(-fabsf(l[j])), r = __fdividef(1.0f, 1.0f + q);
+        t[j] = l[j] > 0.0f ? r : q * r;
+        rest[j] = l[j] > 0.0f ? q * r : r;
+        high |= l[j] > kLow;
+    }
+    if (__any_sync(0xffffffffu, high)) return;
+    float m = kNegInf;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
+    m = warp_max(m);
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = l[j] == kNegInf ? 0.0f : expf(l[j] - m);   // (1 + exp(l) is 1; NaN stays)
+}
+
+// the last sequence that begins at or before token t
+__device__ __forceinline__ int sequence_of(const int32_t *offsets, int S, int t)
+{
+    int lo = 0, hi = S;   // offsets[lo] <= t (or lo = 0) < offsets[hi] (or hi = S)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (offsets[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <typename T, int PER, int VEC>
+__global__ void __launch_bounds__(32 * kWarps) balance_parts_kernel(const BalanceArgs p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ float s_sum[kWarps][kMaxExperts];
+    __shared__ int s_count[kMaxExperts], s_meta[2], s_seq;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
+    if (tid == 0) s_seq = sequence_of(p.offsets, p.S, begin);
+    for (int e = tid; e < p.E; e += 32 * kWarps) s_count[e] = 0;
+    if (tid < 2) s_meta[tid] = 0;
+    __syncthreads();
+    for (int s = s_seq; s < p.S; ++s) {
+        const int lo = max(p.offsets[s], begin), hi = min(p.offsets[s + 1], end);
+        if (p.offsets[s] >= end) break;
+        if (lo >= hi) continue;
+        float sum[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
+        int counted = 0;
+        for (int t = lo + warp; t < hi; t += kWarps) {
+            if (p.valid && !p.valid[t]) continue;
+            ++counted;
+            float l[PER], v[PER], rest[PER];
+            load_row<T, PER, VEC>(static_cast<const T *>(p.logits) + (size_t)t * p.ld, p.E, lane, l);
+            scores(l, v, rest);
+            float total = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) total += v[j];
+            total = warp_sum(total);
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+        }
+        int pairs = 0;
+        for (int i = tid; i < (hi - lo) * p.K; i += 32 * kWarps) {
+            const int t = lo + i / p.K, k = i % p.K;
+            if (p.valid && !p.valid[t]) continue;
+            const int kept = p.keff[t];
+            if (k == 0 && (kept < 0 || kept > p.K)) atomicOr(p.err, kErrBadKeff);
+            if (k >= kept) continue;
+            const int e = p.ids[(size_t)t * p.K + k];
+            if (e < 0 || e >= p.E) {
+                atomicOr(p.err, kErrBadExpertId);
+                continue;
+            }
+            atomicAdd(&s_count[e], 1);
+            ++pairs;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = expert_of<VEC>(j, lane);
+            if (e < p.E) s_sum[warp][e] = sum[j];
+        }
+        if (lane == 0 && counted) atomicAdd(&s_meta[0], counted);
+        if (pairs) atomicAdd(&s_meta[1], pairs);
+        __syncthreads();
+        const size_t slot = (size_t)blockIdx.x + s;
+        for (int e = tid; e < p.E; e += 32 * kWarps) {
+            float v = s_sum[0][e];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) v += s_sum[w][e];
+            p.psum[slot * p.E + e] = v;
+            p.pcount[slot * p.E + e] = s_count[e];
+            s_count[e] = 0;
+        }
+        if (tid < 2) {
+            p.pmeta[slot * 2 + tid] = s_meta[tid];
+            s_meta[tid] = 0;
+        }
+        __syncthreads();
+    }
+}
+
+// A sequence's sums for 32 experts a CTA; the last CTA adds up the loss.
+__global__ void __launch_bounds__(32 * kWarps) balance_loss_kernel(const BalanceArgs p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ float s_sum[kWarps][32];
+    __shared__ int s_count[kWarps][32], s_meta[2], s_last, s_used, s_bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s = blockIdx.x, e = blockIdx.y * 32 + lane;
+    if (tid < 2) s_meta[tid] = 0;
+    __syncthreads();
+    const int lo = p.offsets[s], hi = p.offsets[s + 1];
+    const bool bad = lo < 0 || lo > hi || hi > p.T;
+    int first = 0, last = -1;
+    if (!bad && lo < hi) {
+        first = lo / p.chunk + s;
+        last = (hi - 1) / p.chunk + s;
+    }
+    float sum = 0.0f;
+    int count = 0, meta[2] = {0, 0};
+    if (e < p.E)
+        for (int i = first + warp; i <= last; i += kWarps) {
+            sum += p.psum[(size_t)i * p.E + e];
+            count += p.pcount[(size_t)i * p.E + e];
+        }
+    for (int i = first + tid; i <= last; i += 32 * kWarps) {
+        meta[0] += p.pmeta[2 * i];
+        meta[1] += p.pmeta[2 * i + 1];
+    }
+    s_sum[warp][lane] = sum;
+    s_count[warp][lane] = count;
+    if (meta[0]) atomicAdd(&s_meta[0], meta[0]);
+    if (meta[1]) atomicAdd(&s_meta[1], meta[1]);
+    __syncthreads();
+    if (warp == 0) {
+        for (int w = 1; w < kWarps; ++w) {
+            sum += s_sum[w][lane];
+            count += s_count[w][lane];
+        }
+        if (e < p.E) p.counts[(size_t)s * p.E + e] = count;
+        const int tokens = s_meta[0], pairs = s_meta[1];
+        float part = e < p.E && pairs > 0 ? (float)count * ((float)p.E / (float)pairs) * (sum / (float)max(tokens, 1)) : 0.0f;
+        part = warp_sum(part);
+        if (lane == 0) {
+            p.ploss[(size_t)s * gridDim.y + blockIdx.y] = part;
+            if (blockIdx.y == 0) p.tokens[s] = tokens;
+            __threadfence();
+            s_last = atomicAdd(p.ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
+        }
+    }
+    if (tid == 0) s_used = s_bad = 0;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    int used = 0, wrong = 0;
+    for (int i = tid; i < p.S; i += 32 * kWarps) {
+        used += __ldcg(p.tokens + i) > 0;
+        wrong |= p.offsets[i] < 0 || p.offsets[i] > p.offsets[i + 1] || p.offsets[i + 1] > p.T;
+    }
+    float total = 0.0f;
+    for (long long i = tid; i < (long long)p.S * gridDim.y; i += 32 * kWarps) total += __ldcg(p.ploss + i);
+    total = warp_sum(total);
+    if (lane == 0) s_sum[0][warp] = total;
+    if (used) atomicAdd(&s_used, used);
+    if (wrong) atomicOr(&s_bad, 1);
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kWarps; ++w) total += s_sum[0][w];
+        if (s_bad) atomicOr(p.err, kErrBadOffsets);
+        p.loss[0] = s_bad ? __int_as_float(0x7fc00000) : s_used ? total / (float)s_used : 0.0f;
+        *p.ticket = 0;
+    }
+}
+
+template <typename T, typename G, int PER, int VEC>
+__global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const BalanceArgs p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ float s_add[kWarps][kMaxExperts];
+    __shared__ int s_used;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float *add = s_add[warp];
+    const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
+    if (tid == 0) s_used = 0;
+    if (p.dw)
+        for (int e = lane; e < p.E; e += 32) add[e] = 0.0f;
+    __syncthreads();
+    if (p.dloss) {
+        int used = 0;
+        for (int i = tid; i < p.S; i += 32 * kWarps) used += p.tokens[i] > 0;
+        used = __reduce_add_sync(0xffffffffu, used);
+        if (lane == 0 && used) atomicAdd(&s_used, used);
+        __syncthreads();
+    }
+    int s = sequence_of(p.offsets, p.S, begin), have = -1;
+    float slope[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) slope[j] = 0.0f;
+    for (int t = begin + warp; t < end; t += kWarps) {
+        while (s + 1 < p.S && p.offsets[s + 1] <= t) ++s;
+        const bool inside = p.offsets[s] <= t && t < p.offsets[s + 1] && !(p.valid && !p.valid[t]);
+        float d[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) d[j] = 0.0f;
+        if (inside) {
+            const T *row = static_cast<const T *>(p.logits) + (size_t)t * p.ld;
+            float l[PER], v[PER], rest[PER];
+            load_row<T, PER, VEC>(row, p.E, lane, l);
+            if (p.dloss && s != have) {   // G of another sequence
+                have = s;
+                int pairs = 0;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int e = expert_of<VEC>(j, lane), c = e < p.E ? p.counts[(size_t)s * p.E + e] : 0;
+                    pairs += c;
+                    slope[j] = (float)c;
+                }
+                pairs = __reduce_add_sync(0xffffffffu, pairs);
+                const float each = pairs > 0 ? p.dloss[0] * ((float)p.E / (float)pairs) / ((float)max(p.tokens[s], 1) * (float)max(s_used, 1)) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) slope[j] *= each;
+            }
+            scores(l, v, rest);
+            if (p.dloss) {
+                float total = 0.0f, dot = 0.0f;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    total += v[j];
+                    dot = fmaf(v[j], slope[j], dot);
+                }
+                total = warp_sum(total);
+                dot = warp_sum(dot);
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                dot *= inv;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) d[j] = (slope[j] - dot) * v[j] * inv * rest[j];
+            }
+            if (p.dw) {
+                const int kept = min(max(p.keff[t], 0), p.K);
+                const int id = lane < kept ? p.ids[(size_t)t * p.K + lane] : -1;
+                const bool on = id >= 0 && id < p.E;
+                float ln[1] = {on ? to_f32(row[id]) : kNegInf}, g[1], r[1];
+                scores(ln, g, r);
+                const float dw = on ? p.dw[(size_t)t * p.K + lane] : 0.0f;
+                float val;
+                if (p.norm) {
+                    const float total = warp_sum(g[0]);
+                    const float h = total == 0.0f ? 0.0f : g[0] / total;
+                    const float dot = warp_sum(h * dw);
+                    val = p.scale * h * r[0] * (dw - dot);
+                } else {
+                    const float q = __expf(-fabsf(ln[0]));
+                    val = p.scale * (ln[0] > 0.0f ? 1.0f - r[0] : q * r[0]) * r[0] * dw;
+                }
+                const unsigned same = __match_any_sync(0xffffffffu, on ? id : -1 - lane);
+                if (__all_sync(0xffffffffu, same == 1u << lane)) {
+                    if (on) add[id] = val;
+                } else {   // an expert kept twice: in order of its places
+                    for (int i = 0; i < p.K; ++i) {
+                        if (lane == i && on) add[id] += val;
+                        __syncwarp();
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int e = expert_of<VEC>(j, lane);
+                    if (e < p.E) d[j] += add[e];
+                }
+                __syncwarp();
+                if (on) add[id] = 0.0f;
+                __syncwarp();
+            }
+        }
+        G *to = static_cast<G *>(p.dlogits) + (size_t)t * p.E;
+        if constexpr (VEC == 4) {
+#pragma unroll
+            for (int j = 0; j < PER; j += 4) {
+                const int e = expert_of<4>(j, lane);
+                if (e >= p.E) continue;
+                union {
+                    uint4 q;
+                    uint2 h;
+                    G g[4];
+                } u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) from_f32(u.g[i], d[j + i]);
+                if constexpr (sizeof(G) == 4) *reinterpret_cast<uint4 *>(to + e) = u.q;
+                else *reinterpret_cast<uint2 *>(to + e) = u.h;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int e = expert_of<1>(j, lane);
+                if (e < p.E) from_f32(to[e], d[j]);
+            }
+        }
+    }
+}
+
+int chunk_tokens(int T)
+{
+    return std::max(kMinChunk, ((T + kMaxChunks - 1) / kMaxChunks + kWarps - 1) / kWarps * kWarps);
+}
+
+struct BalanceLayout {
+    size_t psum, pcount, pmeta, ploss, total;
+};
+
+BalanceLayout balance_layout(int T, int E, int S)
+{
+    const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const size_t slots = (size_t)std::min(kMaxChunks, (T + kMinChunk - 1) / kMinChunk) + S;   // of T tokens or fewer
+    BalanceLayout L;
+    L.psum = 256;
+    L.pcount = L.psum + up(slots * E * 4);
+    L.pmeta = L.pcount + up(slots * E * 4);
+    L.ploss = L.pmeta + up(slots * 8);
+    L.total = L.ploss + up((size_t)S * ((E + 31) / 32) * 4);
+    return L;
+}
+
+// f(logits that a lane holds, VEC) for rows of E
+template <typename F>
+cudaError_t with_row(int E, bool four, F &&f)
+{
+    using std::integral_constant;
+    const int per = (E + 127) / 128 * 4;
+    const auto by_vec = [&](auto n) {
+        return four ? f(n, integral_constant<int, 4>()) : f(n, integral_constant<int, 1>());
+    };
+    switch (per) {
+    case 4: return by_vec(integral_constant<int, 4>());
+    case 8: return by_vec(integral_constant<int, 8>());
+    case 12: return by_vec(integral_constant<int, 12>());
+    default: return by_vec(integral_constant<int, 16>());
+    }
+}
+
+int elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
+
+// four logits at a time where every row allows it
+bool by_four(const BalanceArgs &a, int dtype) { return a.E % 4 == 0 && a.ld % 4 == 0 && !off(a.logits, 4 * elem_bytes(dtype)); }
+
+cudaError_t launch_forward(const BalanceArgs &a, int dtype, cudaStream_t st)
+{
+    cudaError_t e = cudaSuccess;
+    if (a.T > 0)
+        e = with_dtype(dtype, [&](auto t) {
+            return with_row(a.E, by_four(a, dtype), [&](auto per, auto vec) {
+                return launch_kernel(balance_parts_kernel<decltype(t), decltype(per)::value, decltype(vec)::value>,
+                                     dim3((a.T + a.chunk - 1) / a.chunk), dim3(32 * kWarps), 0, st, 1, a);
+            });
+        });
+    if (e != cudaSuccess) return e;
+    return launch_kernel(balance_loss_kernel, dim3(a.S, (a.E + 31) / 32), dim3(32 * kWarps), 0, st, 1, a);
+}
+
+cudaError_t launch_backward(const BalanceArgs &a, int dtype, int gdtype, cudaStream_t st)
+{
+    const bool four = by_four(a, dtype) && !off(a.dlogits, 4 * elem_bytes(gdtype));
+    return with_dtype(dtype, [&](auto t) {
+        return with_row(a.E, four, [&](auto per, auto vec) {
+            using T = decltype(t);
+            const dim3 grid((a.T + a.chunk - 1) / a.chunk);
+            constexpr int PER = decltype(per)::value, VEC = decltype(vec)::value;
+            return gdtype == dtype ? launch_kernel(balance_backward_kernel<T, T, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, a)
+                                   : launch_kernel(balance_backward_kernel<T, float, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, a);
+        });
+    });
+}
+
+#define BALANCE_PTR(p, a)                                                                               \
+    do {                                                                                                \
+        if (!(p)) return set_error(MOE_ERR_ARG, "%s is NULL", #p);                                      \
+        if (off((p), (a))) return set_error(MOE_ERR_ALIGN, "%s is not %d-byte aligned", #p, (int)(a));  \
+    } while (0)
+
+int check_balance(const moe_config *cfg, const void *logits, int dtype, long long ld, const int32_t *ids, const int32_t *keff, int T,
+                  const int32_t *offsets, int S, const int32_t *counts, const int32_t *tokens)
+{
+    int rc;
+    if ((rc = validate_config(cfg, T))) return rc;
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16)
+        return set_error(MOE_ERR_ARG, "unknown dtype %d", dtype);
+    if (ld < cfg->n_experts) return set_error(MOE_ERR_SHAPE, "ld must be at least n_experts (got %lld)", ld);
+    if (S < 1 || S > kMaxSequences) return set_error(MOE_ERR_SHAPE, "n_seq must be in [1, 2^20] (got %d)", S);
+    BALANCE_PTR(offsets, 4);
+    BALANCE_PTR(counts, 4);
+    BALANCE_PTR(tokens, 4);
+    if (T == 0) return MOE_OK;
+    BALANCE_PTR(logits, elem_bytes(dtype));
+    BALANCE_PTR(ids, 4);
+    BALANCE_PTR(keff, 4);
+    return MOE_OK;
+}
+
+int check_workspace(void *ws, size_t bytes, size_t need)
+{
+    if (!ws) return set_error(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (off(ws, 256)) return set_error(MOE_ERR_ALIGN, "workspace is not 256-byte aligned");
+    if (bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace has %zu bytes; %zu needed", bytes, need);
+    return MOE_OK;
+}
+
+int done(cudaError_t e, const char *what)
+{
+    if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return set_error(MOE_OK, "%s", "");
+}
+
+BalanceArgs arguments(const moe_config *cfg, const void *logits, long long ld, const int32_t *ids, const int32_t *keff, int T,
+                      const int32_t *offsets, int S, const uint8_t *valid, const int32_t *counts, const int32_t *tokens, void *ws)
+{
+    BalanceArgs a = {};
+    a.logits = logits;
+    a.ld = ld;
+    a.ids = ids;
+    a.keff = keff;
+    a.offsets = offsets;
+    a.valid = valid;
+    a.T = T;
+    a.E = cfg->n_experts;
+    a.K = cfg->top_k;
+    a.S = S;
+    a.chunk = chunk_tokens(T);
+    a.counts = const_cast<int32_t *>(counts);
+    a.tokens = const_cast<int32_t *>(tokens);
+    a.scale = cfg->routed_scaling_factor;
+    a.norm = cfg->norm_topk_prob;
+    a.err = static_cast<int32_t *>(ws);
+    a.ticket = a.err + 1;
+    return a;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_balance_workspace_size(const moe_config *cfg, int max_tokens, int max_seq)
+{
+    if (validate_config(cfg, max_tokens) || max_seq < 1 || max_seq > kMaxSequences) return 0;
+    return balance_layout(max_tokens, cfg->n_experts, max_seq).total;
+}
+
+int moe_balance_forward(const moe_config *cfg, const void *logits, int dtype, long long ld, const int32_t *ids, const int32_t *keff,
+                        int T, const int32_t *seq_offsets, int n_seq, const uint8_t *valid, float *loss, int32_t *counts,
+                        int32_t *tokens, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc;
+    if ((rc = check_balance(cfg, logits, dtype, ld, ids, keff, T, seq_offsets, n_seq, counts, tokens))) return rc;
+    BALANCE_PTR(loss, 4);
+    const BalanceLayout L = balance_layout(T, cfg->n_experts, n_seq);
+    if ((rc = check_workspace(workspace, workspace_bytes, L.total)) || (rc = require_device())) return rc;
+    BalanceArgs a = arguments(cfg, logits, ld, ids, keff, T, seq_offsets, n_seq, valid, counts, tokens, workspace);
+    char *ws = static_cast<char *>(workspace);
+    a.psum = reinterpret_cast<float *>(ws + L.psum);
+    a.pcount = reinterpret_cast<int32_t *>(ws + L.pcount);
+    a.pmeta = reinterpret_cast<int32_t *>(ws + L.pmeta);
+    a.ploss = reinterpret_cast<float *>(ws + L.ploss);
+    a.loss = loss;
+    return done(launch_forward(a, dtype, (cudaStream_t)stream), "balance loss launch");
+}
+
+int moe_balance_backward(const moe_config *cfg, const void *logits, int dtype, long long ld, const int32_t *ids, const int32_t *keff,
+                         int T, const int32_t *seq_offsets, int n_seq, const uint8_t *valid, const int32_t *counts,
+                         const int32_t *tokens, const float *dloss, const float *dw, void *dlogits, int grad_dtype, void *stream)
+{
+    int rc;
+    if ((rc = check_balance(cfg, logits, dtype, ld, ids, keff, T, seq_offsets, n_seq, counts, tokens))) return rc;
+    if (grad_dtype != dtype && grad_dtype != MOE_DTYPE_F32)
+        return set_error(MOE_ERR_ARG, "grad_dtype must be dtype or fp32 (got %d)", grad_dtype);
+    if (!dloss && !dw) return set_error(MOE_ERR_ARG, "dloss and dw are both NULL");
+    if (off(dloss, 4) || off(dw, 4)) return set_error(MOE_ERR_ALIGN, "dloss or dw is not 4-byte aligned");
+    if (T == 0) return done(cudaSuccess, "");
+    BALANCE_PTR(dlogits, elem_bytes(grad_dtype));
+    if ((rc = require_device())) return rc;
+    BalanceArgs a = arguments(cfg, logits, ld, ids, keff, T, seq_offsets, n_seq, valid, counts, tokens, nullptr);
+    a.dloss = dloss;
+    a.dw = dw;
+    a.dlogits = dlogits;
+    return done(launch_backward(a, dtype, grad_dtype, (cudaStream_t)stream), "balance gradient launch");
+}
+
+}  // extern "C"

@@ -692,6 +692,7 @@ int moe_check_errors(void *workspace, size_t workspace_bytes, void *stream)
     if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a bounded device-side wait gave up; the kernel stopped early and its outputs are incomplete");
     if (flag & kErrBadOffsets) return fail(MOE_ERR_DEVICE, "a group whose offsets are out of order or past the rows was skipped");
     if (flag & kErrBadToken) return fail(MOE_ERR_DEVICE, "a token index outside [0, T) was skipped");
+    if (flag & kErrBadAdapter) return fail(MOE_ERR_DEVICE, "an adapter index outside [-1, adapters) was skipped");
     if (flag) return fail(MOE_ERR_DEVICE, "device error word 0x%x", flag);
     return ok();
 }

@@ -36,6 +36,7 @@ constexpr int kErrBadKeff = 2;
 constexpr int kErrTimeout = 4;     // a bounded device-side wait gave up
 constexpr int kErrBadOffsets = 8;  // a group's offsets are out of order or past the rows
 constexpr int kErrBadToken = 16;   // a token index outside [0, T)
+constexpr int kErrBadAdapter = 32; // an adapter index outside [-1, adapters)
 
 // ---------------------------------------------------------------------------
 // Work plan of the grouped expert FFN.  A "slot" is one expert applied to its
