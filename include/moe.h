@@ -385,12 +385,12 @@ int moe_balance_forward(const moe_config *cfg, const void *logits, int dtype, lo
  *   The other operands as moe_balance_forward took them, counts and tokens as it wrote them (read with
  *   dloss).  The counts are constants and the choice has no gradient.
  *   dlogits [T][E] (dense) of grad_dtype, dtype or fp32, written in full: zero for tokens that are
- *   not valid or in no sequence. */
+ *   not valid or in no sequence.  workspace: 256 bytes (the error word), zeroed once. */
 int moe_balance_backward(const moe_config *cfg, const void *logits, int dtype, long long ld,
                          const int32_t *ids, const int32_t *keff, int T, const int32_t *seq_offsets,
                          int n_seq, const uint8_t *valid, const int32_t *counts,
                          const int32_t *tokens, const float *dloss, const float *dw, void *dlogits,
-                         int grad_dtype, void *stream);
+                         int grad_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of moe_balance_forward for up to max_tokens tokens in up to max_seq
  * sequences; 0 for an invalid config or count. */

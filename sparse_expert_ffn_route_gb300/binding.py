@@ -155,7 +155,7 @@ def load_library():
     L.moe_block_norm_workspace_size.argtypes = [i32, i32]
     L.moe_block_norm_workspace_size.restype = sz
     L.moe_balance_forward.argtypes = [vp, vp, i32, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp]
-    L.moe_balance_backward.argtypes = [vp, vp, i32, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp]
+    L.moe_balance_backward.argtypes = [vp, vp, i32, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     L.moe_balance_workspace_size.argtypes = [vp, i32, i32]
     L.moe_balance_workspace_size.restype = sz
     L.moe_adapter_matmul.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, i32, vp, sz, vp]
@@ -684,8 +684,8 @@ def moe_balance_forward(cfg, logits, ids, keff, seq_offsets, loss, counts, token
         _check(rc, "moe_balance_forward")
 
 
-def moe_balance_backward(cfg, logits, ids, keff, seq_offsets, counts, tokens, dlogits, dloss=None, dw=None, valid=None,
-                         stream=None):
+def moe_balance_backward(cfg, logits, ids, keff, seq_offsets, counts, tokens, dlogits, workspace, dloss=None, dw=None,
+                         valid=None, stream=None):
     """dlogits [T][E] (float32 or the logits' type) from dloss [1] float32, the balance loss's gradient, and dw [T][K]
     float32, that of the weights moe_route applies (either may be None).  counts and tokens as
     moe_balance_forward wrote them."""
@@ -693,7 +693,8 @@ def moe_balance_backward(cfg, logits, ids, keff, seq_offsets, counts, tokens, dl
     f32 = torch.float32
     rc = load_library().moe_balance_backward(
         *args, *kept, _opt(dloss, "dloss", (1,), f32, dev), _opt(dw, "dw", (T, cfg.top_k), f32, dev),
-        _dense(dlogits, "dlogits", (T, cfg.n_experts), dlogits.dtype, dev), _dtype(dlogits, "dlogits"), _raw_stream(stream, dev))
+        _dense(dlogits, "dlogits", (T, cfg.n_experts), dlogits.dtype, dev), _dtype(dlogits, "dlogits"), _space(workspace, dev),
+        workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_balance_backward")
 

@@ -350,9 +350,11 @@ __global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const Bal
                 for (int j = 0; j < PER; ++j) d[j] = (slope[j] - dot) * v[j] * inv * rest[j];
             }
             if (p.dw) {
-                const int kept = min(max(p.keff[t], 0), p.K);
+                const int keff = p.keff[t], kept = min(keff, p.K);
                 const int id = lane < kept ? p.ids[(size_t)t * p.K + lane] : -1;
                 const bool on = id >= 0 && id < p.E;
+                if (lane < kept && !on) atomicOr(p.err, kErrBadExpertId);
+                if (keff < 0 || keff > p.K) atomicOr(p.err, kErrBadKeff);
                 float ln[1] = {on ? to_f32(row[id]) : kNegInf}, g[1], r[1];
                 scores(ln, g, r);
                 const float dw = on ? p.dw[(size_t)t * p.K + lane] : 0.0f;
@@ -584,7 +586,8 @@ int moe_balance_forward(const moe_config *cfg, const void *logits, int dtype, lo
 
 int moe_balance_backward(const moe_config *cfg, const void *logits, int dtype, long long ld, const int32_t *ids, const int32_t *keff,
                          int T, const int32_t *seq_offsets, int n_seq, const uint8_t *valid, const int32_t *counts,
-                         const int32_t *tokens, const float *dloss, const float *dw, void *dlogits, int grad_dtype, void *stream)
+                         const int32_t *tokens, const float *dloss, const float *dw, void *dlogits, int grad_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream)
 {
     int rc;
     if ((rc = check_balance(cfg, logits, dtype, ld, ids, keff, T, seq_offsets, n_seq, counts, tokens))) return rc;
@@ -594,8 +597,8 @@ int moe_balance_backward(const moe_config *cfg, const void *logits, int dtype, l
     if (off(dloss, 4) || off(dw, 4)) return set_error(MOE_ERR_ALIGN, "dloss or dw is not 4-byte aligned");
     if (T == 0) return done(cudaSuccess, "");
     BALANCE_PTR(dlogits, elem_bytes(grad_dtype));
-    if ((rc = require_device())) return rc;
-    BalanceArgs a = arguments(cfg, logits, ld, ids, keff, T, seq_offsets, n_seq, valid, counts, tokens, nullptr);
+    if ((rc = check_workspace(workspace, workspace_bytes, 256)) || (rc = require_device())) return rc;
+    BalanceArgs a = arguments(cfg, logits, ld, ids, keff, T, seq_offsets, n_seq, valid, counts, tokens, workspace);
     a.dloss = dloss;
     a.dw = dw;
     a.dlogits = dlogits;

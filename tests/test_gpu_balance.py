@@ -41,7 +41,7 @@ def run(o, dloss=None, dw=False, norm=True, scale=2.5, gdtype=None, logits=None)
     d = None
     if dloss is not None or dw:
         d = torch.full(l.shape, 9.0, dtype=gdtype or l.dtype, device="cuda")
-        moe.moe_balance_backward(*args, counts, tokens, d, dloss=None if dloss is None else torch.tensor([dloss], device="cuda"),
+        moe.moe_balance_backward(*args, counts, tokens, d, ws, dloss=None if dloss is None else torch.tensor([dloss], device="cuda"),
                                  dw=o["dw"].cuda() if dw else None, valid=dev(o["valid"]))
     moe.moe_check_errors(ws)
     return loss.cpu(), counts.cpu(), tokens.cpu(), None if d is None else d.cpu()
@@ -192,7 +192,7 @@ def test_the_same_again_and_in_a_graph():
 
     def step():
         moe.moe_balance_forward(*args, loss, counts, tokens, ws)
-        moe.moe_balance_backward(*args, counts, tokens, d, dloss=one, dw=dw)
+        moe.moe_balance_backward(*args, counts, tokens, d, ws, dloss=one, dw=dw)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
