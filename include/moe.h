@@ -351,7 +351,7 @@ size_t moe_block_norm_workspace_size(int T, int H);
  *   A segment whose offsets are out of order or past the rows is skipped, and recorded; one whose id is
  *   no adapter becomes NaN, and is recorded (moe_check_errors).
  *   K, N multiples of 8 in [8, 65536], rank a multiple of 8 in [8, 128] (smaller ones padded with
- *   zeros), adapters in [1, 2^16], segments in [1, 2^20], T in [0, 2^24], rows of x 16-byte aligned.
+ *   zeros), adapters in [1, 2^16], adapters * N below 2^31, segments in [1, 2^20], T in [0, 2^24], rows of x 16-byte aligned.
  *   workspace: 256 bytes (the error word), zeroed once before its first use. */
 int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, const void *down,
                        const void *up, const float *scale, int adapters, int rank, int N,

@@ -1,75 +1,25 @@
 // adapter.cu -- low-rank adapters of many requests beside a projection they share:
 //   y[p] = base[p] + scale[a] (x[p] down[a]^T) up[a]^T,  a = ids[s], for the rows p of segment s.
 //
+// Many rows a segment: tiles of 128 rows on the tensor cores (adapter_tiles.cuh).
+//
 // Few rows a segment (a decode batch).  A cluster of 8 CTAs takes up to 8 rows of one segment: each CTA
 // forms the rows' R numbers over its eighth of the inputs, the eighths are added in rank order through
 // distributed shared memory, and each CTA writes its eighth of the outputs.  One launch, nothing goes
 // through global memory in between.
 #include <algorithm>
 
-#include "cluster_wait.cuh"
-#include "launch.cuh"
-#include "moe_internal.cuh"
-#include "vec8.cuh"
+#include "adapter_tiles.cuh"
 
 namespace moe {
 
+using namespace adapter;
+
 namespace {
 
-constexpr int kMaxRank = 128, kMaxAdapterDim = 65536, kMaxAdapters = 1 << 16, kMaxSegments = 1 << 20;
 constexpr int kFewRows = 8;       // rows of a tile
 constexpr int kFewCluster = 8;
 constexpr int kFewThreads = 256;
-
-struct AdapterArgs {
-    const void *x;
-    long long ldx;
-    const void *down, *up;
-    const float *scale;
-    const int32_t *offsets, *ids;
-    const void *base;
-    void *y;
-    int T, S, K, N, R, A;
-    int32_t *err;
-};
-
-// Tiles of `rows` rows on a fixed grid over the batch, cut by the segments: the part of grid cell c that is
-// segment s's is tile c + s.  (A later part has a later cell or a later segment, so no two share a number.)
-struct Tile {
-    int lo, hi;      // rows; empty where the number is not used
-    int adapter;     // -1: none
-    bool bad;        // not an adapter: the rows become NaN
-};
-
-// by one warp
-__device__ __forceinline__ Tile find_tile(const AdapterArgs &p, int tile, int rows, int lane)
-{
-    Tile t = {0, 0, -1, false};
-    int s = 0, n = p.S;      // the last segment whose first tile is `tile` or before it lies in [s, s + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32, at = lane * step;
-        const bool before = at < n && p.offsets[s + at] / rows + s + at <= tile;
-        const int got = __popc(__ballot_sync(0xffffffffu, before));
-        if (got == 0) return t;
-        n = min(step, n - (got - 1) * step);
-        s += (got - 1) * step;
-    }
-    const int cell = tile - s, from = p.offsets[s], to = p.offsets[s + 1];
-    if (cell < 0 || from < 0 || from > to || to > p.T) return t;
-    t.lo = max(from, cell * rows);
-    t.hi = (int)min((long long)to, ((long long)cell + 1) * rows);
-    t.adapter = p.ids[s];
-    t.bad = t.adapter < -1 || t.adapter >= p.A;
-    return t;
-}
-
-// what is wrong with segment s, recorded
-__device__ __forceinline__ void check_segment(const AdapterArgs &p, int s)
-{
-    const int from = p.offsets[s], to = p.offsets[s + 1], id = p.ids[s];
-    if (from < 0 || from > to || to > p.T) atomicOr(p.err, kErrBadOffsets);
-    if (id < -1 || id >= p.A) atomicOr(p.err, kErrBadAdapter);
-}
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 {
@@ -218,7 +168,7 @@ auto with_half(int dtype, F &&f)
     return dtype == MOE_DTYPE_BF16 ? f(__nv_bfloat16()) : f(__half());
 }
 
-cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_t st)
+cudaError_t launch_few(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_t st)
 {
     const long long tiles = (p.T + kFewRows - 1) / kFewRows + p.S;
     const size_t smem = (size_t)kFewRows * ((p.K / 8 + kFewCluster - 1) / kFewCluster * 8) * 2;
@@ -227,6 +177,14 @@ cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, cudaStr
             return launch_kernel(adapter_few_kernel<decltype(t), decltype(y)>, dim3((unsigned)(tiles * kFewCluster)), dim3(kFewThreads),
                                  smem, st, kFewCluster, p);
         });
+    });
+}
+
+cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_t st)
+{
+    if (p.T < 16ll * p.S) return launch_few(p, dtype, y_dtype, st);
+    return with_half(dtype, [&](auto t) {
+        return with_dtype(y_dtype, [&](auto y) { return adapter::launch_tiles<decltype(t), decltype(y)>(p, dtype, st); });
     });
 }
 
@@ -268,6 +226,7 @@ int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, co
     if (rank < 8 || rank > kMaxRank || rank % 8)
         return set_error(MOE_ERR_SHAPE, "rank must be a multiple of 8 in [8, %d] (got %d)", kMaxRank, rank);
     if (adapters < 1 || adapters > kMaxAdapters) return set_error(MOE_ERR_SHAPE, "adapters must be in [1, 2^16] (got %d)", adapters);
+    if ((long long)adapters * N > INT32_MAX) return set_error(MOE_ERR_SHAPE, "adapters * N must be below 2^31");
     if (segments < 1 || segments > kMaxSegments) return set_error(MOE_ERR_SHAPE, "segments must be in [1, 2^20] (got %d)", segments);
     if (ldx < K) return set_error(MOE_ERR_SHAPE, "ldx must be at least K (got %lld)", ldx);
     if (ldx % 8) return set_error(MOE_ERR_ALIGN, "rows of x are not 16-byte aligned (ldx %lld)", ldx);

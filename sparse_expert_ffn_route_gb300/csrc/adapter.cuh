@@ -1,0 +1,65 @@
+// adapter.cuh -- what the two kernels of the adapters (adapter.cu, adapter_tiles.cuh) share: arguments, and
+// the tiles of a batch cut into segments.
+#pragma once
+
+#include "cluster_wait.cuh"
+#include "launch.cuh"
+#include "moe_internal.cuh"
+#include "vec8.cuh"
+
+namespace moe {
+namespace adapter {
+
+constexpr int kMaxRank = 128, kMaxAdapterDim = 65536, kMaxAdapters = 1 << 16, kMaxSegments = 1 << 20;
+struct AdapterArgs {
+    const void *x;
+    long long ldx;
+    const void *down, *up;
+    const float *scale;
+    const int32_t *offsets, *ids;
+    const void *base;
+    void *y;
+    int T, S, K, N, R, A;
+    int32_t *err;
+};
+
+// Tiles of `rows` rows on a fixed grid over the batch, cut by the segments: the part of grid cell c that is
+// segment s's is tile c + s.  (A later part has a later cell or a later segment, so no two share a number.)
+struct Tile {
+    int lo, hi;      // rows; empty where the number is not used
+    int adapter;     // -1: none
+    bool bad;        // not an adapter: the rows become NaN
+};
+
+// by one warp
+__device__ __forceinline__ Tile find_tile(const AdapterArgs &p, int tile, int rows, int lane)
+{
+    Tile t = {0, 0, -1, false};
+    int s = 0, n = p.S;      // the last segment whose first tile is `tile` or before it lies in [s, s + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const bool before = at < n && p.offsets[s + at] / rows + s + at <= tile;
+        const int got = __popc(__ballot_sync(0xffffffffu, before));
+        if (got == 0) return t;
+        n = min(step, n - (got - 1) * step);
+        s += (got - 1) * step;
+    }
+    const int cell = tile - s, from = p.offsets[s], to = p.offsets[s + 1];
+    if (cell < 0 || from < 0 || from > to || to > p.T) return t;
+    t.lo = max(from, cell * rows);
+    t.hi = (int)min((long long)to, ((long long)cell + 1) * rows);
+    t.adapter = p.ids[s];
+    t.bad = t.adapter < -1 || t.adapter >= p.A;
+    return t;
+}
+
+// what is wrong with segment s, recorded
+__device__ __forceinline__ void check_segment(const AdapterArgs &p, int s)
+{
+    const int from = p.offsets[s], to = p.offsets[s + 1], id = p.ids[s];
+    if (from < 0 || from > to || to > p.T) atomicOr(p.err, kErrBadOffsets);
+    if (id < -1 || id >= p.A) atomicOr(p.err, kErrBadAdapter);
+}
+
+}  // namespace adapter
+}  // namespace moe
