@@ -352,11 +352,16 @@ size_t moe_block_norm_workspace_size(int T, int H);
  *   no adapter becomes NaN, and is recorded (moe_check_errors).
  *   K, N multiples of 8 in [8, 65536], rank a multiple of 8 in [8, 128] (smaller ones padded with
  *   zeros), adapters in [1, 2^16], adapters * N below 2^31, segments in [1, 2^20], T in [0, 2^24], rows of x 16-byte aligned.
- *   workspace: 256 bytes (the error word), zeroed once before its first use. */
+ *   workspace: moe_adapter_workspace_size(T, rank) bytes, first 256 zeroed once.  With less, the
+ *   rows are taken in as many passes as it needs; moe_adapter_workspace_size(min(T, 128), rank) is the
+ *   least.  For one call at a time. */
 int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, const void *down,
                        const void *up, const float *scale, int adapters, int rank, int N,
                        const int32_t *offsets, const int32_t *ids, int segments, const void *base,
                        void *y, int y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of moe_adapter_matmul for T rows in one pass; 0 for sizes outside the limits. */
+size_t moe_adapter_workspace_size(int T, int rank);
 
 /* How evenly a batch's routing loads the experts.  For each of n_seq sequences s (tokens
  * seq_offsets[s] <= t < seq_offsets[s+1]) with sig = sigmoid(logits):

@@ -20,6 +20,7 @@ from .binding import (EXPORTS, LIBRARY_PATH, MOE_ERR_ALIGN, MOE_ERR_ARG, MOE_ERR
                       moe_gated_workspace_size, moe_mxfp4_expert_ffn, moe_mxfp4_matmul,
                       moe_mxfp4_workspace_size, moe_quantize_mxfp4, MOE_GATE_CHANNEL, MOE_GATE_FULL,
                       MOE_GATE_NONE, MOE_GATE_TOKEN, alloc_adapter_workspace, alloc_balance_workspace,
-                      alloc_block_norm_workspace, moe_adapter_matmul, moe_balance_backward,
+                      alloc_block_norm_workspace, moe_adapter_matmul,
+                      moe_adapter_workspace_size, moe_balance_backward,
                       moe_balance_forward, moe_balance_workspace_size, moe_block_norm_backward,
                       moe_block_norm_forward, moe_block_norm_workspace_size)

@@ -52,7 +52,7 @@ EXPORTS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_expert_ffn", "
            "moe_mxfp4_workspace_size", "moe_gated_forward", "moe_gated_backward",
            "moe_gated_workspace_size", "moe_block_norm_forward", "moe_block_norm_backward",
            "moe_block_norm_workspace_size", "moe_balance_forward", "moe_balance_backward",
-           "moe_balance_workspace_size", "moe_adapter_matmul")
+           "moe_balance_workspace_size", "moe_adapter_matmul", "moe_adapter_workspace_size")
 
 
 class MoeError(RuntimeError):
@@ -159,6 +159,8 @@ def load_library():
     L.moe_balance_workspace_size.argtypes = [vp, i32, i32]
     L.moe_balance_workspace_size.restype = sz
     L.moe_adapter_matmul.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, i32, vp, sz, vp]
+    L.moe_adapter_workspace_size.argtypes = [i32, i32]
+    L.moe_adapter_workspace_size.restype = sz
     L.moe_last_error_string.argtypes = []
     L.moe_last_error_string.restype = ctypes.c_char_p
     _lib = L
@@ -699,9 +701,19 @@ def moe_balance_backward(cfg, logits, ids, keff, seq_offsets, counts, tokens, dl
         _check(rc, "moe_balance_backward")
 
 
-def alloc_adapter_workspace(device="cuda") -> torch.Tensor:
-    """Zeroed workspace of moe_adapter_matmul (the error word)."""
-    return torch.zeros(256, dtype=torch.uint8, device=device)
+def moe_adapter_workspace_size(T: int, rank: int) -> int:
+    return int(load_library().moe_adapter_workspace_size(T, rank))
+
+
+def alloc_adapter_workspace(T: int = 32768, rank: int = 64, device="cuda") -> torch.Tensor:
+    """Workspace of moe_adapter_matmul, its head zeroed.  It serves any T and rank: more rows or a higher rank
+    than it is made for take more passes."""
+    n = moe_adapter_workspace_size(T, rank)
+    if n == 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_adapter_workspace_size", "sizes outside the limits")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def moe_adapter_matmul(x, down, up, scale, offsets, ids, y, workspace, base=None, stream=None):

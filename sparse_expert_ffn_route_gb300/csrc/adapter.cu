@@ -180,11 +180,11 @@ cudaError_t launch_few(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_
     });
 }
 
-cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_t st)
+cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, void *workspace, size_t bytes, cudaStream_t st)
 {
     if (p.T < 16ll * p.S) return launch_few(p, dtype, y_dtype, st);
     return with_half(dtype, [&](auto t) {
-        return with_dtype(y_dtype, [&](auto y) { return adapter::launch_tiles<decltype(t), decltype(y)>(p, dtype, st); });
+        return with_dtype(y_dtype, [&](auto y) { return adapter::launch_tiles<decltype(t), decltype(y)>(p, dtype, workspace, bytes, st); });
     });
 }
 
@@ -209,6 +209,12 @@ using namespace moe;
     } while (0)
 
 extern "C" {
+
+size_t moe_adapter_workspace_size(int T, int rank)
+{
+    if (T < 0 || T > 1 << 24 || rank < 8 || rank > kMaxRank || rank % 8) return 0;
+    return 256 + (size_t)(T + adapter::kTileRows - 1) / adapter::kTileRows * adapter::kTileRows * adapter::row_bytes(rank);
+}
 
 int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, const void *down, const void *up, const float *scale,
                        int adapters, int rank, int N, const int32_t *offsets, const int32_t *ids, int segments, const void *base,
@@ -241,7 +247,8 @@ int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, co
     if (off(scale, 4)) return set_error(MOE_ERR_ALIGN, "scale is not 4-byte aligned");
     if (!workspace) return set_error(MOE_ERR_WORKSPACE, "workspace is NULL");
     if (off(workspace, 256)) return set_error(MOE_ERR_ALIGN, "workspace is not 256-byte aligned");
-    if (workspace_bytes < 256) return set_error(MOE_ERR_WORKSPACE, "workspace has %zu bytes; 256 needed", workspace_bytes);
+    const size_t need = moe_adapter_workspace_size(std::min(T, adapter::kTileRows), rank);
+    if (workspace_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace has %zu bytes; %zu needed", workspace_bytes, need);
     if ((rc = require_device())) return rc;
     AdapterArgs p = {};
     p.x = x;
@@ -260,7 +267,7 @@ int moe_adapter_matmul(const void *x, long long ldx, int dtype, int T, int K, co
     p.R = rank;
     p.A = adapters;
     p.err = static_cast<int32_t *>(workspace);
-    return done(launch_adapter(p, dtype, y_dtype, (cudaStream_t)stream), "adapter launch");
+    return done(launch_adapter(p, dtype, y_dtype, workspace, workspace_bytes, (cudaStream_t)stream), "adapter launch");
 }
 
 }  // extern "C"

@@ -169,6 +169,22 @@ def test_bad_lists_are_recorded(n):
     call([0, 2 * n, n, T], [0, 1, 0])
 
 
+def test_a_small_workspace_takes_several_passes():
+    o = make([100, 400, 3, 260], [1, 0, -1, 1], 264, 136, 24, 2, before=7, after=4)
+    want = run(o)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for rows in (128, 300):
+        for in_place in (False, True):
+            ws = moe.alloc_adapter_workspace(rows, 24)
+            y = o["base"].clone() if in_place else torch.full_like(o["base"], 7.0)
+            moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y, ws,
+                                   base=y if in_place else o["base"])
+            moe.moe_check_errors(ws)
+            assert torch.equal(y[7:-4], want[7:-4])
+    with pytest.raises(moe.MoeError):
+        moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y, ws[:256])
+
+
 def test_in_a_graph():
     o = make([1, 1, 70, 1], [0, 1, 2, 0], 512, 512, 16, 3, out=BF16)
     want = run(o)
