@@ -38,17 +38,20 @@ __device__ __forceinline__ void few_down(const T *xs, int width, const T *down, 
 #pragma unroll
         for (int i = 0; i < U * M; ++i) acc[i] = 0.0f;
         for (int k = lane * 8; k < width; k += 256) {
-            Vec8<T> d[U];
+            float d[U][8], x[8];
+            Vec8<T> v[U], w;
 #pragma unroll
-            for (int u = 0; u < U; ++u) d[u].load(down + (r0 + u) * ldd + k);
+            for (int u = 0; u < U; ++u) v[u].load(down + (r0 + u) * ldd + k);
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u].get(d[u]);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                Vec8<T> x;
-                x.load(xs + (size_t)m * width + k);
+                w.load(xs + (size_t)m * width + k);
+                w.get(x);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[u * M + m] = fmaf(x.get(i), d[u].get(i), acc[u * M + m]);
+                    for (int i = 0; i < 8; ++i) acc[u * M + m] = fmaf(x[i], d[u][i], acc[u * M + m]);
             }
         }
         constexpr int V = U * M;   // a power of two, at most 32
@@ -70,13 +73,16 @@ __device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, cons
         const T *b = up + (size_t)n * p.R;
         for (int r = 0; r < p.R; r += 8) {
             Vec8<T> v;
+            float f[8], g[8];
             v.load(b + r);
+            v.get(f);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 Vec8<float> w;
                 w.load(u + m * kMaxRank + r);
+                w.get(g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[m] = fmaf(w.get(i), v.get(i), acc[m]);
+                for (int i = 0; i < 8; ++i) acc[m] = fmaf(g[i], f[i], acc[m]);
             }
         }
 #pragma unroll
