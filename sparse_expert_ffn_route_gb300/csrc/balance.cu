@@ -24,9 +24,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kLossWarps = 16;
 constexpr int kMaxChunks = 608;      // four CTAs an SM
-constexpr int kMinChunk = kWarps;    // tokens: one a warp
+constexpr int kMinChunk = 2 * kWarps;   // tokens
+constexpr int grad_ctas(int per) { return per >= 12 ? 3 : 4; }   // CTAs an SM of the gradient's kernel, by its registers
 constexpr int kMaxSequences = 1 << 20;
 
 struct BalanceArgs {
@@ -60,32 +61,31 @@ __device__ __forceinline__ int expert_of(int j, int lane)
     return VEC == 4 ? ((j >> 2) * 32 + lane) * 4 + (j & 3) : j * 32 + lane;
 }
 
+// a row as it lies in memory, so that the next token's is on its way while one is worked on
 template <typename T, int PER, int VEC>
-__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&l)[PER])
-{
-    if constexpr (VEC == 4) {
+struct RawRow {
+    union __align__(16) {
+        uint2 w[PER * sizeof(T) / 8];
+        T t[PER];
+    };
+    __device__ RawRow() {}
+    __device__ __forceinline__ void load(const T *row, int E, int lane)
+    {
 #pragma unroll
-        for (int j = 0; j < PER; j += 4) {
-            const int e = expert_of<4>(j, lane);
-            union {
-                uint2 w[sizeof(T) / 2];
-                T t[4];
-            } u;
-            if (e < E) {
-                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(&u) = *reinterpret_cast<const uint4 *>(row + e);
-                else u.w[0] = *reinterpret_cast<const uint2 *>(row + e);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) l[j + i] = e < E ? to_f32(u.t[i]) : kNegInf;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = expert_of<1>(j, lane);
-            l[j] = e < E ? to_f32(row[e]) : kNegInf;
+        for (int j = 0; j < PER; j += VEC) {
+            const int e = expert_of<VEC>(j, lane);
+            if (e >= E) continue;
+            if constexpr (VEC == 1) t[j] = row[e];
+            else if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t + j) = *reinterpret_cast<const uint4 *>(row + e);
+            else *reinterpret_cast<uint2 *>(t + j) = *reinterpret_cast<const uint2 *>(row + e);
         }
     }
-}
+    __device__ __forceinline__ void get(int E, int lane, float (&l)[PER]) const
+    {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) l[j] = expert_of<VEC>(j, lane) < E ? to_f32(t[j]) : kNegInf;
+    }
+};
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -103,25 +103,28 @@ __device__ __forceinline__ float warp_max(float v)
 
 constexpr float kLow = -60.0f;   // sums of scores above exp(-60) are far from fp32's smallest numbers
 
-// t: scores of this lane's N logits up to a common factor; rest: 1 - sig.  A row of nothing but -inf has t = 0.
-template <int N>
-__device__ __forceinline__ void scores(const float (&l)[N], float (&t)[N], float (&rest)[N])
+// f(j, score, 1 - sig) for this lane's N logits, the scores up to a common factor; a row of nothing but -inf
+// scores 0.
+template <int N, typename F>
+__device__ __forceinline__ void scores(const float (&l)[N], F &&f)
 {
     bool high = false;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const float q = __expf(-fabsf(l[j])), r = __fdividef(1.0f, 1.0f + q);
-        t[j] = l[j] > 0.0f ? r : q * r;
-        rest[j] = l[j] > 0.0f ? q * r : r;
-        high |= l[j] > kLow;
+    for (int j = 0; j < N; ++j) high |= l[j] > kLow;
+    if (__any_sync(0xffffffffu, high)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float q = __expf(-fabsf(l[j])), r = __fdividef(1.0f, 1.0f + q), qr = q * r;
+            f(j, l[j] > 0.0f ? r : qr, l[j] > 0.0f ? qr : r);
+        }
+        return;
     }
-    if (__any_sync(0xffffffffu, high)) return;
     float m = kNegInf;
 #pragma unroll
     for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
     m = warp_max(m);
 #pragma unroll
-    for (int j = 0; j < N; ++j) t[j] = l[j] == kNegInf ? 0.0f : expf(l[j] - m);   // (1 + exp(l) is 1; NaN stays)
+    for (int j = 0; j < N; ++j) f(j, l[j] == kNegInf ? 0.0f : expf(l[j] - m), 1.0f);   // (1 + exp(l) is 1; NaN stays)
 }
 
 // the last sequence that begins at or before token t
@@ -137,7 +140,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *offsets, int S, int t)
 }
 
 template <typename T, int PER, int VEC>
-__global__ void __launch_bounds__(32 * kWarps) balance_parts_kernel(const BalanceArgs p)
+__global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const BalanceArgs p)
 {
     pdl_wait();
     pdl_launch_dependents();
@@ -157,19 +160,24 @@ __global__ void __launch_bounds__(32 * kWarps) balance_parts_kernel(const Balanc
 #pragma unroll
         for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
         int counted = 0;
+        RawRow<T, PER, VEC> raw;
+        const T *logits = static_cast<const T *>(p.logits);
+        if (lo + warp < hi) raw.load(logits + (size_t)(lo + warp) * p.ld, p.E, lane);
         for (int t = lo + warp; t < hi; t += kWarps) {
+            float l[PER];
+            raw.get(p.E, lane, l);
+            if (t + kWarps < hi) raw.load(logits + (size_t)(t + kWarps) * p.ld, p.E, lane);
             if (p.valid && !p.valid[t]) continue;
             ++counted;
-            float l[PER], v[PER], rest[PER];
-            load_row<T, PER, VEC>(static_cast<const T *>(p.logits) + (size_t)t * p.ld, p.E, lane, l);
-            scores(l, v, rest);
             float total = 0.0f;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) total += v[j];
+            scores(l, [&](int j, float v, float) {
+                l[j] = v;
+                total += v;
+            });
             total = warp_sum(total);
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            const float inv = total == 0.0f ? 0.0f : __fdividef(1.0f, total);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+            for (int j = 0; j < PER; ++j) sum[j] = fmaf(l[j], inv, sum[j]);
         }
         int pairs = 0;
         for (int i = tid; i < (hi - lo) * p.K; i += 32 * kWarps) {
@@ -212,12 +220,12 @@ __global__ void __launch_bounds__(32 * kWarps) balance_parts_kernel(const Balanc
 }
 
 // A sequence's sums for 32 experts a CTA; the last CTA adds up the loss.
-__global__ void __launch_bounds__(32 * kWarps) balance_loss_kernel(const BalanceArgs p)
+__global__ void __launch_bounds__(32 * kLossWarps) balance_loss_kernel(const BalanceArgs p)
 {
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ float s_sum[kWarps][32];
-    __shared__ int s_count[kWarps][32], s_meta[2], s_last, s_used, s_bad;
+    __shared__ float s_sum[kLossWarps][32];
+    __shared__ int s_count[kLossWarps][32], s_meta[2], s_last, s_used, s_bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x, e = blockIdx.y * 32 + lane;
     if (tid < 2) s_meta[tid] = 0;
@@ -232,11 +240,12 @@ __global__ void __launch_bounds__(32 * kWarps) balance_loss_kernel(const Balance
     float sum = 0.0f;
     int count = 0, meta[2] = {0, 0};
     if (e < p.E)
-        for (int i = first + warp; i <= last; i += kWarps) {
+#pragma unroll 4
+        for (int i = first + warp; i <= last; i += kLossWarps) {
             sum += p.psum[(size_t)i * p.E + e];
             count += p.pcount[(size_t)i * p.E + e];
         }
-    for (int i = first + tid; i <= last; i += 32 * kWarps) {
+    for (int i = first + tid; i <= last; i += 32 * kLossWarps) {
         meta[0] += p.pmeta[2 * i];
         meta[1] += p.pmeta[2 * i + 1];
     }
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(32 * kWarps) balance_loss_kernel(const Balance
     if (meta[1]) atomicAdd(&s_meta[1], meta[1]);
     __syncthreads();
     if (warp == 0) {
-        for (int w = 1; w < kWarps; ++w) {
+        for (int w = 1; w < kLossWarps; ++w) {
             sum += s_sum[w][lane];
             count += s_count[w][lane];
         }
@@ -266,19 +275,19 @@ __global__ void __launch_bounds__(32 * kWarps) balance_loss_kernel(const Balance
     if (!s_last) return;
     __threadfence();
     int used = 0, wrong = 0;
-    for (int i = tid; i < p.S; i += 32 * kWarps) {
+    for (int i = tid; i < p.S; i += 32 * kLossWarps) {
         used += __ldcg(p.tokens + i) > 0;
         wrong |= p.offsets[i] < 0 || p.offsets[i] > p.offsets[i + 1] || p.offsets[i + 1] > p.T;
     }
     float total = 0.0f;
-    for (long long i = tid; i < (long long)p.S * gridDim.y; i += 32 * kWarps) total += __ldcg(p.ploss + i);
+    for (long long i = tid; i < (long long)p.S * gridDim.y; i += 32 * kLossWarps) total += __ldcg(p.ploss + i);
     total = warp_sum(total);
     if (lane == 0) s_sum[0][warp] = total;
     if (used) atomicAdd(&s_used, used);
     if (wrong) atomicOr(&s_bad, 1);
     __syncthreads();
     if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) total += s_sum[0][w];
+        for (int w = 1; w < kLossWarps; ++w) total += s_sum[0][w];
         if (s_bad) atomicOr(p.err, kErrBadOffsets);
         p.loss[0] = s_bad ? __int_as_float(0x7fc00000) : s_used ? total / (float)s_used : 0.0f;
         *p.ticket = 0;
@@ -286,18 +295,18 @@ __global__ void __launch_bounds__(32 * kWarps) balance_loss_kernel(const Balance
 }
 
 template <typename T, typename G, int PER, int VEC>
-__global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const BalanceArgs p)
+__global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_kernel(const BalanceArgs p)
 {
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ float s_add[kWarps][kMaxExperts];
+    __shared__ __align__(16) float s_add[kWarps][kMaxExperts];
     __shared__ int s_used;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float *add = s_add[warp];
     const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
     if (tid == 0) s_used = 0;
     if (p.dw)
-        for (int e = lane; e < p.E; e += 32) add[e] = 0.0f;
+        for (int e = lane; e < kMaxExperts; e += 32) add[e] = 0.0f;
     __syncthreads();
     if (p.dloss) {
         int used = 0;
@@ -306,20 +315,43 @@ __global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const Bal
         if (lane == 0 && used) atomicAdd(&s_used, used);
         __syncthreads();
     }
+    const T *logits = static_cast<const T *>(p.logits);
+    // of the next token: its row, and on the lanes below K its places
+    RawRow<T, PER, VEC> raw;
+    int next_id = -1, next_keff = 0;
+    float next_dw = 0.0f;
+    const auto fetch = [&](int t) {
+        if (t >= end) return;
+        raw.load(logits + (size_t)t * p.ld, p.E, lane);
+        if (p.dw) {
+            next_keff = p.keff[t];
+            if (lane < p.K) {
+                next_id = p.ids[(size_t)t * p.K + lane];
+                next_dw = p.dw[(size_t)t * p.K + lane];
+            }
+        }
+    };
+    fetch(begin + warp);
     int s = sequence_of(p.offsets, p.S, begin), have = -1;
+    int from = p.offsets[s], to = p.offsets[s + 1];
     float slope[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) slope[j] = 0.0f;
     for (int t = begin + warp; t < end; t += kWarps) {
-        while (s + 1 < p.S && p.offsets[s + 1] <= t) ++s;
-        const bool inside = p.offsets[s] <= t && t < p.offsets[s + 1] && !(p.valid && !p.valid[t]);
+        while (to <= t && s + 1 < p.S) {
+            ++s;
+            from = p.offsets[s];
+            to = p.offsets[s + 1];
+        }
+        const bool inside = from <= t && t < to && !(p.valid && !p.valid[t]);
         float d[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) d[j] = 0.0f;
+        raw.get(p.E, lane, d);
+        const int keff = next_keff, id = lane < min(keff, p.K) ? next_id : -1;
+        const float my_dw = next_dw;
+        fetch(t + kWarps);
+        const bool on = inside && p.dw && id >= 0 && id < p.E;
+        const float mine = on ? to_f32(logits[(size_t)t * p.ld + id]) : kNegInf;   // (in L1)
         if (inside) {
-            const T *row = static_cast<const T *>(p.logits) + (size_t)t * p.ld;
-            float l[PER], v[PER], rest[PER];
-            load_row<T, PER, VEC>(row, p.E, lane, l);
             if (p.dloss && s != have) {   // G of another sequence
                 have = s;
                 int pairs = 0;
@@ -334,39 +366,40 @@ __global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const Bal
 #pragma unroll
                 for (int j = 0; j < PER; ++j) slope[j] *= each;
             }
-            scores(l, v, rest);
+            float total = 0.0f, dot = 0.0f;
             if (p.dloss) {
-                float total = 0.0f, dot = 0.0f;
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    total += v[j];
-                    dot = fmaf(v[j], slope[j], dot);
-                }
+                scores(d, [&](int j, float v, float rest) {
+                    total += v;
+                    dot = fmaf(v, slope[j], dot);
+                    d[j] = v * rest;
+                });
                 total = warp_sum(total);
                 dot = warp_sum(dot);
-                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                const float inv = total == 0.0f ? 0.0f : __fdividef(1.0f, total);
                 dot *= inv;
 #pragma unroll
-                for (int j = 0; j < PER; ++j) d[j] = (slope[j] - dot) * v[j] * inv * rest[j];
+                for (int j = 0; j < PER; ++j) d[j] *= (slope[j] - dot) * inv;
+            } else {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) d[j] = 0.0f;
             }
             if (p.dw) {
-                const int keff = p.keff[t], kept = min(keff, p.K);
-                const int id = lane < kept ? p.ids[(size_t)t * p.K + lane] : -1;
-                const bool on = id >= 0 && id < p.E;
-                if (lane < kept && !on) atomicOr(p.err, kErrBadExpertId);
+                if (lane < min(keff, p.K) && !on) atomicOr(p.err, kErrBadExpertId);
                 if (keff < 0 || keff > p.K) atomicOr(p.err, kErrBadKeff);
-                float ln[1] = {on ? to_f32(row[id]) : kNegInf}, g[1], r[1];
-                scores(ln, g, r);
-                const float dw = on ? p.dw[(size_t)t * p.K + lane] : 0.0f;
-                float val;
+                const float l1[1] = {mine};
+                const float dw = on ? my_dw : 0.0f;
+                float val, g = 0.0f, r = 1.0f;
+                scores(l1, [&](int, float v, float rest) {
+                    g = v;
+                    r = rest;
+                });
                 if (p.norm) {
-                    const float total = warp_sum(g[0]);
-                    const float h = total == 0.0f ? 0.0f : g[0] / total;
-                    const float dot = warp_sum(h * dw);
-                    val = p.scale * h * r[0] * (dw - dot);
+                    const float sum = warp_sum(g);
+                    const float h = sum == 0.0f ? 0.0f : g / sum;
+                    val = p.scale * h * r * (dw - warp_sum(h * dw));
                 } else {
-                    const float q = __expf(-fabsf(ln[0]));
-                    val = p.scale * (ln[0] > 0.0f ? 1.0f - r[0] : q * r[0]) * r[0] * dw;
+                    const float q = __expf(-fabsf(mine));
+                    val = p.scale * (mine > 0.0f ? 1.0f - r : q * r) * r * dw;
                 }
                 const unsigned same = __match_any_sync(0xffffffffu, on ? id : -1 - lane);
                 if (__all_sync(0xffffffffu, same == 1u << lane)) {
@@ -379,16 +412,27 @@ __global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const Bal
                 }
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const int e = expert_of<VEC>(j, lane);
-                    if (e < p.E) d[j] += add[e];
+                for (int j = 0; j < PER; j += VEC) {
+                    const int e = expert_of<VEC>(j, lane);   // (past E within the buffer, and zero)
+                    if constexpr (VEC == 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(add + e);
+                        d[j] += v.x;
+                        d[j + 1] += v.y;
+                        d[j + 2] += v.z;
+                        d[j + 3] += v.w;
+                    } else {
+                        d[j] += add[e];
+                    }
                 }
                 __syncwarp();
                 if (on) add[id] = 0.0f;
                 __syncwarp();
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) d[j] = 0.0f;
         }
-        G *to = static_cast<G *>(p.dlogits) + (size_t)t * p.E;
+        G *row = static_cast<G *>(p.dlogits) + (size_t)t * p.E;
         if constexpr (VEC == 4) {
 #pragma unroll
             for (int j = 0; j < PER; j += 4) {
@@ -399,24 +443,25 @@ __global__ void __launch_bounds__(32 * kWarps) balance_backward_kernel(const Bal
                     uint2 h;
                     G g[4];
                 } u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) from_f32(u.g[i], d[j + i]);
-                if constexpr (sizeof(G) == 4) *reinterpret_cast<uint4 *>(to + e) = u.q;
-                else *reinterpret_cast<uint2 *>(to + e) = u.h;
+                pair_from_f32(u.g, d[j], d[j + 1]);
+                pair_from_f32(u.g + 2, d[j + 2], d[j + 3]);
+                if constexpr (sizeof(G) == 4) *reinterpret_cast<uint4 *>(row + e) = u.q;
+                else *reinterpret_cast<uint2 *>(row + e) = u.h;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int e = expert_of<1>(j, lane);
-                if (e < p.E) from_f32(to[e], d[j]);
+                if (e < p.E) from_f32(row[e], d[j]);
             }
         }
     }
 }
 
-int chunk_tokens(int T)
+// tokens of a CTA where `ctas` of them are wanted
+int chunk_tokens(int T, int ctas = kMaxChunks)
 {
-    return std::max(kMinChunk, ((T + kMaxChunks - 1) / kMaxChunks + kWarps - 1) / kWarps * kWarps);
+    return std::max(kMinChunk, ((T + ctas - 1) / ctas + kWarps - 1) / kWarps * kWarps);
 }
 
 struct BalanceLayout {
@@ -471,7 +516,7 @@ cudaError_t launch_forward(const BalanceArgs &a, int dtype, cudaStream_t st)
             });
         });
     if (e != cudaSuccess) return e;
-    return launch_kernel(balance_loss_kernel, dim3(a.S, (a.E + 31) / 32), dim3(32 * kWarps), 0, st, 1, a);
+    return launch_kernel(balance_loss_kernel, dim3(a.S, (a.E + 31) / 32), dim3(32 * kLossWarps), 0, st, 1, a);
 }
 
 cudaError_t launch_backward(const BalanceArgs &a, int dtype, int gdtype, cudaStream_t st)
@@ -480,10 +525,12 @@ cudaError_t launch_backward(const BalanceArgs &a, int dtype, int gdtype, cudaStr
     return with_dtype(dtype, [&](auto t) {
         return with_row(a.E, four, [&](auto per, auto vec) {
             using T = decltype(t);
-            const dim3 grid((a.T + a.chunk - 1) / a.chunk);
             constexpr int PER = decltype(per)::value, VEC = decltype(vec)::value;
-            return gdtype == dtype ? launch_kernel(balance_backward_kernel<T, T, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, a)
-                                   : launch_kernel(balance_backward_kernel<T, float, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, a);
+            BalanceArgs b = a;
+            b.chunk = chunk_tokens(a.T, 152 * grad_ctas(PER));
+            const dim3 grid((a.T + b.chunk - 1) / b.chunk);
+            return gdtype == dtype ? launch_kernel(balance_backward_kernel<T, T, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, b)
+                                   : launch_kernel(balance_backward_kernel<T, float, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, b);
         });
     });
 }
