@@ -36,6 +36,7 @@ struct BalanceArgs {
     const int32_t *ids, *keff, *offsets;
     const uint8_t *valid;
     int T, E, K, S, chunk;
+    int finish;        // the kernel of the chunks forms the loss too
     // sums of a chunk's part of a sequence, in slot (chunk + sequence): a later part has a later chunk or
     // a later sequence, so no two share a slot and a sequence's are consecutive
     float *psum;       // [slots][E]
@@ -68,7 +69,11 @@ struct RawRow {
         uint2 w[PER * sizeof(T) / 8];
         T t[PER];
     };
-    __device__ RawRow() {}
+    __device__ __forceinline__ RawRow()   // (what a row does not reach is never loaded, and scores 0)
+    {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) from_f32(t[j], kNegInf);
+    }
     __device__ __forceinline__ void load(const T *row, int E, int lane)
     {
 #pragma unroll
@@ -80,10 +85,10 @@ struct RawRow {
             else *reinterpret_cast<uint2 *>(t + j) = *reinterpret_cast<const uint2 *>(row + e);
         }
     }
-    __device__ __forceinline__ void get(int E, int lane, float (&l)[PER]) const
+    __device__ __forceinline__ void get(float (&l)[PER]) const
     {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) l[j] = expert_of<VEC>(j, lane) < E ? to_f32(t[j]) : kNegInf;
+        for (int j = 0; j < PER; j += 2) pair_to_f32(t + j, l[j], l[j + 1]);
     }
 };
 
@@ -102,29 +107,56 @@ __device__ __forceinline__ float warp_max(float v)
 }
 
 constexpr float kLow = -60.0f;   // sums of scores above exp(-60) are far from fp32's smallest numbers
+constexpr float kLog2e = 1.44269504f;
 
-// f(j, score, 1 - sig) for this lane's N logits, the scores up to a common factor; a row of nothing but -inf
-// scores 0.
-template <int N, typename F>
-__device__ __forceinline__ void scores(const float (&l)[N], F &&f)
+__device__ __forceinline__ float ex2(float v)
 {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float rcp(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// sig = 1 / (1 + q) and 1 - sig = q sig with q = exp(-l).  (Where q has left fp32's range sig is 0, and so is what is
+// formed here of 1 - sig, which only stands in products with sig.)
+__device__ __forceinline__ void sigmoid(float l, float &sig, float &rest)
+{
+    const float q = ex2(-kLog2e * l);
+    sig = rcp(1.0f + q);
+    rest = sig * fminf(q, 3.0e38f);
+}
+
+// f(j, score, 1 - sig) for the row's N logits of this lane, the scores up to a common factor; a row of nothing but
+// -inf scores 0.
+template <typename T, int PER, int VEC, typename F>
+__device__ __forceinline__ void scores(const RawRow<T, PER, VEC> &raw, F &&f)
+{
+    float l[PER];
+    raw.get(l);
     bool high = false;
 #pragma unroll
-    for (int j = 0; j < N; ++j) high |= l[j] > kLow;
+    for (int j = 0; j < PER; ++j) high |= l[j] > kLow;
     if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float q = __expf(-fabsf(l[j])), r = __fdividef(1.0f, 1.0f + q), qr = q * r;
-            f(j, l[j] > 0.0f ? r : qr, l[j] > 0.0f ? qr : r);
+        for (int j = 0; j < PER; ++j) {
+            float v, rest;
+            sigmoid(l[j], v, rest);
+            f(j, v, rest);
         }
         return;
     }
     float m = kNegInf;
 #pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
+    for (int j = 0; j < PER; ++j) m = fmaxf(m, l[j]);
     m = warp_max(m);
 #pragma unroll
-    for (int j = 0; j < N; ++j) f(j, l[j] == kNegInf ? 0.0f : expf(l[j] - m), 1.0f);   // (1 + exp(l) is 1; NaN stays)
+    for (int j = 0; j < PER; ++j) f(j, l[j] == kNegInf ? 0.0f : expf(l[j] - m), 1.0f);   // (1 + exp(l) is 1; NaN stays)
 }
 
 // the last sequence that begins at or before token t
@@ -137,6 +169,28 @@ __device__ __forceinline__ int sequence_of(const int32_t *offsets, int S, int t)
         else hi = mid;
     }
     return lo;
+}
+
+// the slots of a sequence's sums (none where its offsets are wrong: false)
+__device__ __forceinline__ bool slots_of(const BalanceArgs &p, int s, int &first, int &last)
+{
+    const int lo = p.offsets[s], hi = p.offsets[s + 1];
+    first = 0;
+    last = -1;
+    if (lo < 0 || lo > hi || hi > p.T) return false;
+    if (lo < hi) {
+        first = lo / p.chunk + s;
+        last = (hi - 1) / p.chunk + s;
+    }
+    return true;
+}
+
+// by one thread, at the very end
+__device__ __forceinline__ void put_loss(const BalanceArgs &p, float total, int used, bool wrong)
+{
+    if (wrong) atomicOr(p.err, kErrBadOffsets);
+    p.loss[0] = wrong ? __int_as_float(0x7fc00000) : used ? total / (float)used : 0.0f;
+    *p.ticket = 0;
 }
 
 template <typename T, int PER, int VEC>
@@ -164,20 +218,18 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
         const T *logits = static_cast<const T *>(p.logits);
         if (lo + warp < hi) raw.load(logits + (size_t)(lo + warp) * p.ld, p.E, lane);
         for (int t = lo + warp; t < hi; t += kWarps) {
-            float l[PER];
-            raw.get(p.E, lane, l);
+            float v[PER], total = 0.0f;
+            scores(raw, [&](int j, float score, float) {
+                v[j] = score;
+                total += score;
+            });
             if (t + kWarps < hi) raw.load(logits + (size_t)(t + kWarps) * p.ld, p.E, lane);
             if (p.valid && !p.valid[t]) continue;
             ++counted;
-            float total = 0.0f;
-            scores(l, [&](int j, float v, float) {
-                l[j] = v;
-                total += v;
-            });
             total = warp_sum(total);
-            const float inv = total == 0.0f ? 0.0f : __fdividef(1.0f, total);
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-            for (int j = 0; j < PER; ++j) sum[j] = fmaf(l[j], inv, sum[j]);
+            for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
         }
         int pairs = 0;
         for (int i = tid; i < (hi - lo) * p.K; i += 32 * kWarps) {
@@ -217,6 +269,56 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
         }
         __syncthreads();
     }
+    if (!p.finish) return;
+    // few sums: the last CTA adds them up, a sequence a warp
+    if (tid == 0) {
+        __threadfence();
+        s_seq = atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_seq) return;
+    __threadfence();
+    float total = 0.0f;
+    int used = 0;
+    bool wrong = false;
+    for (int s = warp; s < p.S; s += kWarps) {
+        int first, last;
+        wrong |= !slots_of(p, s, first, last);
+        int tokens = 0, pairs = 0;
+        for (int i = first + lane; i <= last; i += 32) {
+            tokens += __ldcg(p.pmeta + 2 * i);
+            pairs += __ldcg(p.pmeta + 2 * i + 1);
+        }
+        tokens = __reduce_add_sync(0xffffffffu, tokens);
+        pairs = __reduce_add_sync(0xffffffffu, pairs);
+        if (lane == 0) p.tokens[s] = tokens;
+        used += tokens > 0;
+        const float even = pairs > 0 ? (float)p.E / ((float)pairs * (float)max(tokens, 1)) : 0.0f;
+        for (int e = lane; e < p.E; e += 32) {
+            float sum = 0.0f;
+            int count = 0;
+#pragma unroll 4
+            for (int i = first; i <= last; ++i) {
+                sum += __ldcg(p.psum + (size_t)i * p.E + e);
+                count += __ldcg(p.pcount + (size_t)i * p.E + e);
+            }
+            p.counts[(size_t)s * p.E + e] = count;
+            total = fmaf((float)count * even, sum, total);
+        }
+    }
+    total = warp_sum(total);
+    if (tid < 2) s_meta[tid] = 0;
+    __syncthreads();
+    if (lane == 0) {
+        s_sum[0][warp] = total;
+        if (used) atomicAdd(&s_meta[0], used);
+        if (wrong) atomicOr(&s_meta[1], 1);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kWarps; ++w) total += s_sum[0][w];
+        put_loss(p, total, s_meta[0], s_meta[1] != 0);
+    }
 }
 
 // A sequence's sums for 32 experts a CTA; the last CTA adds up the loss.
@@ -230,13 +332,8 @@ __global__ void __launch_bounds__(32 * kLossWarps) balance_loss_kernel(const Bal
     const int s = blockIdx.x, e = blockIdx.y * 32 + lane;
     if (tid < 2) s_meta[tid] = 0;
     __syncthreads();
-    const int lo = p.offsets[s], hi = p.offsets[s + 1];
-    const bool bad = lo < 0 || lo > hi || hi > p.T;
-    int first = 0, last = -1;
-    if (!bad && lo < hi) {
-        first = lo / p.chunk + s;
-        last = (hi - 1) / p.chunk + s;
-    }
+    int first, last;
+    slots_of(p, s, first, last);
     float sum = 0.0f;
     int count = 0, meta[2] = {0, 0};
     if (e < p.E)
@@ -288,9 +385,7 @@ __global__ void __launch_bounds__(32 * kLossWarps) balance_loss_kernel(const Bal
     __syncthreads();
     if (tid == 0) {
         for (int w = 1; w < kLossWarps; ++w) total += s_sum[0][w];
-        if (s_bad) atomicOr(p.err, kErrBadOffsets);
-        p.loss[0] = s_bad ? __int_as_float(0x7fc00000) : s_used ? total / (float)s_used : 0.0f;
-        *p.ticket = 0;
+        put_loss(p, total, s_used, s_bad != 0);
     }
 }
 
@@ -344,15 +439,13 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
             to = p.offsets[s + 1];
         }
         const bool inside = from <= t && t < to && !(p.valid && !p.valid[t]);
-        float d[PER];
-        raw.get(p.E, lane, d);
+        float d[PER], total = 0.0f, dot = 0.0f;
         const int keff = next_keff, id = lane < min(keff, p.K) ? next_id : -1;
         const float my_dw = next_dw;
-        fetch(t + kWarps);
         const bool on = inside && p.dw && id >= 0 && id < p.E;
         const float mine = on ? to_f32(logits[(size_t)t * p.ld + id]) : kNegInf;   // (in L1)
-        if (inside) {
-            if (p.dloss && s != have) {   // G of another sequence
+        if (inside && p.dloss) {
+            if (s != have) {   // G of another sequence
                 have = s;
                 int pairs = 0;
 #pragma unroll
@@ -366,40 +459,43 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
 #pragma unroll
                 for (int j = 0; j < PER; ++j) slope[j] *= each;
             }
-            float total = 0.0f, dot = 0.0f;
+            scores(raw, [&](int j, float v, float rest) {
+                total += v;
+                dot = fmaf(v, slope[j], dot);
+                d[j] = v * rest;
+            });
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) d[j] = 0.0f;
+        }
+        fetch(t + kWarps);
+        if (inside) {
             if (p.dloss) {
-                scores(d, [&](int j, float v, float rest) {
-                    total += v;
-                    dot = fmaf(v, slope[j], dot);
-                    d[j] = v * rest;
-                });
                 total = warp_sum(total);
                 dot = warp_sum(dot);
-                const float inv = total == 0.0f ? 0.0f : __fdividef(1.0f, total);
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
                 dot *= inv;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) d[j] *= (slope[j] - dot) * inv;
-            } else {
-#pragma unroll
-                for (int j = 0; j < PER; ++j) d[j] = 0.0f;
             }
             if (p.dw) {
                 if (lane < min(keff, p.K) && !on) atomicOr(p.err, kErrBadExpertId);
                 if (keff < 0 || keff > p.K) atomicOr(p.err, kErrBadKeff);
-                const float l1[1] = {mine};
                 const float dw = on ? my_dw : 0.0f;
-                float val, g = 0.0f, r = 1.0f;
-                scores(l1, [&](int, float v, float rest) {
-                    g = v;
-                    r = rest;
-                });
+                float val, g, r;
+                sigmoid(mine, g, r);
                 if (p.norm) {
+                    if (!__any_sync(0xffffffffu, mine > kLow)) {
+                        const float m = warp_max(mine);
+                        g = mine == kNegInf ? 0.0f : expf(mine - m);
+                        r = 1.0f;
+                    }
                     const float sum = warp_sum(g);
                     const float h = sum == 0.0f ? 0.0f : g / sum;
                     val = p.scale * h * r * (dw - warp_sum(h * dw));
                 } else {
-                    const float q = __expf(-fabsf(mine));
-                    val = p.scale * (mine > 0.0f ? 1.0f - r : q * r) * r * dw;
+                    const float q = __expf(-fabsf(mine)), one = rcp(1.0f + q);   // sig (1 - sig), the same for l and -l
+                    val = p.scale * q * one * one * dw;
                 }
                 const unsigned same = __match_any_sync(0xffffffffu, on ? id : -1 - lane);
                 if (__all_sync(0xffffffffu, same == 1u << lane)) {
@@ -428,9 +524,6 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
                 if (on) add[id] = 0.0f;
                 __syncwarp();
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < PER; ++j) d[j] = 0.0f;
         }
         G *row = static_cast<G *>(p.dlogits) + (size_t)t * p.E;
         if constexpr (VEC == 4) {
@@ -505,17 +598,23 @@ bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
 // four logits at a time where every row allows it
 bool by_four(const BalanceArgs &a, int dtype) { return a.E % 4 == 0 && a.ld % 4 == 0 && !off(a.logits, 4 * elem_bytes(dtype)); }
 
-cudaError_t launch_forward(const BalanceArgs &a, int dtype, cudaStream_t st)
+// One kernel where the last CTA has few sums to add, 16384 of a chunk and expert: 64 tokens of 64 experts XX us
+// against YY for two kernels, ZZ
+constexpr int kFinishSums = 16384;
+
+cudaError_t launch_forward(BalanceArgs a, int dtype, cudaStream_t st)
 {
-    cudaError_t e = cudaSuccess;
-    if (a.T > 0)
-        e = with_dtype(dtype, [&](auto t) {
+    const long long chunks = (a.T + a.chunk - 1) / a.chunk;
+    a.finish = a.T > 0 && (chunks + a.S) * a.E <= kFinishSums;
+    if (a.T > 0) {
+        const cudaError_t e = with_dtype(dtype, [&](auto t) {
             return with_row(a.E, by_four(a, dtype), [&](auto per, auto vec) {
-                return launch_kernel(balance_parts_kernel<decltype(t), decltype(per)::value, decltype(vec)::value>,
-                                     dim3((a.T + a.chunk - 1) / a.chunk), dim3(32 * kWarps), 0, st, 1, a);
+                return launch_kernel(balance_parts_kernel<decltype(t), decltype(per)::value, decltype(vec)::value>, dim3((unsigned)chunks),
+                                     dim3(32 * kWarps), 0, st, 1, a);
             });
         });
-    if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || a.finish) return e;
+    }
     return launch_kernel(balance_loss_kernel, dim3(a.S, (a.E + 31) / 32), dim3(32 * kLossWarps), 0, st, 1, a);
 }
 
