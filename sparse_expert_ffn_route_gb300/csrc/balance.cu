@@ -598,9 +598,10 @@ bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
 // four logits at a time where every row allows it
 bool by_four(const BalanceArgs &a, int dtype) { return a.E % 4 == 0 && a.ld % 4 == 0 && !off(a.logits, 4 * elem_bytes(dtype)); }
 
-// One kernel where the last CTA has few sums to add, 16384 of a chunk and expert: 64 tokens of 64 experts XX us
-// against YY for two kernels, ZZ
-constexpr int kFinishSums = 16384;
+// One kernel where the last CTA has few sums (of a chunk and expert) to add, else a second one.  Microseconds, one
+// kernel and two: 16 tokens of 64 experts (128 sums) 5.5, 7.3; 64 of 64 in 3 sequences (448) 8.4, 9.3; 64 of 256
+// (1280) 8.7, 7.6; 256 of 256 (4352) 18.0, 7.6.
+constexpr int kFinishSums = 1024;
 
 cudaError_t launch_forward(BalanceArgs a, int dtype, cudaStream_t st)
 {
