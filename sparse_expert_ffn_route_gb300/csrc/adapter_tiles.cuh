@@ -221,28 +221,33 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
     }
     __syncwarp();
     cluster_sync();   // every CTA's sums are there
-    if (warp >= kFirstEpi) {
-        // this CTA's share of the rows: added over the cluster and cut into two 16-bit parts
-        const int rows = kTileRows / a.splits, count = t.hi - t.lo;
-        for (int i = warp - kFirstEpi; i < rows; i += 4) {
-            const int row = rank * rows + i;
-            if (row >= count) break;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (4 * lane < p.R) {
-                const uint32_t from = r0 + (uint32_t)(row * pitch + 4 * lane) * 4;
-                float4 w[8];
+    // this CTA's share of the rows: added over the cluster, two rows of a warp at a time, and cut into two 16-bit parts
+    constexpr int kWarps = kDownThreads / 32, kAtOnce = 2;
+    const int rows = min(kTileRows / a.splits, t.hi - t.lo - rank * (kTileRows / a.splits));
+    for (int i0 = warp; i0 < rows; i0 += kWarps * kAtOnce) {
+        float4 w[kAtOnce][8];
+        if (4 * lane < p.R)
+#pragma unroll
+            for (int n = 0; n < kAtOnce; ++n) {
+                const int row = rank * (kTileRows / a.splits) + i0 + n * kWarps;
+                const uint32_t from = r0 + (uint32_t)(min(row, kTileRows - 1) * pitch + 4 * lane) * 4;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    if (q < a.splits) w[q] = ld_cluster_v4(map_rank(from, q));
+                    if (q < a.splits) w[n][q] = ld_cluster_v4(map_rank(from, q));
+            }
+#pragma unroll
+        for (int n = 0; n < kAtOnce; ++n) {
+            if (i0 + n * kWarps >= rows) continue;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (4 * lane < p.R)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     if (q < a.splits) {
-                        v[0] += w[q].x;
-                        v[1] += w[q].y;
-                        v[2] += w[q].z;
-                        v[3] += w[q].w;
+                        v[0] += w[n][q].x;
+                        v[1] += w[n][q].y;
+                        v[2] += w[n][q].z;
+                        v[3] += w[n][q].w;
                     }
-            }
             float top = 0.0f;
             bool odd = false;
 #pragma unroll
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
                 const float had = to_f32(h.t[j]), rest = v[j] * by - had;
                 from_f32(l.t[j], fabsf(had) <= 3.4e38f ? rest : 0.0f);
             }
-            const size_t line = (size_t)(t.lo + row - a.row0);
+            const size_t line = (size_t)(t.lo + rank * (kTileRows / a.splits) + i0 + n * kWarps - a.row0);
             if (4 * lane < a.r16) {
                 *reinterpret_cast<uint2 *>(static_cast<T *>(a.hi) + line * a.r16 + 4 * lane) = h.w;
                 *reinterpret_cast<uint2 *>(static_cast<T *>(a.lo) + line * a.r16 + 4 * lane) = l.w;
@@ -282,7 +287,9 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
         gemm::tmem_dealloc<false>(tmem, kTmemCols);
         __syncwarp();
     }
-    cluster_sync();   // no CTA leaves while another reads its sums
+    // no CTA leaves while another reads its sums (or, once it has given up, writes to its memory)
+    if (aborted(&c->abort)) cluster_sync();
+    else cluster_sync_relaxed();
 }
 
 template <typename T, typename Y>
