@@ -3,11 +3,14 @@
 //
 // Many rows a segment: tiles of 128 rows on the tensor cores (adapter_tiles.cuh).
 //
-// Few rows a segment (a decode batch).  A cluster of 8 CTAs takes up to 8 rows of one segment: each CTA
-// forms the rows' R numbers over its eighth of the inputs, the eighths are added in rank order through
-// distributed shared memory, and each CTA writes its eighth of the outputs.  One launch, nothing goes
-// through global memory in between.
+// Few rows a segment (a decode batch).  A cluster of 8 CTAs takes up to 4 rows of one segment: each CTA forms the
+// rows' R numbers over its eighth of the inputs and sends them to all eight, which add them in rank order, and
+// each writes its eighth of the outputs.  One launch, nothing goes through global memory in between.  It is a
+// chain of waits (list, weights, cluster, outputs), so what can be asked for early is: a thread's first row of up
+// comes during the first product, and the sums are pushed into the others' shared memory, not fetched from there
+// (64 tokens of 32 adapters, 6144 x 2048, rank 16: 10.1 us with the sums fetched and x staged, 6.9 like this).
 #include <algorithm>
+#include <cmath>
 
 #include "adapter_tiles.cuh"
 
@@ -17,28 +20,30 @@ using namespace adapter;
 
 namespace {
 
-constexpr int kFewRows = 8;       // rows of a tile
+constexpr int kFewRows = 4;       // rows of a tile
 constexpr int kFewCluster = 8;
 constexpr int kFewThreads = 256;
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// part[m][r] = sum over this CTA's inputs of x[m] down[r], M rows, four r of a warp at a time
+// Sums over this CTA's inputs k of x[m][k] down[r][k], M rows, two r of a warp at a time, sent to every CTA of the
+// cluster: to[rank][m][r].
 template <typename T, int M>
-__device__ __forceinline__ void few_down(const T *xs, int width, const T *down, long long ldd, int R, float *part, int warp, int lane)
+__device__ __forceinline__ void few_down(const T *x, long long ldx, int rows, int width, const T *down, long long ldd, int R,
+                                         float *to, int rank, int warp, int lane)
 {
-    constexpr int U = 4;
+    constexpr int U = 2, V = U * M;   // V: a power of two, at most 16
+    bool started = false;
     for (int r0 = warp * U; r0 < R; r0 += kFewThreads / 32 * U) {
-        float acc[U * M];
+        float acc[V];
 #pragma unroll
-        for (int i = 0; i < U * M; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll(M <= 2 ? 2 : 1)
         for (int k = lane * 8; k < width; k += 256) {
-            float d[U][8], x[8];
+            float d[U][8], f[8];
             Vec8<T> v[U], w;
 #pragma unroll
             for (int u = 0; u < U; ++u) v[u].load(down + (r0 + u) * ldd + k);
@@ -46,24 +51,30 @@ __device__ __forceinline__ void few_down(const T *xs, int width, const T *down, 
             for (int u = 0; u < U; ++u) v[u].get(d[u]);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                w.load(xs + (size_t)m * width + k);
-                w.get(x);
+                if (M > 2 && m >= rows) break;
+                w.load(x + min(m, rows - 1) * ldx + k);
+                w.get(f);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[u * M + m] = fmaf(x[i], d[u][i], acc[u * M + m]);
+                    for (int i = 0; i < 8; ++i) acc[u * M + m] = fmaf(f[i], d[u][i], acc[u * M + m]);
             }
         }
-        constexpr int V = U * M;   // a power of two, at most 32
         ReduceScatter<V, 16>::run(acc, lane);
-        constexpr int shift = 5 - ilog2(V);
-        const int i = lane >> shift;
-        if ((lane & ((1 << shift) - 1)) == 0) part[(i % M) * kMaxRank + r0 + i / M] = acc[0];
+        constexpr int each = 32 / V;       // lanes that hold one value
+        const int i = lane / each;
+        if (!started) gemm::cluster_wait();    // every CTA of the cluster runs
+        started = true;
+        const uint32_t at = smem_u32(to + (rank * kFewRows + i % M) * kMaxRank + r0 + i / M);
+        for (int q = lane % each; q < kFewCluster; q += each) st_cluster_f32(map_rank(at, q), acc[0]);
+        __syncwarp();
     }
+    if (!started) gemm::cluster_wait();
 }
 
 template <typename T, typename Y, int M>
-__device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, const float *u, const T *up, float scale, int n0, int n1)
+__device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, const float *u, const T *up, float scale, int n0, int n1,
+                                       const Vec8<T> (&ahead)[2])
 {
     const int rows = t.hi - t.lo;
     for (int n = n0 + threadIdx.x; n < n1; n += kFewThreads) {
@@ -71,10 +82,9 @@ __device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, cons
 #pragma unroll
         for (int m = 0; m < M; ++m) acc[m] = 0.0f;
         const T *b = up + (size_t)n * p.R;
-        for (int r = 0; r < p.R; r += 8) {
-            Vec8<T> v;
+        const bool first = n < n0 + kFewThreads;
+        const auto add = [&](const Vec8<T> &v, int r) {
             float f[8], g[8];
-            v.load(b + r);
             v.get(f);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
@@ -84,6 +94,17 @@ __device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, cons
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[m] = fmaf(g[i], f[i], acc[m]);
             }
+        };
+        int r = 0;
+        if (first) {
+            add(ahead[0], 0);
+            if (p.R > 8) add(ahead[1], 8);
+            r = 16;
+        }
+        for (; r < p.R; r += 8) {
+            Vec8<T> v;
+            v.load(b + r);
+            add(v, r);
         }
 #pragma unroll
         for (int m = 0; m < M; ++m)
@@ -96,28 +117,21 @@ __device__ __forceinline__ void few_up(const AdapterArgs &p, const Tile &t, cons
 }
 
 template <typename T, typename Y>
-__global__ void __launch_bounds__(kFewThreads) adapter_few_kernel(const AdapterArgs p)
+__global__ void __launch_bounds__(kFewThreads, 4) adapter_few_kernel(const AdapterArgs p)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float s_part[kFewRows * kMaxRank], s_u[kFewRows * kMaxRank];
-    __shared__ Tile s_tile;
+    __shared__ __align__(16) float s_part[kFewCluster * kFewRows * kMaxRank], s_u[kFewRows * kMaxRank];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tile = blockIdx.x / kFewCluster, rank = blockIdx.x % kFewCluster;
-    if (warp == 0) {
-        const Tile t = find_tile(p, tile, kFewRows, lane);
-        if (lane == 0) s_tile = t;
-        if (lane == 0 && rank == 0 && tile < p.S) check_segment(p, tile);
-    }
-    __syncthreads();
-    const Tile t = s_tile;
+    const Tile t = find_tile(p, tile, kFewRows, lane);   // (by every warp, for want of a barrier)
+    if (warp == 0 && lane == 0 && rank == 0 && tile < p.S) check_segment(p, tile);
     const int rows = t.hi - t.lo;
     if (rows <= 0) return;                       // (the same for the whole cluster)
     const int nslice = (p.N / 8 + kFewCluster - 1) / kFewCluster * 8;
     const int n0 = min(p.N, rank * nslice), n1 = min(p.N, n0 + nslice);
     if (t.adapter < 0 || t.bad) {
-        for (int m = t.lo; m < t.hi; ++m)
+        for (int m = t.lo; m < t.hi && (t.bad || p.base != p.y); ++m)
             for (int n = n0 + tid; n < n1; n += kFewThreads) {
                 const size_t at = (size_t)m * p.N + n;
                 Y v;
@@ -128,43 +142,42 @@ __global__ void __launch_bounds__(kFewThreads) adapter_few_kernel(const AdapterA
             }
         return;
     }
+    gemm::cluster_arrive();
+    // this thread's first row of up, on its way during the first product
+    const T *up = static_cast<const T *>(p.up) + (size_t)t.adapter * p.N * p.R;
+    Vec8<T> ahead[2];
+    ahead[0].zero();
+    ahead[1].zero();
+    if (n0 + tid < n1) {
+        ahead[0].load(up + (size_t)(n0 + tid) * p.R);
+        if (p.R > 8) ahead[1].load(up + (size_t)(n0 + tid) * p.R + 8);
+    }
+    const float scale = p.scale ? p.scale[t.adapter] : 1.0f;
     const int kslice = (p.K / 8 + kFewCluster - 1) / kFewCluster * 8;
     const int k0 = min(p.K, rank * kslice), width = min(p.K, k0 + kslice) - k0;
-    const int m_up = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
-    T *xs = reinterpret_cast<T *>(smem);
-    for (int i = tid * 8; i < m_up * width; i += kFewThreads * 8) {
-        const int m = i / width, k = i - m * width;
-        Vec8<T> v;
-        if (m < rows) v.load(static_cast<const T *>(p.x) + (size_t)(t.lo + m) * p.ldx + k0 + k);
-        else v.zero();
-        v.store(xs + i);
-    }
-    __syncthreads();
+    const int m_up = rows == 1 ? 1 : rows == 2 ? 2 : 4;
+    const T *x = static_cast<const T *>(p.x) + (size_t)t.lo * p.ldx + k0;
     const T *down = static_cast<const T *>(p.down) + (size_t)t.adapter * p.R * p.K + k0;
     switch (m_up) {
-    case 1: few_down<T, 1>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
-    case 2: few_down<T, 2>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
-    case 4: few_down<T, 4>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
-    default: few_down<T, 8>(xs, width, down, p.K, p.R, s_part, warp, lane); break;
+    case 1: few_down<T, 1>(x, p.ldx, rows, width, down, p.K, p.R, s_part, rank, warp, lane); break;
+    case 2: few_down<T, 2>(x, p.ldx, rows, width, down, p.K, p.R, s_part, rank, warp, lane); break;
+    default: few_down<T, 4>(x, p.ldx, rows, width, down, p.K, p.R, s_part, rank, warp, lane); break;
     }
-    cluster_sync();
+    __syncwarp();
+    cluster_sync();                              // every CTA's sums are there, and nothing is sent after this
     for (int i = tid; i < m_up * p.R; i += kFewThreads) {
         const int at = i / p.R * kMaxRank + i % p.R;
         float sum = 0.0f;
 #pragma unroll
-        for (int c = 0; c < kFewCluster; ++c) sum += ld_cluster_f32(map_rank(smem_u32(s_part + at), c));
+        for (int c = 0; c < kFewCluster; ++c) sum += s_part[c * kFewRows * kMaxRank + at];
         s_u[at] = sum;
     }
     __syncthreads();
-    const T *up = static_cast<const T *>(p.up) + (size_t)t.adapter * p.N * p.R;
-    const float scale = p.scale ? p.scale[t.adapter] : 1.0f;
     switch (m_up) {
-    case 1: few_up<T, Y, 1>(p, t, s_u, up, scale, n0, n1); break;
-    case 2: few_up<T, Y, 2>(p, t, s_u, up, scale, n0, n1); break;
-    case 4: few_up<T, Y, 4>(p, t, s_u, up, scale, n0, n1); break;
-    default: few_up<T, Y, 8>(p, t, s_u, up, scale, n0, n1); break;
+    case 1: few_up<T, Y, 1>(p, t, s_u, up, scale, n0, n1, ahead); break;
+    case 2: few_up<T, Y, 2>(p, t, s_u, up, scale, n0, n1, ahead); break;
+    default: few_up<T, Y, 4>(p, t, s_u, up, scale, n0, n1, ahead); break;
     }
-    cluster_sync();   // no CTA leaves while another reads its sums
 }
 
 // f(T()) of the two 16-bit types
@@ -177,18 +190,31 @@ auto with_half(int dtype, F &&f)
 cudaError_t launch_few(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_t st)
 {
     const long long tiles = (p.T + kFewRows - 1) / kFewRows + p.S;
-    const size_t smem = (size_t)kFewRows * ((p.K / 8 + kFewCluster - 1) / kFewCluster * 8) * 2;
     return with_half(dtype, [&](auto t) {
         return with_dtype(y_dtype, [&](auto y) {
             return launch_kernel(adapter_few_kernel<decltype(t), decltype(y)>, dim3((unsigned)(tiles * kFewCluster)), dim3(kFewThreads),
-                                 smem, st, kFewCluster, p);
+                                 0, st, kFewCluster, p);
         });
     });
 }
 
+// Which kernels, by what they take on GB300 in microseconds.  The clusters' time goes with their number for each SM
+// and with a tile's products; a tile of 128 rows costs its copies whatever stands in it.  Measured, clusters and tiles
+// (rows, segments, K, N, rank): 1, 1, 2048, 6144, 16: 4.8, 6.9; 1, 1, 6144, 6144, 64: 10.3, 8.6; 64, 64, 6144, 2048, 16: 7.1,
+// 17.2; 64, 64, 6144, 6144, 64: 25.7, 31.8; 64, 16, 6144, 6144, 64: 24.9, 13.6; 128, 16, 6144, 2048, 16: 8.9, 10.6; 256, 64,
+// 6144, 2048, 16: 14.8, 16.9; 256, 64, 6144, 6144, 64: 58.1, 30.5; 256, 256, 6144, 6144, 16: 27.2, 86.1.
+bool few_rows(const AdapterArgs &p)
+{
+    const double each = std::max(1.0, (double)p.T / p.S), rows = std::min(each, (double)kFewRows);
+    const double sms = p.S * std::ceil(each / kFewRows) * kFewCluster / num_sms(), work = (double)p.R * (p.K + p.N) / 1e5;
+    const double few = 4 + 0.5 * sms + std::max(1.0, sms) * work * (0.45 + 0.35 * rows);
+    const double tiles = 6 + 2.1e-4 * (p.K + p.N) + (p.S + (double)p.T / adapter::kTileRows) * (0.02 + 2.2e-5 * (p.K + p.N));
+    return few < tiles;
+}
+
 cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, void *workspace, size_t bytes, cudaStream_t st)
 {
-    if (p.T < 16ll * p.S) return launch_few(p, dtype, y_dtype, st);
+    if (few_rows(p)) return launch_few(p, dtype, y_dtype, st);
     return with_half(dtype, [&](auto t) {
         return with_dtype(y_dtype, [&](auto y) { return adapter::launch_tiles<decltype(t), decltype(y)>(p, dtype, workspace, bytes, st); });
     });

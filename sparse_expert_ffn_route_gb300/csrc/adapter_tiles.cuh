@@ -11,7 +11,7 @@
 //
 // What they move is x once and base and y once: bound by memory.  Two CTAs stand on an SM (half of its shared
 // memory each) with a ring of copies in flight.  One kernel for both products, the clusters handing u on
-// through distributed shared memory, was slower: 105 us where these take XX (8192 rows, 6144 x 6144, rank 64):
+// through distributed shared memory, was slower: 105 us where these take 67 (8192 rows, 6144 x 6144, rank 64):
 // every tile's exchange, 15,000 cycles, stood between its two streams.
 //
 // Warps: 0 and 1 load (x and down; base and up), 2 issues the MMAs, those from 4 on are the epilogue.  Every wait
@@ -53,8 +53,11 @@ struct TileArgs {
     int wide;            // y's rows lie on 32-byte boundaries
 };
 
+// operands with a row a tile's row: boxes of all 128, and of 32 for a tile that has no more (its other lanes
+// hold whatever was there; none of them is stored)
+constexpr int kShortRows = 32;
 struct TileMaps {
-    CUtensorMap a, b, c, d;   // x, down | base, up, hi, lo
+    CUtensorMap a[2], b, c[2], d[2];   // x, down | base, up, hi, lo
 };
 
 struct TileCtrl {
@@ -174,17 +177,19 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
     const int kper = (a.ksteps + a.splits - 1) / a.splits;
     const int k0 = min(a.ksteps, rank * kper), ksteps = min(a.ksteps, k0 + kper) - k0;
     const uint32_t r0 = smem_u32(ring);
+    const bool few = t.hi - t.lo <= kShortRows;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, &c->abort, p.err); };
     const int pitch = p.R + 4;   // of the rows' sums, which take the ring's place
     Turn at;
     bool ok = true;
     if (warp <= 1) {
         const int y = warp == 0 ? uniform(t.lo) : uniform(t.adapter) * p.R;
-        const CUtensorMap *map = warp == 0 ? &maps.a : &maps.b;
+        const CUtensorMap *map = warp == 0 ? &maps.a[few] : &maps.b;
+        const uint32_t bytes = (few ? kShortRows : kTileRows) * 128 + a.r16 * 128;
         for (int k = 0; k < ksteps; ++k, at.next(a.stages)) {
             if (at.it >= (uint32_t)a.stages && !(ok = wait(&c->empty[at.s], at.phase ^ 1))) break;
             const uint32_t bar = smem_u32(&c->full[at.s]);
-            if (warp == 0) expect_tx(bar, kXBytes + a.r16 * 128);
+            if (warp == 0) expect_tx(bar, bytes);
             tma_2d(r0 + at.s * a.stage_bytes + (warp == 0 ? 0 : kXBytes), map, 64 * (k0 + k), y, bar);
         }
         if (warp == 0)   // the last commits land before this shared memory is another kernel's
@@ -329,17 +334,19 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
     }
     const uint32_t r0 = smem_u32(ring), u0 = smem_u32(ubuf);
     const int adapter = uniform(t.adapter), row0 = uniform(t.lo);
+    const bool few = t.hi - t.lo <= kShortRows;
+    const int row_bytes = (few ? kShortRows : kTileRows) * 128;   // of a box
     const auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, &c->abort, p.err); };
     Turn at;
     bool ok = true;
     if (warp == 0) {
-        const uint32_t bytes = (p.base ? kXBytes : 0) + a.blocks * NC * 128;
+        const uint32_t bytes = (p.base ? row_bytes : 0) + a.blocks * NC * 128;
         for (int j = 0; j < nchunks; ++j, at.next(a.stages)) {
             if (j == a.stages) pdl_wait();   // (no bounded wait begins before the kernel ahead ends)
             if (j >= a.stages && !(ok = wait(&c->empty[at.s], at.phase ^ 1))) break;
             const uint32_t bar = smem_u32(&c->full[at.s]);
             expect_tx(bar, bytes);
-            if (p.base) tma_2d(r0 + at.s * a.stage_bytes, &maps.a, 64 * (chunk0 + j), row0, bar);   // 128 bytes, of whatever type
+            if (p.base) tma_2d(r0 + at.s * a.stage_bytes, &maps.a[few], 64 * (chunk0 + j), row0, bar);   // 128 bytes, of whatever type
         }
         pdl_wait();
         for (uint32_t j = at.it > (uint32_t)a.stages ? at.it - a.stages : 0; j < at.it && ok; ++j)
@@ -356,10 +363,10 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
         pdl_wait();
         pdl_launch_dependents();
         const uint32_t bar = smem_u32(&c->ufull);
-        expect_tx(bar, 2 * a.blocks * kXBytes);
+        expect_tx(bar, 2 * a.blocks * row_bytes);
         for (int b = 0; b < a.blocks; ++b) {
-            tma_2d(u0 + b * kXBytes, &maps.c, 64 * b, row0 - a.row0, bar);
-            tma_2d(u0 + (a.blocks + b) * kXBytes, &maps.d, 64 * b, row0 - a.row0, bar);
+            tma_2d(u0 + b * kXBytes, &maps.c[few], 64 * b, row0 - a.row0, bar);
+            tma_2d(u0 + (a.blocks + b) * kXBytes, &maps.d[few], 64 * b, row0 - a.row0, bar);
         }
     } else if (warp == 2) {
         const uint32_t idesc = a.idesc | (uint32_t)(NC >> 3) << 17;
@@ -466,7 +473,12 @@ cudaError_t launch_pass(TileArgs a, int dtype, cudaStream_t st)
     a.stages = std::max((sums + a.stage_bytes - 1) / a.stage_bytes,
                         std::min(kMaxTileStages, (kHalfSm - 1024 - (int)sizeof(TileCtrl)) / a.stage_bytes));
     TileMaps m;
-    cudaError_t e = rows_map(&m.a, p.x, 16, p.K, p.ldx, p.T, kTileRows);
+    cudaError_t e = cudaSuccess;
+    const auto both = [&](CUtensorMap (&map)[2], const void *from, long long cols, long long ld, long long n) {
+        if (e == cudaSuccess) e = rows_map(&map[0], from, 16, cols, ld, n, kTileRows);
+        if (e == cudaSuccess) e = rows_map(&map[1], from, 16, cols, ld, n, kShortRows);
+    };
+    both(m.a, p.x, p.K, p.ldx, p.T);
     if (e == cudaSuccess) e = rows_map(&m.b, p.down, 16, p.K, p.K, (long long)p.A * p.R, a.r16);
     if (e != cudaSuccess) return e;
     e = launch_kernel(adapter_down_kernel<T>, dim3((unsigned)tiles * a.splits), dim3(kDownThreads),
@@ -486,10 +498,10 @@ cudaError_t launch_pass(TileArgs a, int dtype, cudaStream_t st)
     const int ubytes = 2 * a.blocks * kXBytes;
     a.stages = std::min(kMaxTileStages, ((a.blocks == 1 ? 1 : 2) * kHalfSm - 1024 - (int)sizeof(TileCtrl) - ubytes) / a.stage_bytes);
     a.wide = (((uintptr_t)p.N * sizeof(Y)) | (uintptr_t)p.y) % 32 == 0;
-    if (p.base) e = rows_map(&m.a, p.base, 16, (long long)p.N * sizeof(Y) / 2, (long long)p.N * sizeof(Y) / 2, p.T, kTileRows);
+    if (p.base) both(m.a, p.base, (long long)p.N * sizeof(Y) / 2, (long long)p.N * sizeof(Y) / 2, p.T);
     if (e == cudaSuccess) e = rows_map(&m.b, p.up, 16, p.R, p.R, (long long)p.A * p.N, NC);
-    if (e == cudaSuccess) e = rows_map(&m.c, a.hi, 16, a.r16, a.r16, rows, kTileRows);
-    if (e == cudaSuccess) e = rows_map(&m.d, a.lo, 16, a.r16, a.r16, rows, kTileRows);
+    both(m.c, a.hi, a.r16, a.r16, rows);
+    both(m.d, a.lo, a.r16, a.r16, rows);
     if (e != cudaSuccess) return e;
     return launch_kernel(adapter_up_kernel<T, Y>, dim3((unsigned)tiles * a.slices), dim3(kUpThreads),
                          1024 + (size_t)a.stages * a.stage_bytes + ubytes + sizeof(TileCtrl), st, 1, a, m);
