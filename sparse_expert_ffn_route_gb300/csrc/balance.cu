@@ -159,16 +159,17 @@ __device__ __forceinline__ void scores(const RawRow<T, PER, VEC> &raw, F &&f)
     for (int j = 0; j < PER; ++j) f(j, l[j] == kNegInf ? 0.0f : expf(l[j] - m), 1.0f);   // (1 + exp(l) is 1; NaN stays)
 }
 
-// the last sequence that begins at or before token t
-__device__ __forceinline__ int sequence_of(const int32_t *offsets, int S, int t)
+// the last sequence that begins at or before token t (or the first), by a warp
+__device__ __forceinline__ int sequence_of(const int32_t *offsets, int S, int t, int lane)
 {
-    int lo = 0, hi = S;   // offsets[lo] <= t (or lo = 0) < offsets[hi] (or hi = S)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (offsets[mid] <= t) lo = mid;
-        else hi = mid;
+    int s = 0, n = S;   // it lies in [s, s + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const int got = max(1, __popc(__ballot_sync(0xffffffffu, at < n && offsets[s + at] <= t)));
+        n = min(step, n - (got - 1) * step);
+        s += (got - 1) * step;
     }
-    return lo;
+    return s;
 }
 
 // the slots of a sequence's sums (none where its offsets are wrong: false)
@@ -199,14 +200,18 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
     pdl_wait();
     pdl_launch_dependents();
     __shared__ float s_sum[kWarps][kMaxExperts];
-    __shared__ int s_count[kMaxExperts], s_meta[2], s_seq;
+    __shared__ int s_count[kMaxExperts], s_meta[2], s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
-    if (tid == 0) s_seq = sequence_of(p.offsets, p.S, begin);
+    RawRow<T, PER, VEC> raw;      // of token t, this warp's next
+    const T *logits = static_cast<const T *>(p.logits);
+    int t = begin + warp;
+    if (t < end) raw.load(logits + (size_t)t * p.ld, p.E, lane);
+    const int first_seq = sequence_of(p.offsets, p.S, begin, lane);
     for (int e = tid; e < p.E; e += 32 * kWarps) s_count[e] = 0;
     if (tid < 2) s_meta[tid] = 0;
     __syncthreads();
-    for (int s = s_seq; s < p.S; ++s) {
+    for (int s = first_seq; s < p.S; ++s) {
         const int lo = max(p.offsets[s], begin), hi = min(p.offsets[s + 1], end);
         if (p.offsets[s] >= end) break;
         if (lo >= hi) continue;
@@ -214,17 +219,14 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
 #pragma unroll
         for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
         int counted = 0;
-        RawRow<T, PER, VEC> raw;
-        const T *logits = static_cast<const T *>(p.logits);
-        if (lo + warp < hi) raw.load(logits + (size_t)(lo + warp) * p.ld, p.E, lane);
-        for (int t = lo + warp; t < hi; t += kWarps) {
+        for (; t < hi; t += kWarps) {
             float v[PER], total = 0.0f;
             scores(raw, [&](int j, float score, float) {
                 v[j] = score;
                 total += score;
             });
-            if (t + kWarps < hi) raw.load(logits + (size_t)(t + kWarps) * p.ld, p.E, lane);
-            if (p.valid && !p.valid[t]) continue;
+            if (t + kWarps < end) raw.load(logits + (size_t)(t + kWarps) * p.ld, p.E, lane);
+            if (t < lo || (p.valid && !p.valid[t])) continue;
             ++counted;
             total = warp_sum(total);
             const float inv = total == 0.0f ? 0.0f : 1.0f / total;
@@ -233,12 +235,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
         }
         int pairs = 0;
         for (int i = tid; i < (hi - lo) * p.K; i += 32 * kWarps) {
-            const int t = lo + i / p.K, k = i % p.K;
-            if (p.valid && !p.valid[t]) continue;
-            const int kept = p.keff[t];
+            const int at = lo + i / p.K, k = i % p.K;
+            const int kept = p.keff[at], e = p.ids[(size_t)at * p.K + k];
+            if (p.valid && !p.valid[at]) continue;
             if (k == 0 && (kept < 0 || kept > p.K)) atomicOr(p.err, kErrBadKeff);
             if (k >= kept) continue;
-            const int e = p.ids[(size_t)t * p.K + k];
             if (e < 0 || e >= p.E) {
                 atomicOr(p.err, kErrBadExpertId);
                 continue;
@@ -273,10 +274,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
     // few sums: the last CTA adds them up, a sequence a warp
     if (tid == 0) {
         __threadfence();
-        s_seq = atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
+        s_last = atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
     }
     __syncthreads();
-    if (!s_seq) return;
+    if (!s_last) return;
     __threadfence();
     float total = 0.0f;
     int used = 0;
@@ -399,17 +400,6 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float *add = s_add[warp];
     const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
-    if (tid == 0) s_used = 0;
-    if (p.dw)
-        for (int e = lane; e < kMaxExperts; e += 32) add[e] = 0.0f;
-    __syncthreads();
-    if (p.dloss) {
-        int used = 0;
-        for (int i = tid; i < p.S; i += 32 * kWarps) used += p.tokens[i] > 0;
-        used = __reduce_add_sync(0xffffffffu, used);
-        if (lane == 0 && used) atomicAdd(&s_used, used);
-        __syncthreads();
-    }
     const T *logits = static_cast<const T *>(p.logits);
     // of the next token: its row, and on the lanes below K its places
     RawRow<T, PER, VEC> raw;
@@ -427,7 +417,18 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
         }
     };
     fetch(begin + warp);
-    int s = sequence_of(p.offsets, p.S, begin), have = -1;
+    if (tid == 0) s_used = 0;
+    if (p.dw)
+        for (int e = lane; e < kMaxExperts; e += 32) add[e] = 0.0f;
+    __syncthreads();
+    if (p.dloss) {
+        int used = 0;
+        for (int i = tid; i < p.S; i += 32 * kWarps) used += p.tokens[i] > 0;
+        used = __reduce_add_sync(0xffffffffu, used);
+        if (lane == 0 && used) atomicAdd(&s_used, used);
+        __syncthreads();
+    }
+    int s = sequence_of(p.offsets, p.S, begin, lane), have = -1;
     int from = p.offsets[s], to = p.offsets[s + 1];
     float slope[PER];
 #pragma unroll

@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(512) norm_parts_kernel(const float *part, int 
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, h = blockIdx.x * 32 + lane;
     float sum = 0.0f;
     if (h < H)
+#pragma unroll 4
         for (int i = w; i < parts; i += 16) sum += part[((size_t)i * 3 + blockIdx.y) * H + h];
     s_sum[w][lane] = sum;
     __syncthreads();
