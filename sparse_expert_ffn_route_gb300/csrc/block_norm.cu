@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_forward_kernel(const Nor
 template <typename X, typename Y, int THREADS>
 __global__ void __launch_bounds__(THREADS, 2) norm_rows_kernel(const NormArgs p)
 {
-    constexpr bool HOLD = THREADS <= 384;   // the weights stay in registers
+    constexpr bool HOLD = THREADS <= 448;   // the weights stay in registers
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float s_sum[2][32];
     pdl_wait();
@@ -570,10 +570,10 @@ __global__ void __launch_bounds__(512) norm_parts_kernel(const float *part, int 
 int norm_threads(int H, int vecs) { return ((H / 8 + vecs - 1) / vecs + 31) / 32 * 32; }
 
 // CTAs of the backward kernel: as many as stand on 152 SMs by their registers (up to 768 threads an SM), and no
-// more than there are rows for at four each
-constexpr int kWideThreads = 1024, kGradThreads = 768;
+// more than there are rows for at two each
+constexpr int kGradThreads = 768;
 int ctas_per_sm(int H) { return std::max(1, std::min(8, kGradThreads / norm_threads(H, 1))); }
-int norm_parts(int T, int H) { return std::max(1, std::min((T + 3) / 4, 152 * ctas_per_sm(H))); }
+int norm_parts(int T, int H) { return std::max(1, std::min((T + 1) / 2, 152 * ctas_per_sm(H))); }
 
 constexpr int kRingBytesSm = 216 * 1024;   // shared memory of an SM for rings
 
@@ -587,7 +587,7 @@ cudaError_t launch_forward(const NormArgs &p, int x_dtype, int dtype, cudaStream
             const int ring = kRowStages * p.H * (int)(sizeof(X) + (p.y ? sizeof(Y) : 0) + (p.kind == kGateFull ? sizeof(Y) : 0));
             const int fit = std::min(2 * kMaxNormThreads / threads, kRingBytesSm / ring);   // CTAs of an SM
             if (fit >= 2 && p.T >= 3 * fit * num_sms())
-                return launch_kernel(threads <= 384 ? norm_rows_kernel<X, Y, 384> : norm_rows_kernel<X, Y, 512>, dim3(fit * num_sms()), dim3(threads), ring, st, 1, p);
+                return launch_kernel(threads <= 448 ? norm_rows_kernel<X, Y, 448> : norm_rows_kernel<X, Y, 512>, dim3(fit * num_sms()), dim3(threads), ring, st, 1, p);
             return launch_kernel(norm_forward_kernel<X, Y>, dim3(p.T), dim3(threads), 0, st, 1, p);
         });
     });
@@ -604,7 +604,10 @@ cudaError_t launch_backward(NormArgs p, int x_dtype, int dtype, float *dpre, flo
             p.stages = std::max(1, std::min(kMaxNormStages, kRingBytesSm / std::min((parts + 151) / 152, ctas_per_sm(p.H)) / row));
             const auto go = [&](auto kind) {
                 constexpr int KIND = decltype(kind)::value;
-                return launch_kernel(threads <= kGradThreads ? norm_backward_kernel<X, Y, kGradThreads, KIND> : norm_backward_kernel<X, Y, kWideThreads, KIND>,
+                // 80, 72 and 64 registers a thread
+                return launch_kernel(threads <= kGradThreads ? norm_backward_kernel<X, Y, kGradThreads, KIND>
+                                     : threads <= 896        ? norm_backward_kernel<X, Y, 896, KIND>
+                                                             : norm_backward_kernel<X, Y, 1024, KIND>,
                                      dim3(parts), dim3(threads), (size_t)p.stages * row, st, 1, p);
             };
             using std::integral_constant;
