@@ -571,8 +571,8 @@ def _strided(t: torch.Tensor, name: str, rows: int, width: int, device: int):
 
 
 def _gate(gate, dgate, T: int, H: int, dtype, device: int):
-    """(pointer, kind) of a gate [H] or [1][H], [T][1] or [T], or [T][H].  Of [1][H] for one token the
-    gradient's type tells: a channel's is float32."""
+    """(pointer, kind) of a gate [H] or [1][H], [T][1], or [T][H].  Of [1][H] for one token the gradient's type
+    tells: a channel's is float32."""
     if gate is None:
         return None, MOE_GATE_NONE
     shape = tuple(gate.shape)
@@ -580,7 +580,7 @@ def _gate(gate, dgate, T: int, H: int, dtype, device: int):
         kind = MOE_GATE_FULL
     elif shape in ((H,), (1, H)):
         kind = MOE_GATE_CHANNEL
-    elif shape in ((T, 1), (T,)):
+    elif shape == (T, 1):
         kind = MOE_GATE_TOKEN
     else:
         raise ValueError("gate must be [H], [T][1] or [T][H] for T %d, H %d (got %s)" % (T, H, shape))

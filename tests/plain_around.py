@@ -104,7 +104,7 @@ def balance(logits, ids, keff, offsets, K, valid=None, dloss=None, dw=None, norm
                 if 0 <= int(ids[t][i]) < E:
                     counts[s, int(ids[t][i])] += 1
     n = max(int((tokens > 0).sum()), 1)
-    f = counts * E / counts.sum(1, keepdim=True).clamp_min(1)
+    f = counts.double() * E / counts.sum(1, keepdim=True).clamp_min(1)
     slope = f / (tokens.clamp_min(1)[:, None] * n)
     loss = (slope * mean).sum()
     # exp(-|l|) to 2 units and |l| roundings of its argument, quotient, the sums over E / 32 + 5 terms

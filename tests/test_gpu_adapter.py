@@ -169,6 +169,27 @@ def test_bad_lists_are_recorded(n):
     call([0, 2 * n, n, T], [0, 1, 0])
 
 
+def test_more_than_two_to_the_31_elements():
+    """Outputs and rows past 2^31 elements, with tiles and with few rows a segment."""
+    T, K, N = 360000, 64, 6144
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    down, up = torch.randn(2, 8, K, generator=g, device="cuda").to(BF16), torch.randn(2, N, 8, generator=g, device="cuda").to(BF16)
+    y, ws = torch.empty(T, N, dtype=BF16, device="cuda"), moe.alloc_adapter_workspace()
+    for lengths in ([T - 500, 500], [2, 3] * (T // 5)):
+        off = torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+        ids = (torch.arange(len(lengths), device="cuda") % 2).to(torch.int32)
+        y.fill_(7)
+        moe.moe_adapter_matmul(x, down, up, None, off, ids, y, ws)
+        moe.moe_check_errors(ws)
+        rows = torch.tensor([0, 4, (1 << 31) // N - 1, (1 << 31) // N + 1, T - 501, T - 500, T - 1], device="cuda")
+        of = ids[torch.searchsorted(off, rows.to(torch.int32), right=True) - 1].long()
+        u = torch.einsum("tk,trk->tr", x[rows].double(), down[of].double())
+        want = torch.einsum("tr,tnr->tn", u, up[of].double())
+        mag = torch.einsum("tr,tnr->tn", torch.einsum("tk,trk->tr", x[rows].double().abs(), down[of].double().abs()), up[of].double().abs())
+        assert bool(((y[rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + (K * 2 * pa.U + 2.0 ** -17) * 1.01 * mag).all())
+
+
 def test_a_small_workspace_takes_several_passes():
     o = make([100, 400, 3, 260], [1, 0, -1, 1], 264, 136, 24, 2, before=7, after=4)
     want = run(o)

@@ -97,6 +97,49 @@ def test_parts_left_out(post, pre, gate):
     check(o, run(o))
 
 
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("T,H,stream,dt", [(2000, 1024, F32, BF16), (1001, 6144, BF16, BF16), (15000, 64, F16, F32), (1500, 7168, BF16, F16),
+                                           (3000, 2056, F32, F32)])
+def test_many_rows(T, H, stream, dt, gate):
+    """Several rows a CTA, forward too; with everything there and with parts left out."""
+    o = operands(T, H, stream, dt, gate)
+    check(o, run(o, a=1.1, b=0.5), a=1.1, b=0.5)
+    o = operands(T, H, stream, dt, gate, post=False)
+    check(o, run(o))
+    if gate == "none":
+        o = {k: v for k, v in o.items() if k in ("x", "pre_w", "dout", "dn")}
+        check(o, run(o))
+
+
+def test_many_rows_in_place():
+    o = operands(2500, 1032, BF16, BF16, "full", pad=24)
+    got = run(o)
+    check(o, got)
+    dense = {k: None if v is None else v.contiguous() for k, v in o.items()}
+    for k, v in run(dense, alias=True).items():
+        assert torch.equal(v, got[k])
+    x, y = dense["x"].clone(), dense["y"].clone()
+    moe.moe_block_norm_forward(x, 1e-5, y=y, post_w=o["post_w"], gate=o["gate"], pre_w=o["pre_w"], out=x, n=y)
+    assert torch.equal(x, got["out"]) and torch.equal(y, got["n"])
+
+
+def test_more_than_two_to_the_31_elements():
+    T, H = 540000, 4096
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty(T, H, dtype=BF16, device="cuda").normal_(generator=g)
+    w = 1 + 0.3 * randn(g, H)
+    n, kept = torch.empty_like(x), torch.empty(T, 2, device="cuda")
+    moe.moe_block_norm_forward(x, 1e-5, pre_w=w, n=n, kept=kept)
+    ws = moe.alloc_block_norm_workspace(T, H)
+    dx = torch.empty_like(x)
+    moe.moe_block_norm_backward(x, kept, ws, pre_w=w, dn=n, dx=dx)
+    moe.moe_check_errors(ws)
+    for at in (0, (1 << 31) // H - 1, (1 << 31) // H, T - 3):
+        p = slice(at, at + 3)
+        o = {"x": x[p], "pre_w": w, "dn": n[p], "dout": None}
+        check(o, {"n": n[p], "dx": dx[p]})
+
+
 def test_a_first_norm():
     """Without y: the norm ahead of a block alone, with and without a scale."""
     o = operands(50, 768, F32, BF16, "none")
