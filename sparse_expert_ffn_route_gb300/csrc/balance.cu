@@ -471,29 +471,33 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
         }
         fetch(t + kWarps);
         if (inside) {
+            const float dw = on ? my_dw : 0.0f;
+            float g = 0.0f, r = 0.0f;
+            if (p.dw) {
+                if (lane < min(keff, p.K) && !on) atomicOr(p.err, kErrBadExpertId);
+                if (keff < 0 || keff > p.K) atomicOr(p.err, kErrBadKeff);
+                sigmoid(mine, g, r);
+                if (p.norm && !__any_sync(0xffffffffu, mine > kLow)) {
+                    const float m = warp_max(mine);
+                    g = mine == kNegInf ? 0.0f : expf(mine - m);
+                    r = 1.0f;
+                }
+            }
+            // the token's four sums at once
+            float sums[4] = {total, dot, g, g * dw};
+            ReduceScatter<4, 16>::run(sums, lane);
+            total = __shfl_sync(0xffffffffu, sums[0], 0);
             if (p.dloss) {
-                total = warp_sum(total);
-                dot = warp_sum(dot);
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                dot *= inv;
+                dot = __shfl_sync(0xffffffffu, sums[0], 8) * inv;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) d[j] *= (slope[j] - dot) * inv;
             }
             if (p.dw) {
-                if (lane < min(keff, p.K) && !on) atomicOr(p.err, kErrBadExpertId);
-                if (keff < 0 || keff > p.K) atomicOr(p.err, kErrBadKeff);
-                const float dw = on ? my_dw : 0.0f;
-                float val, g, r;
-                sigmoid(mine, g, r);
+                float val;
                 if (p.norm) {
-                    if (!__any_sync(0xffffffffu, mine > kLow)) {
-                        const float m = warp_max(mine);
-                        g = mine == kNegInf ? 0.0f : expf(mine - m);
-                        r = 1.0f;
-                    }
-                    const float sum = warp_sum(g);
-                    const float h = sum == 0.0f ? 0.0f : g / sum;
-                    val = p.scale * h * r * (dw - warp_sum(h * dw));
+                    const float sum = __shfl_sync(0xffffffffu, sums[0], 16), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    val = p.scale * g * inv * r * (dw - __shfl_sync(0xffffffffu, sums[0], 24) * inv);
                 } else {
                     const float q = __expf(-fabsf(mine)), one = rcp(1.0f + q);   // sig (1 - sig), the same for l and -l
                     val = p.scale * q * one * one * dw;
