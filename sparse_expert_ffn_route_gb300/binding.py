@@ -558,15 +558,12 @@ def moe_gated_backward(dh, x, w_gate, w_up, g, u, dx, dw_gate, dw_up, workspace,
 
 
 # --- Around the expert layer: norms between blocks, the routing's balance, adapters ---------------------
-def _opt(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> Optional[int]:
-    return None if t is None else _dense(t, name, shape, dtype, device)
-
-
 def _strided(t: torch.Tensor, name: str, rows: int, width: int, device: int):
     """(pointer, row stride) of a 2-D tensor [rows][width] on `device` whose rows are contiguous."""
     dev, r, w, ld = _rows(t, name)
     if (r, w) != (rows, width) or dev != device:
-        raise ValueError("%s must be [%d][%d] on device %d (got %s on %s)" % (name, rows, width, device, tuple(t.shape), t.device))
+        raise ValueError("%s must be [%d][%d] on device %d (got %s on %s)" % (
+            name, rows, width, device, tuple(t.shape), t.device))
     return t.data_ptr(), ld
 
 
@@ -615,9 +612,12 @@ def moe_block_norm_forward(x, eps, y=None, post_w=None, gate=None, pre_w=None, o
     py, ldy = (None, 0) if y is None else _strided(y, "y", T, H, dev)
     pg, kind = _gate(gate, None, T, H, dt, dev)
     rc = load_library().moe_block_norm_forward(
-        x.data_ptr(), ld, _dtype(x, "x"), py, ldy, pg, kind, _dtype(like, "y"), _opt(post_w, "post_w", (H,), f32, dev),
-        _opt(pre_w, "pre_w", (H,), f32, dev), eps, residual_scale, branch_scale, T, H, _opt(out, "out", (T, H), x.dtype, dev),
-        _opt(n, "n", (T, H), dt, dev), _opt(kept, "kept", (T, 2), f32, dev), _raw_stream(stream, dev))
+        x.data_ptr(), ld, _dtype(x, "x"), py, ldy, pg, kind, _dtype(like, "y"),
+        None if post_w is None else _dense(post_w, "post_w", (H,), f32, dev),
+        None if pre_w is None else _dense(pre_w, "pre_w", (H,), f32, dev), eps, residual_scale, branch_scale, T, H,
+        None if out is None else _dense(out, "out", (T, H), x.dtype, dev),
+        None if n is None else _dense(n, "n", (T, H), dt, dev),
+        None if kept is None else _dense(kept, "kept", (T, 2), f32, dev), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_block_norm_forward")
 
@@ -639,10 +639,16 @@ def moe_block_norm_backward(x, kept, workspace, y=None, post_w=None, gate=None, 
             raise ValueError("dgate without a gate")
         pdg = _dense(dgate, "dgate", tuple(gate.shape), dt if kind == MOE_GATE_FULL else f32, dev)
     rc = load_library().moe_block_norm_backward(
-        x.data_ptr(), ld, _dtype(x, "x"), py, ldy, pg, kind, _dtype(like, "y"), _opt(post_w, "post_w", (H,), f32, dev),
-        _opt(pre_w, "pre_w", (H,), f32, dev), _dense(kept, "kept", (T, 2), f32, dev), residual_scale, branch_scale, T, H,
-        _opt(dout, "dout", (T, H), x.dtype, dev), _opt(dn, "dn", (T, H), dt, dev), _opt(dx, "dx", (T, H), x.dtype, dev),
-        _opt(dy, "dy", (T, H), dt, dev), pdg, _opt(dpost, "dpost", (H,), f32, dev), _opt(dpre, "dpre", (H,), f32, dev),
+        x.data_ptr(), ld, _dtype(x, "x"), py, ldy, pg, kind, _dtype(like, "y"),
+        None if post_w is None else _dense(post_w, "post_w", (H,), f32, dev),
+        None if pre_w is None else _dense(pre_w, "pre_w", (H,), f32, dev), _dense(kept, "kept", (T, 2), f32, dev),
+        residual_scale, branch_scale, T, H,
+        None if dout is None else _dense(dout, "dout", (T, H), x.dtype, dev),
+        None if dn is None else _dense(dn, "dn", (T, H), dt, dev),
+        None if dx is None else _dense(dx, "dx", (T, H), x.dtype, dev),
+        None if dy is None else _dense(dy, "dy", (T, H), dt, dev), pdg,
+        None if dpost is None else _dense(dpost, "dpost", (H,), f32, dev),
+        None if dpre is None else _dense(dpre, "dpre", (H,), f32, dev),
         _space(workspace, dev), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_block_norm_backward")
@@ -662,16 +668,16 @@ def alloc_balance_workspace(cfg: MoeConfig, max_tokens: int, max_seq: int, devic
     return ws
 
 
-def _balance(cfg, logits, ids, keff, seq_offsets, counts, tokens, valid):
-    """The operands that both directions take: (device, T, the first arguments, counts and tokens)."""
+def _routing(cfg, logits, ids, keff, seq_offsets, valid):
+    """(device, T, sequences, the operands that both directions begin with)."""
     dev, T, E, ld = _rows(logits, "logits")
-    S, K, i32 = seq_offsets.numel() - 1, cfg.top_k, torch.int32
+    S, i32 = seq_offsets.numel() - 1, torch.int32
     if E != cfg.n_experts:
         raise ValueError("logits must have n_experts = %d columns (got %d)" % (cfg.n_experts, E))
-    return (dev, T, [ctypes.byref(cfg), logits.data_ptr(), _dtype(logits, "logits"), ld, _dense(ids, "ids", (T, K), i32, dev),
-                     _dense(keff, "keff", (T,), i32, dev), T, _dense(seq_offsets, "seq_offsets", (S + 1,), i32, dev), S,
-                     _opt(valid, "valid", (T,), torch.uint8, dev)],
-            [_dense(counts, "counts", (S, E), i32, dev), _dense(tokens, "tokens", (S,), i32, dev)])
+    return dev, T, S, (ctypes.byref(cfg), logits.data_ptr(), _dtype(logits, "logits"), ld,
+                       _dense(ids, "ids", (T, cfg.top_k), i32, dev), _dense(keff, "keff", (T,), i32, dev), T,
+                       _dense(seq_offsets, "seq_offsets", (S + 1,), i32, dev), S,
+                       None if valid is None else _dense(valid, "valid", (T,), torch.uint8, dev))
 
 
 def moe_balance_forward(cfg, logits, ids, keff, seq_offsets, loss, counts, tokens, workspace, valid=None, stream=None):
@@ -679,9 +685,10 @@ def moe_balance_forward(cfg, logits, ids, keff, seq_offsets, loss, counts, token
     tokens [S] int32 (counted tokens) and loss [1] float32, from the router's logits [T][E] (float32, bfloat16 or
     float16; rows may be strided) and moe_route's ids [T][K], keff [T].  seq_offsets [S + 1] int32; valid [T] uint8
     (None: all): tokens with 0 are left out."""
-    dev, _, args, kept = _balance(cfg, logits, ids, keff, seq_offsets, counts, tokens, valid)
-    rc = load_library().moe_balance_forward(*args, _dense(loss, "loss", (1,), torch.float32, dev), *kept, _space(workspace, dev),
-                                            workspace.numel(), _raw_stream(stream, dev))
+    dev, T, S, operands = _routing(cfg, logits, ids, keff, seq_offsets, valid)
+    rc = load_library().moe_balance_forward(
+        *operands, _dense(loss, "loss", (1,), torch.float32, dev), _dense(counts, "counts", (S, cfg.n_experts), torch.int32, dev),
+        _dense(tokens, "tokens", (S,), torch.int32, dev), _space(workspace, dev), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_balance_forward")
 
@@ -691,11 +698,13 @@ def moe_balance_backward(cfg, logits, ids, keff, seq_offsets, counts, tokens, dl
     """dlogits [T][E] (float32 or the logits' type) from dloss [1] float32, the balance loss's gradient, and dw [T][K]
     float32, that of the weights moe_route applies (either may be None).  counts and tokens as
     moe_balance_forward wrote them."""
-    dev, T, args, kept = _balance(cfg, logits, ids, keff, seq_offsets, counts, tokens, valid)
-    f32 = torch.float32
+    dev, T, S, operands = _routing(cfg, logits, ids, keff, seq_offsets, valid)
+    f32, E = torch.float32, cfg.n_experts
     rc = load_library().moe_balance_backward(
-        *args, *kept, _opt(dloss, "dloss", (1,), f32, dev), _opt(dw, "dw", (T, cfg.top_k), f32, dev),
-        _dense(dlogits, "dlogits", (T, cfg.n_experts), dlogits.dtype, dev), _dtype(dlogits, "dlogits"), _space(workspace, dev),
+        *operands, _dense(counts, "counts", (S, E), torch.int32, dev), _dense(tokens, "tokens", (S,), torch.int32, dev),
+        None if dloss is None else _dense(dloss, "dloss", (1,), f32, dev),
+        None if dw is None else _dense(dw, "dw", (T, cfg.top_k), f32, dev),
+        _dense(dlogits, "dlogits", (T, E), dlogits.dtype, dev), _dtype(dlogits, "dlogits"), _space(workspace, dev),
         workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _check(rc, "moe_balance_backward")
@@ -728,8 +737,9 @@ def moe_adapter_matmul(x, down, up, scale, offsets, ids, y, workspace, base=None
     S = ids.numel()
     rc = load_library().moe_adapter_matmul(
         x.data_ptr(), ld, _dtype(x, "x"), T, K, _dense(down, "down", (A, R, K), dt, dev), _dense(up, "up", (A, N, R), dt, dev),
-        _opt(scale, "scale", (A,), torch.float32, dev), A, R, N, _dense(offsets, "offsets", (S + 1,), torch.int32, dev),
-        _dense(ids, "ids", (S,), torch.int32, dev), S, _opt(base, "base", (T, N), y.dtype, dev),
+        None if scale is None else _dense(scale, "scale", (A,), torch.float32, dev), A, R, N,
+        _dense(offsets, "offsets", (S + 1,), torch.int32, dev), _dense(ids, "ids", (S,), torch.int32, dev), S,
+        None if base is None else _dense(base, "base", (T, N), y.dtype, dev),
         _dense(y, "y", (T, N), y.dtype, dev), _dtype(y, "y"), _space(workspace, dev), workspace.numel(),
         _raw_stream(stream, dev))
     if rc:
