@@ -183,14 +183,15 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_forward_kernel(const Nor
 
 // The same on many rows: rows blockIdx, blockIdx + grid, ... on two CTAs an SM, so that one works while the other
 // waits for its warps, the next rows on their way into a ring in shared memory (asynchronous copies; a thread
-// reads back only what it copied).  8192 rows of 6144, bf16, full gate: 80 us with the weights in registers (99 with them from L1,
-// which the ring leaves too small for them), the kernel above 95.
+// reads back only what it copied).  8192 rows of 6144, bf16, full gate: 76 us with the weights in registers (99 with
+// them from L1, which the ring leaves too small for them), the kernel above 95.
 template <typename X, typename Y, int THREADS>
 __global__ void __launch_bounds__(THREADS, 2) norm_rows_kernel(const NormArgs p)
 {
     constexpr bool HOLD = THREADS <= 448;   // the weights stay in registers
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float s_sum[2][32];
+    __shared__ float s_sum[2][2][32];   // by turns: a row may exchange once only, and then no barrier stands between its
+                                        // sums' last read and the next row's
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t bx = p.H * sizeof(X), by = p.y ? p.H * sizeof(Y) : 0, bg = p.kind == kGateFull ? p.H * sizeof(Y) : 0;
@@ -227,8 +228,8 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rows_kernel(const NormArgs p)
         }
     };
     if (HOLD) weights();
-    int slot = 0, last = kRowStages - 1;
-    for (int row = blockIdx.x; row < p.T; row += step) {
+    int slot = 0, last = kRowStages - 1, turn = 0;
+    for (int row = blockIdx.x; row < p.T; row += step, turn ^= 1) {
         const size_t t = row;
         const float row_gate = next_gate;
         number(row + step);
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rows_kernel(const NormArgs p)
                 for (int i = 0; i < 8; ++i) ss[0] = fmaf(z[v][i], z[v][i], ss[0]);
             }
             if (p.post) {
-                block_sums(ss, s_sum[0], nothing);
+                block_sums(ss, s_sum[turn][0], nothing);
                 iy = inverse(ss[0], p.H, p.eps);
             }
         }
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rows_kernel(const NormArgs p)
         }
         float io = 1.0f;
         if (p.pre) {
-            block_sums(ss, s_sum[1], nothing);
+            block_sums(ss, s_sum[turn][1], nothing);
             io = inverse(ss[0], p.H, p.eps);
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
@@ -586,8 +587,10 @@ cudaError_t launch_forward(const NormArgs &p, int x_dtype, int dtype, cudaStream
             using Y = decltype(yt);
             const int ring = kRowStages * p.H * (int)(sizeof(X) + (p.y ? sizeof(Y) : 0) + (p.kind == kGateFull ? sizeof(Y) : 0));
             const int fit = std::min(2 * kMaxNormThreads / threads, kRingBytesSm / ring);   // CTAs of an SM
+            // (three rows a CTA fill its ring; with fewer the kernel of one row a CTA begins sooner)
             if (fit >= 2 && p.T >= 3 * fit * num_sms())
-                return launch_kernel(threads <= 448 ? norm_rows_kernel<X, Y, 448> : norm_rows_kernel<X, Y, 512>, dim3(fit * num_sms()), dim3(threads), ring, st, 1, p);
+                return launch_kernel(threads <= 448 ? norm_rows_kernel<X, Y, 448> : norm_rows_kernel<X, Y, 512>, dim3(fit * num_sms()),
+                                     dim3(threads), ring, st, 1, p);
             return launch_kernel(norm_forward_kernel<X, Y>, dim3(p.T), dim3(threads), 0, st, 1, p);
         });
     });

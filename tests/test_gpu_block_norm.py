@@ -111,6 +111,18 @@ def test_many_rows(T, H, stream, dt, gate):
         check(o, run(o))
 
 
+@pytest.mark.parametrize("post,pre", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("T,H", [(4000, 512), (2000, 4104)])
+def test_many_rows_are_the_same_every_time(T, H, post, pre):
+    """One exchange between a row's warps or two; the rows of a CTA follow one another without a pause."""
+    o = operands(T, H, BF16, BF16, "channel", post, pre)
+    first = run(o)
+    check(o, first)
+    for _ in range(10):
+        for k, v in run(o).items():
+            assert torch.equal(v, first[k]), k
+
+
 def test_many_rows_in_place():
     o = operands(2500, 1032, BF16, BF16, "full", pad=24)
     got = run(o)
