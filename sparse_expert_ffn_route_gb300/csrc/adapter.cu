@@ -130,18 +130,7 @@ __global__ void __launch_bounds__(kFewThreads, 4) adapter_few_kernel(const Adapt
     if (rows <= 0) return;                       // (the same for the whole cluster)
     const int nslice = (p.N / 8 + kFewCluster - 1) / kFewCluster * 8;
     const int n0 = min(p.N, rank * nslice), n1 = min(p.N, n0 + nslice);
-    if (t.adapter < 0 || t.bad) {
-        for (int m = t.lo; m < t.hi && (t.bad || p.base != p.y); ++m)
-            for (int n = n0 + tid; n < n1; n += kFewThreads) {
-                const size_t at = (size_t)m * p.N + n;
-                Y v;
-                if (t.bad) from_f32(v, __int_as_float(0x7fc00000));
-                else if (p.base) v = static_cast<const Y *>(p.base)[at];
-                else from_f32(v, 0.0f);
-                static_cast<Y *>(p.y)[at] = v;
-            }
-        return;
-    }
+    if (t.adapter < 0 || t.bad) return pass_through<Y>(p, t, n0, n1, tid, kFewThreads);
     gemm::cluster_arrive();
     // this thread's first row of up, on its way during the first product
     const T *up = static_cast<const T *>(p.up) + (size_t)t.adapter * p.N * p.R;

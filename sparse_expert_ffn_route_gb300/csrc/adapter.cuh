@@ -61,5 +61,39 @@ __device__ __forceinline__ void check_segment(const AdapterArgs &p, int s)
     if (id < -1 || id >= p.A) atomicOr(p.err, kErrBadAdapter);
 }
 
+// y = base (or zero, or NaN for a segment whose id is no adapter) for the tile's columns [n0, n1), by `threads` threads;
+// rows and columns are whole 16-byte pieces, four of a thread on their way at once
+template <typename Y>
+__device__ __forceinline__ void pass_through(const AdapterArgs &p, const Tile &t, int n0, int n1, int tid, int threads)
+{
+    if (!t.bad && p.base == p.y) return;
+    constexpr int N = 16 / sizeof(Y);
+    union Piece {
+        uint4 w;
+        Y y[N];
+        __device__ Piece() {}
+    } fill;
+#pragma unroll
+    for (int j = 0; j < N; ++j) from_f32(fill.y[j], t.bad ? __int_as_float(0x7fc00000) : 0.0f);
+    const bool copy = !t.bad && p.base;
+    const int width = (n1 - n0) / N;
+    const int total = (t.hi - t.lo) * width;   // (at most 128 rows of 2^14 pieces)
+    for (int i0 = tid; i0 < total; i0 += 4 * threads) {
+        uint4 v[4];
+        size_t at[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * threads;
+            if (i >= total) continue;
+            const int row = i / width;
+            at[j] = (size_t)(t.lo + row) * p.N + n0 + (i - row * width) * N;
+            v[j] = copy ? *reinterpret_cast<const uint4 *>(static_cast<const Y *>(p.base) + at[j]) : fill.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + j * threads < total) *reinterpret_cast<uint4 *>(static_cast<Y *>(p.y) + at[j]) = v[j];
+    }
+}
+
 }  // namespace adapter
 }  // namespace moe

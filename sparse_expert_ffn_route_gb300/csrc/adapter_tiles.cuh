@@ -318,17 +318,8 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
     if (t.lo >= t.hi || t.adapter < 0 || t.bad || nchunks == 0) {
         pdl_wait();
         pdl_launch_dependents();
-        const int n0 = chunk0 * NC, n1 = min(p.N, (chunk0 + nchunks) * NC);
-        if (t.bad || p.base != p.y)
-            for (int m = t.lo + warp; m < t.hi && (t.adapter < 0 || t.bad); m += kUpThreads / 32)
-                for (int n = n0 + lane; n < n1; n += 32) {
-                    const size_t at = (size_t)m * p.N + n;
-                    Y v;
-                    if (t.bad) from_f32(v, __int_as_float(0x7fc00000));
-                    else if (p.base) v = static_cast<const Y *>(p.base)[at];
-                    else from_f32(v, 0.0f);
-                    static_cast<Y *>(p.y)[at] = v;
-                }
+        if (t.lo < t.hi && (t.adapter < 0 || t.bad) && nchunks > 0)
+            pass_through<Y>(p, t, chunk0 * NC, min(p.N, (chunk0 + nchunks) * NC), tid, kUpThreads);
         if (warp == 2) gemm::tmem_dealloc<false>(tmem, kTmemCols);
         return;
     }

@@ -84,6 +84,22 @@ def test_many_tokens_in_one_sequence_and_across_chunks():
     check(o, dloss=1.0, dw=True)
 
 
+def test_many_short_sequences():
+    """One token each, and lengths from none to many side by side in a chunk."""
+    o = make(70, 100, 4, 70, varied=True, masked=True)
+    o["offsets"] = list(range(71))
+    check(o, dloss=1.0, dw=True)
+    for E in (40, 41):
+        o = make(2000, E, 3, 2, dtype=BF16, varied=True, masked=True)
+        g = torch.Generator().manual_seed(6)
+        lengths = (torch.rand(300, generator=g) ** 5 * 60).long().tolist()
+        off = [5]
+        for n in lengths:
+            off.append(min(1990, off[-1] + n))
+        o["offsets"] = off
+        check(o, dloss=1.0, dw=True)
+
+
 def test_tokens_outside_sequences_and_empty_ones():
     o = make(60, 24, 3, 4, before=9, after=11)
     check(o, dloss=1.0, dw=True)
