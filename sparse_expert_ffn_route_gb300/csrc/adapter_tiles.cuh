@@ -19,6 +19,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "adapter.cuh"
 #include "gemm_tc.cuh"
@@ -444,6 +445,34 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
 // bytes of the workspace for a row of a pass
 inline size_t row_bytes(int R) { return (size_t)(R + 15) / 16 * 16 * 4 + 4; }
 
+// clusters of `size` CTAs of the first kernel that the current device runs at once, two CTAs an SM (the query counts one)
+template <typename T>
+int down_clusters(int size)
+{
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][size].load();
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size * num_sms());
+    cfg.blockDim = dim3(kDownThreads);
+    cfg.dynamicSmemBytes = kHalfSm;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const void *k = reinterpret_cast<const void *>(adapter_down_kernel<T>);
+    if (ensure_dynamic_smem(k, kHalfSm) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev][size].store(2 * n);
+    return 2 * n;
+}
+
 template <typename T, typename Y>
 cudaError_t launch_pass(TileArgs a, int dtype, cudaStream_t st)
 {
@@ -455,10 +484,21 @@ cudaError_t launch_pass(TileArgs a, int dtype, cudaStream_t st)
     a.r16 = (p.R + 15) / 16 * 16;
     a.blocks = (p.R + 63) / 64;
     const int rows = std::min(p.T - a.row0, (a.cell1 - a.cell0) * kTileRows);
-    // down: as many CTAs a tile as fit at once
+    // down: the CTAs a tile (they run together, so a cluster has to fit) whose waves take least, a wave's start and
+    // sum counted as six stages.  Microseconds of the whole call by 2, 4 and 8: 8192 rows, 6144 x 6144, rank 64 70, 65, 73;
+    // 4096 rows 47, 41, 45; 3000 rows 42, 35, 33; 16000 rows, 2048 x 6144, rank 32 89, 92, 99.
     a.ksteps = (p.K + 63) / 64;
     a.splits = 1;
-    while (a.splits < 8 && 2 * a.splits * tiles <= slots && 2 * a.splits <= a.ksteps) a.splits *= 2;
+    long long best = 0;
+    for (int s = 1; s <= 8 && (s == 1 || s <= a.ksteps); s *= 2) {
+        const int fit = down_clusters<T>(s);
+        if (fit <= 0) continue;
+        const long long cost = (tiles + fit - 1) / fit * ((a.ksteps + s - 1) / s + 6);
+        if (!best || cost < best) {
+            best = cost;
+            a.splits = s;
+        }
+    }
     a.stage_bytes = kXBytes + a.r16 * 128;
     const int sums = (kTileRows * (p.R + 4) * 4 + 1023) / 1024 * 1024;
     a.stages = std::max((sums + a.stage_bytes - 1) / a.stage_bytes,
@@ -477,7 +517,7 @@ cudaError_t launch_pass(TileArgs a, int dtype, cudaStream_t st)
     if (e != cudaSuccess) return e;
     // up: the number of CTAs a tile whose waves take least, a CTA's start counted as three chunks
     a.chunks = (p.N + NC - 1) / NC;
-    long long best = 0;
+    best = 0;
     for (int s = 1; s <= std::min(a.chunks, 32); ++s) {
         const long long cost = ((long long)tiles * s + slots - 1) / slots * ((a.chunks + s - 1) / s + 3);
         if (!best || cost < best) {
