@@ -218,41 +218,49 @@ __device__ __forceinline__ void short_parts(const BalanceArgs &p, int first, int
                                             int *count, int warp, int lane)
 {
     const T *logits = static_cast<const T *>(p.logits);
-    for (int s = first + warp; s <= last; s += kWarps) {
-        const int lo = max(p.offsets[s], begin), hi = min(p.offsets[s + 1], end);
-        if (lo >= hi) continue;
-        for (int e = lane; e < p.E; e += 32) count[e] = 0;
-        __syncwarp();
-        float sum[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
-        int counted = 0, pairs = 0;
-        for (int t = lo; t < hi; ++t) {
-            raw.load(logits + (size_t)t * p.ld, p.E, lane);
-            if (p.valid && !p.valid[t]) continue;
-            ++counted;
-            if (lane < p.K) pairs += count_pair(p, t, lane, count);
-            float v[PER], total = 0.0f;
-            scores(raw, [&](int j, float score, float) {
-                v[j] = score;
-                total += score;
-            });
-            total = warp_sum(total);
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+    // (a lane looks at one of 32 sequences of the warp's, most of which may be empty)
+    for (int s0 = first + warp; s0 <= last; s0 += 32 * kWarps) {
+        const int my = s0 + lane * kWarps;
+        int my_lo = 0, my_hi = 0;
+        if (my <= last) {
+            my_lo = max(p.offsets[my], begin);
+            my_hi = min(p.offsets[my + 1], end);
         }
-        pairs = __reduce_add_sync(0xffffffffu, pairs);
-        __syncwarp();
-        const size_t slot = (size_t)blockIdx.x + s;
-        for (int e = lane; e < p.E; e += 32) p.pcount[slot * p.E + e] = count[e];
+        for (unsigned some = __ballot_sync(0xffffffffu, my_lo < my_hi); some; some &= some - 1) {
+            const int which = __ffs(some) - 1, lo = __shfl_sync(0xffffffffu, my_lo, which), hi = __shfl_sync(0xffffffffu, my_hi, which);
+            for (int e = lane; e < p.E; e += 32) count[e] = 0;
+            __syncwarp();
+            float sum[PER];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = expert_of<VEC>(j, lane);
-            if (e < p.E) p.psum[slot * p.E + e] = sum[j];
+            for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
+            int counted = 0, pairs = 0;
+            for (int t = lo; t < hi; ++t) {
+                raw.load(logits + (size_t)t * p.ld, p.E, lane);
+                if (p.valid && !p.valid[t]) continue;
+                ++counted;
+                if (lane < p.K) pairs += count_pair(p, t, lane, count);
+                float v[PER], total = 0.0f;
+                scores(raw, [&](int j, float score, float) {
+                    v[j] = score;
+                    total += score;
+                });
+                total = warp_sum(total);
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+            }
+            pairs = __reduce_add_sync(0xffffffffu, pairs);
+            __syncwarp();
+            const size_t slot = (size_t)blockIdx.x + s0 + which * kWarps;
+            for (int e = lane; e < p.E; e += 32) p.pcount[slot * p.E + e] = count[e];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int e = expert_of<VEC>(j, lane);
+                if (e < p.E) p.psum[slot * p.E + e] = sum[j];
+            }
+            if (lane < 2) p.pmeta[slot * 2 + lane] = lane ? pairs : counted;
+            __syncwarp();
         }
-        if (lane < 2) p.pmeta[slot * 2 + lane] = lane ? pairs : counted;
-        __syncwarp();
     }
 }
 
@@ -489,8 +497,8 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
 #pragma unroll
     for (int j = 0; j < PER; ++j) slope[j] = 0.0f;
     for (int t = begin + warp; t < end; t += kWarps) {
-        while (to <= t && s + 1 < p.S) {
-            ++s;
+        if (to <= t && s + 1 < p.S) {
+            s = sequence_of(p.offsets, p.S, t, lane);
             from = p.offsets[s];
             to = p.offsets[s + 1];
         }

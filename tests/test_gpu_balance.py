@@ -110,6 +110,15 @@ def test_tokens_outside_sequences_and_empty_ones():
     assert float(loss) == 0 and not counts.any() and not tokens.any() and not d.any()
 
 
+@pytest.mark.parametrize("T", [40, 400])
+def test_long_runs_of_empty_sequences(T):
+    """Between, ahead of and behind the few that have tokens."""
+    o = make(T, 24, 3, 4, varied=True)
+    runs = ((0, 700), (3, 1), (17, 333), (18, 256), (19, 1500), (T - 2, 30), (T, 90))
+    o["offsets"] = [at for at, n in runs for _ in range(n)]
+    check(o, dloss=1.0, dw=True)
+
+
 def test_padding_is_not_read():
     o = make(40, 24, 3, 2, masked=True)
     clean = run(o, dloss=1.0, dw=True)
