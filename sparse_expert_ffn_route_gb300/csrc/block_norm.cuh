@@ -404,7 +404,18 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormArgs p
             int polls = kClusterWaitLimit;
             poll(&full[slot], phase, polls);
             ok = polls > 0;
-            if (!ok) atomicOr(p.err, kErrTimeout);
+            if (!ok) {   // nothing more is asked for, and the copies in flight get their time
+                atomicOr(p.err, kErrTimeout);
+                polls = kSettleLimit;
+                uint32_t parity = phase;
+                for (int i = 0, at = slot; i < p.stages && row + i * step < p.T; ++i) {
+                    poll(&full[at], parity, polls);
+                    if (++at == p.stages) {
+                        at = 0;
+                        parity ^= 1;
+                    }
+                }
+            }
         }
         const uint8_t *sx = ring + (size_t)slot * stage, *so = sx + rb.x, *sy = so + rb.dout, *sn = sy + rb.y, *sg = sn + rb.dn;
         // What is absent reads as what leaves the formulas as they are: y, dn, dout 0, weights and gate 1.
@@ -524,10 +535,6 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormArgs p
             slot = 0;
             phase ^= 1;
         }
-    }
-    if (!ok) {   // what is still in flight gets its time
-        int polls = kSettleLimit;
-        poll(&full[slot], phase, polls);
     }
     if (!on) return;
     float *part = p.part + (size_t)blockIdx.x * 3 * p.H + h;
