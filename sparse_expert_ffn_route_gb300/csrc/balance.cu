@@ -12,8 +12,8 @@
 // Scores far below zero are taken relative to the largest, t = exp(l - m) / (1 + exp(l)), so that p keeps its
 // digits where every sig is a denormal number or zero.
 //
-// A warp holds a token's row, E / 32 logits a lane.  Both directions are one read of the logits: bound by
-// memory for the widths of a router (256 fp32 logits are 1 KB a token).
+// A warp holds a token's row, or several narrow ones at once.  Both directions are one read of the logits: bound by
+// memory for the widths of a router (256 fp32 logits are 1 KB a token), for narrower ones by the instructions a token.
 #include <algorithm>
 
 #include "launch.cuh"
@@ -32,6 +32,7 @@ constexpr int grad_ctas(int per) { return per >= 12 ? 3 : 4; }   // CTAs an SM o
 // 221 experts: 9.5 us, by the block 19.3; 2000 sequences of ten, 128 experts: by a warp each 4 us slower)
 constexpr int kShortPart = 4;
 constexpr int kMaxSequences = 1 << 20;
+static_assert(kMaxTopK <= 16, "a row's lanes hold its places");
 
 struct BalanceArgs {
     const void *logits;
@@ -58,15 +59,45 @@ struct BalanceArgs {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// A lane's part of a row: VEC 4 takes groups of four consecutive logits, VEC 1 every 32nd one.
-template <int VEC>
+// A lane's part of a row that G lanes of a warp share: VEC 4 takes groups of four consecutive logits, VEC 1 every G'th one.
+template <int VEC, int G>
 __device__ __forceinline__ int expert_of(int j, int lane)
 {
-    return VEC == 4 ? ((j >> 2) * 32 + lane) * 4 + (j & 3) : j * 32 + lane;
+    return VEC == 4 ? ((j >> 2) * G + lane) * 4 + (j & 3) : j * G + lane;
+}
+
+// the lanes of a warp that share this lane's row
+template <int G>
+__device__ __forceinline__ unsigned row_lanes()
+{
+    return G == 32 ? 0xffffffffu : ((1u << (G % 32)) - 1) << (threadIdx.x % 32 / G * G);
+}
+
+// The same over G lanes each; the whole warp comes here.
+template <int G>
+__device__ __forceinline__ bool any_of(bool v)
+{
+    return G == 32 ? __any_sync(0xffffffffu, v) : (__ballot_sync(0xffffffffu, v) & row_lanes<G>()) != 0;
+}
+
+template <int G = 32>
+__device__ __forceinline__ float sum_of(float v)
+{
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+template <int G>
+__device__ __forceinline__ float max_of(float v)
+{
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
 }
 
 // a row as it lies in memory, so that the next token's is on its way while one is worked on
-template <typename T, int PER, int VEC>
+template <typename T, int PER, int VEC, int G>
 struct RawRow {
     union __align__(16) {
         uint2 w[PER * sizeof(T) / 8];
@@ -81,7 +112,7 @@ struct RawRow {
     {
 #pragma unroll
         for (int j = 0; j < PER; j += VEC) {
-            const int e = expert_of<VEC>(j, lane);
+            const int e = expert_of<VEC, G>(j, lane);
             if (e >= E) continue;
             if constexpr (VEC == 1) t[j] = row[e];
             else if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t + j) = *reinterpret_cast<const uint4 *>(row + e);
@@ -94,20 +125,6 @@ struct RawRow {
         for (int j = 0; j < PER; j += 2) pair_to_f32(t + j, l[j], l[j + 1]);
     }
 };
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
-
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
-}
 
 constexpr float kLow = -60.0f;   // sums of scores above exp(-60) are far from fp32's smallest numbers
 constexpr float kLog2e = 1.44269504f;
@@ -137,15 +154,16 @@ __device__ __forceinline__ void sigmoid(float l, float &sig, float &rest)
 
 // f(j, score, 1 - sig) for the row's N logits of this lane, the scores up to a common factor; a row of nothing but
 // -inf scores 0.
-template <typename T, int PER, int VEC, typename F>
-__device__ __forceinline__ void scores(const RawRow<T, PER, VEC> &raw, F &&f)
+template <typename T, int PER, int VEC, int G, typename F>
+__device__ __forceinline__ void scores(const RawRow<T, PER, VEC, G> &raw, F &&f)
 {
     float l[PER];
     raw.get(l);
     bool high = false;
 #pragma unroll
     for (int j = 0; j < PER; ++j) high |= l[j] > kLow;
-    if (__any_sync(0xffffffffu, high)) {
+    high = any_of<G>(high);
+    if (G == 32 ? high : __all_sync(0xffffffffu, high)) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             float v, rest;
@@ -157,18 +175,27 @@ __device__ __forceinline__ void scores(const RawRow<T, PER, VEC> &raw, F &&f)
     float m = kNegInf;
 #pragma unroll
     for (int j = 0; j < PER; ++j) m = fmaxf(m, l[j]);
-    m = warp_max(m);
+    m = max_of<G>(m);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) f(j, l[j] == kNegInf ? 0.0f : expf(l[j] - m), 1.0f);   // (1 + exp(l) is 1; NaN stays)
+    for (int j = 0; j < PER; ++j) {
+        float v, rest;
+        sigmoid(l[j], v, rest);
+        if (!high) {   // (1 + exp(l) is 1; NaN stays)
+            v = l[j] == kNegInf ? 0.0f : expf(l[j] - m);
+            rest = 1.0f;
+        }
+        f(j, v, rest);
+    }
 }
 
-// the last sequence that begins at or before token t (or the first), by a warp
+// the last sequence that begins at or before token t (or the first), by G lanes
+template <int G>
 __device__ __forceinline__ int sequence_of(const int32_t *offsets, int S, int t, int lane)
 {
     int s = 0, n = S;   // it lies in [s, s + n)
     while (n > 1) {
-        const int step = (n + 31) / 32, at = lane * step;
-        const int got = max(1, __popc(__ballot_sync(0xffffffffu, at < n && offsets[s + at] <= t)));
+        const int step = (n + G - 1) / G, at = lane * step;
+        const int got = max(1, __popc(__ballot_sync(row_lanes<G>(), at < n && offsets[s + at] <= t)));
         n = min(step, n - (got - 1) * step);
         s += (got - 1) * step;
     }
@@ -211,16 +238,27 @@ __device__ __forceinline__ int count_pair(const BalanceArgs &p, int t, int k, in
     return 1;
 }
 
-// The parts [first, last] of a chunk, each by one warp, its row the only one on its way: many short sequences.  `count`
-// holds a warp's counts.
-template <typename T, int PER, int VEC>
-__device__ __forceinline__ void short_parts(const BalanceArgs &p, int first, int last, int begin, int end, RawRow<T, PER, VEC> &raw,
-                                            int *count, int warp, int lane)
+// the sums of a warp's groups, in the lanes of the first
+template <int PER, int G>
+__device__ __forceinline__ void add_groups(float (&sum)[PER])
 {
+#pragma unroll
+    for (int off = G; off < 32; off *= 2)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], off);
+}
+
+// The parts [first, last] of a chunk, each by one warp, its rows the only ones on their way: many short sequences.
+// `count` holds a warp's counts.
+template <typename T, int PER, int VEC, int G>
+__device__ __forceinline__ void short_parts(const BalanceArgs &p, int first, int last, int begin, int end, RawRow<T, PER, VEC, G> &raw,
+                                            int *count)
+{
+    const int warp = threadIdx.x / 32, wl = threadIdx.x % 32, lane = wl % G;
     const T *logits = static_cast<const T *>(p.logits);
     // (a lane looks at one of 32 sequences of the warp's, most of which may be empty)
     for (int s0 = first + warp; s0 <= last; s0 += 32 * kWarps) {
-        const int my = s0 + lane * kWarps;
+        const int my = s0 + wl * kWarps;
         int my_lo = 0, my_hi = 0;
         if (my <= last) {
             my_lo = max(p.offsets[my], begin);
@@ -228,58 +266,67 @@ __device__ __forceinline__ void short_parts(const BalanceArgs &p, int first, int
         }
         for (unsigned some = __ballot_sync(0xffffffffu, my_lo < my_hi); some; some &= some - 1) {
             const int which = __ffs(some) - 1, lo = __shfl_sync(0xffffffffu, my_lo, which), hi = __shfl_sync(0xffffffffu, my_hi, which);
-            for (int e = lane; e < p.E; e += 32) count[e] = 0;
+            for (int e = wl; e < p.E; e += 32) count[e] = 0;
             __syncwarp();
             float sum[PER];
 #pragma unroll
             for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
             int counted = 0, pairs = 0;
-            for (int t = lo; t < hi; ++t) {
-                raw.load(logits + (size_t)t * p.ld, p.E, lane);
-                if (p.valid && !p.valid[t]) continue;
-                ++counted;
-                if (lane < p.K) pairs += count_pair(p, t, lane, count);
+            for (int t0 = lo; t0 < hi; t0 += 32 / G) {
+                const int t = t0 + wl / G;
+                const bool on = t < hi && (!p.valid || p.valid[t]);
+                if (G == 32 && !on) continue;
+                if (t < hi) raw.load(logits + (size_t)t * p.ld, p.E, lane);
+                counted += on && lane == 0;
+                if (on && lane < p.K) pairs += count_pair(p, t, lane, count);
                 float v[PER], total = 0.0f;
                 scores(raw, [&](int j, float score, float) {
                     v[j] = score;
                     total += score;
                 });
-                total = warp_sum(total);
+                total = sum_of<G>(total);
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                if (on)
 #pragma unroll
-                for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+                    for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
             }
             pairs = __reduce_add_sync(0xffffffffu, pairs);
+            counted = __reduce_add_sync(0xffffffffu, counted);
+            add_groups<PER, G>(sum);
             __syncwarp();
             const size_t slot = (size_t)blockIdx.x + s0 + which * kWarps;
-            for (int e = lane; e < p.E; e += 32) p.pcount[slot * p.E + e] = count[e];
+            for (int e = wl; e < p.E; e += 32) p.pcount[slot * p.E + e] = count[e];
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                const int e = expert_of<VEC>(j, lane);
-                if (e < p.E) p.psum[slot * p.E + e] = sum[j];
+                const int e = expert_of<VEC, G>(j, lane);
+                if (wl < G && e < p.E) p.psum[slot * p.E + e] = sum[j];
             }
-            if (lane < 2) p.pmeta[slot * 2 + lane] = lane ? pairs : counted;
+            if (wl < 2) p.pmeta[slot * 2 + wl] = wl ? pairs : counted;
             __syncwarp();
         }
     }
 }
 
-template <typename T, int PER, int VEC>
+template <typename T, int PER, int VEC, int G>
 __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const BalanceArgs p)
 {
     pdl_wait();
     pdl_launch_dependents();
+    constexpr int R = 32 / G;     // rows of a warp
     __shared__ float s_sum[kWarps][kMaxExperts];
     __shared__ int s_count[kMaxExperts], s_meta[2], s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, wl = tid & 31, warp = tid >> 5, lane = wl % G, group = wl / G;
     const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
-    RawRow<T, PER, VEC> raw;      // of token t, this warp's next
+    RawRow<T, PER, VEC, G> raw;      // of token t0 + group, this warp's next
     const T *logits = static_cast<const T *>(p.logits);
-    int t = begin + warp;
-    if (t < end) raw.load(logits + (size_t)t * p.ld, p.E, lane);
-    const int first_seq = sequence_of(p.offsets, p.S, begin, lane), last_seq = sequence_of(p.offsets, p.S, end - 1, lane);
+    const auto fetch = [&](int t) {
+        if (t < end) raw.load(logits + (size_t)t * p.ld, p.E, lane);
+    };
+    int t0 = begin + warp * R;
+    fetch(t0 + group);
+    const int first_seq = sequence_of<32>(p.offsets, p.S, begin, wl), last_seq = sequence_of<32>(p.offsets, p.S, end - 1, wl);
     const bool many = (last_seq - first_seq) * kShortPart > end - begin;
-    if (many) short_parts<T, PER, VEC>(p, first_seq, last_seq, begin, end, raw, reinterpret_cast<int *>(s_sum[warp]), warp, lane);
+    if (many) short_parts<T, PER, VEC, G>(p, first_seq, last_seq, begin, end, raw, reinterpret_cast<int *>(s_sum[warp]));
     for (int e = tid; e < p.E; e += 32 * kWarps) s_count[e] = 0;
     if (tid < 2) s_meta[tid] = 0;
     __syncthreads();
@@ -291,29 +338,40 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
 #pragma unroll
         for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
         int counted = 0;
-        for (; t < hi; t += kWarps) {
+        while (t0 < hi) {
+            const int t = t0 + group;
+            const bool on = lo <= t && t < hi && (!p.valid || p.valid[t]);
             float v[PER], total = 0.0f;
             scores(raw, [&](int j, float score, float) {
                 v[j] = score;
                 total += score;
             });
-            if (t + kWarps < end) raw.load(logits + (size_t)(t + kWarps) * p.ld, p.E, lane);
-            if (t < lo || (p.valid && !p.valid[t])) continue;
-            ++counted;
-            total = warp_sum(total);
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            const bool over = R == 1 || t0 + R <= hi || hi == end;   // (else the next sequence has the rest of these rows)
+            if (over) {
+                t0 += kWarps * R;
+                fetch(t0 + group);
+            }
+            if (R > 1 || on) {
+                total = sum_of<G>(total);
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                if (on) {
+                    ++counted;
 #pragma unroll
-            for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+                    for (int j = 0; j < PER; ++j) sum[j] = fmaf(v[j], inv, sum[j]);
+                }
+            }
+            if (!over) break;
         }
         int pairs = 0;
         for (int i = tid; i < (hi - lo) * p.K; i += 32 * kWarps) {
             const int at = lo + i / p.K;
             if (!p.valid || p.valid[at]) pairs += count_pair(p, at, i % p.K, s_count);
         }
+        add_groups<PER, G>(sum);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = expert_of<VEC>(j, lane);
-            if (e < p.E) s_sum[warp][e] = sum[j];
+            const int e = expert_of<VEC, G>(j, lane);
+            if (group == 0 && e < p.E) s_sum[warp][e] = sum[j];
         }
         if (lane == 0 && counted) atomicAdd(&s_meta[0], counted);
         if (pairs) atomicAdd(&s_meta[1], pairs);
@@ -349,16 +407,16 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
         int first, last;
         wrong |= !slots_of(p, s, first, last);
         int tokens = 0, pairs = 0;
-        for (int i = first + lane; i <= last; i += 32) {
+        for (int i = first + wl; i <= last; i += 32) {
             tokens += __ldcg(p.pmeta + 2 * i);
             pairs += __ldcg(p.pmeta + 2 * i + 1);
         }
         tokens = __reduce_add_sync(0xffffffffu, tokens);
         pairs = __reduce_add_sync(0xffffffffu, pairs);
-        if (lane == 0) p.tokens[s] = tokens;
+        if (wl == 0) p.tokens[s] = tokens;
         used += tokens > 0;
         const float even = pairs > 0 ? (float)p.E / ((float)pairs * (float)max(tokens, 1)) : 0.0f;
-        for (int e = lane; e < p.E; e += 32) {
+        for (int e = wl; e < p.E; e += 32) {
             float sum = 0.0f;
             int count = 0;
 #pragma unroll 4
@@ -370,10 +428,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) balance_parts_kernel(const Bal
             total = fmaf((float)count * even, sum, total);
         }
     }
-    total = warp_sum(total);
+    total = sum_of(total);
     if (tid < 2) s_meta[tid] = 0;
     __syncthreads();
-    if (lane == 0) {
+    if (wl == 0) {
         s_sum[0][warp] = total;
         if (used) atomicAdd(&s_meta[0], used);
         if (wrong) atomicOr(&s_meta[1], 1);
@@ -423,7 +481,7 @@ __global__ void __launch_bounds__(32 * kLossWarps) balance_loss_kernel(const Bal
         if (e < p.E) p.counts[(size_t)s * p.E + e] = count;
         const int tokens = s_meta[0], pairs = s_meta[1];
         float part = e < p.E && pairs > 0 ? (float)count * ((float)p.E / (float)pairs) * (sum / (float)max(tokens, 1)) : 0.0f;
-        part = warp_sum(part);
+        part = sum_of(part);
         if (lane == 0) {
             p.ploss[(size_t)s * gridDim.y + blockIdx.y] = part;
             if (blockIdx.y == 0) p.tokens[s] = tokens;
@@ -442,7 +500,7 @@ __global__ void __launch_bounds__(32 * kLossWarps) balance_loss_kernel(const Bal
     }
     float total = 0.0f;
     for (long long i = tid; i < (long long)p.S * gridDim.y; i += blockDim.x) total += __ldcg(p.ploss + i);
-    total = warp_sum(total);
+    total = sum_of(total);
     if (lane == 0) s_sum[0][warp] = total;
     if (used) atomicAdd(&s_used, used);
     if (wrong) atomicOr(&s_bad, 1);
@@ -453,19 +511,23 @@ __global__ void __launch_bounds__(32 * kLossWarps) balance_loss_kernel(const Bal
     }
 }
 
-template <typename T, typename G, int PER, int VEC>
+template <typename T, typename D, int PER, int VEC, int G>
 __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_kernel(const BalanceArgs p)
 {
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ __align__(16) float s_add[kWarps][kMaxExperts];
+    constexpr int R = 32 / G;     // rows of a warp
+    constexpr unsigned ALL = 0xffffffffu;
+    __shared__ __align__(16) float s_add[kWarps][R * PER * G];
+    __shared__ uint8_t s_mark[kWarps][R * PER * G];
     __shared__ int s_used;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float *add = s_add[warp];
+    const int tid = threadIdx.x, wl = tid & 31, warp = tid >> 5, lane = wl % G, group = wl / G;
+    float *add = s_add[warp] + group * PER * G;
+    uint8_t *mark = s_mark[warp] + group * PER * G;
     const int begin = blockIdx.x * p.chunk, end = min(p.T, begin + p.chunk);
     const T *logits = static_cast<const T *>(p.logits);
     // of the next token: its row, and on the lanes below K its places
-    RawRow<T, PER, VEC> raw;
+    RawRow<T, PER, VEC, G> raw;
     int next_id = -1, next_keff = 0;
     float next_dw = 0.0f;
     const auto fetch = [&](int t) {
@@ -479,50 +541,56 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
             }
         }
     };
-    fetch(begin + warp);
+    int t0 = begin + warp * R;
+    fetch(t0 + group);
     if (tid == 0) s_used = 0;
     if (p.dw)
-        for (int e = lane; e < kMaxExperts; e += 32) add[e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) add[j * G + lane] = 0.0f;
     __syncthreads();
     if (p.dloss) {
         int used = 0;
         for (int i = tid; i < p.S; i += 32 * kWarps) used += p.tokens[i] > 0;
-        used = __reduce_add_sync(0xffffffffu, used);
-        if (lane == 0 && used) atomicAdd(&s_used, used);
+        used = __reduce_add_sync(ALL, used);
+        if (wl == 0 && used) atomicAdd(&s_used, used);
         __syncthreads();
     }
-    int s = sequence_of(p.offsets, p.S, begin, lane), have = -1;
+    int s = sequence_of<G>(p.offsets, p.S, begin, lane), have = -1;
     int from = p.offsets[s], to = p.offsets[s + 1];
     float slope[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) slope[j] = 0.0f;
-    for (int t = begin + warp; t < end; t += kWarps) {
-        if (to <= t && s + 1 < p.S) {
-            s = sequence_of(p.offsets, p.S, t, lane);
+    for (; t0 < end; t0 += kWarps * R) {
+        const int t = t0 + group;
+        if (to <= t && t < end && s + 1 < p.S) {
+            s = sequence_of<G>(p.offsets, p.S, t, lane);
             from = p.offsets[s];
             to = p.offsets[s + 1];
         }
-        const bool inside = from <= t && t < to && !(p.valid && !p.valid[t]);
+        const bool inside = t < end && from <= t && t < to && !(p.valid && !p.valid[t]);
+        const bool some = R == 1 ? inside : __any_sync(ALL, inside);
         float d[PER], total = 0.0f, dot = 0.0f;
         const int keff = next_keff, id = lane < min(keff, p.K) ? next_id : -1;
         const float my_dw = next_dw;
         const bool on = inside && p.dw && id >= 0 && id < p.E;
         const float mine = on ? to_f32(logits[(size_t)t * p.ld + id]) : kNegInf;   // (in L1)
-        if (inside && p.dloss) {
-            if (s != have) {   // G of another sequence
+        if (on) mark[id] = (uint8_t)lane;
+        if (some && p.dloss) {
+            if (inside && s != have) {   // G of another sequence
                 have = s;
                 int pairs = 0;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
-                    const int e = expert_of<VEC>(j, lane), c = e < p.E ? p.counts[(size_t)s * p.E + e] : 0;
+                    const int e = expert_of<VEC, G>(j, lane), c = e < p.E ? p.counts[(size_t)s * p.E + e] : 0;
                     pairs += c;
                     slope[j] = (float)c;
                 }
-                pairs = __reduce_add_sync(0xffffffffu, pairs);
+                pairs = __reduce_add_sync(row_lanes<G>(), pairs);
                 const float each = pairs > 0 ? p.dloss[0] * ((float)p.E / (float)pairs) / ((float)max(p.tokens[s], 1) * (float)max(s_used, 1)) : 0.0f;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) slope[j] *= each;
             }
+            __syncwarp();
             scores(raw, [&](int j, float v, float rest) {
                 total += v;
                 dot = fmaf(v, slope[j], dot);
@@ -532,41 +600,47 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
 #pragma unroll
             for (int j = 0; j < PER; ++j) d[j] = 0.0f;
         }
-        fetch(t + kWarps);
-        if (inside) {
+        fetch(t + kWarps * R);
+        if (some) {
             const float dw = on ? my_dw : 0.0f;
             float g = 0.0f, r = 0.0f;
             if (p.dw) {
-                if (lane < min(keff, p.K) && !on) atomicOr(p.err, kErrBadExpertId);
-                if (keff < 0 || keff > p.K) atomicOr(p.err, kErrBadKeff);
+                if (inside && lane < min(keff, p.K) && !on) atomicOr(p.err, kErrBadExpertId);
+                if (inside && (keff < 0 || keff > p.K)) atomicOr(p.err, kErrBadKeff);
                 sigmoid(mine, g, r);
-                if (p.norm && !__any_sync(0xffffffffu, mine > kLow)) {
-                    const float m = warp_max(mine);
-                    g = mine == kNegInf ? 0.0f : expf(mine - m);
-                    r = 1.0f;
+                if (p.norm) {
+                    const bool high = any_of<G>(mine > kLow);
+                    if (!(R == 1 ? high : __all_sync(ALL, high))) {
+                        const float m = max_of<G>(mine);
+                        if (!high) {
+                            g = mine == kNegInf ? 0.0f : expf(mine - m);
+                            r = 1.0f;
+                        }
+                    }
                 }
             }
+            __syncwarp();   // (the marks)
             // the token's four sums at once
+            constexpr int each = G / 4;   // lanes that end with one
             float sums[4] = {total, dot, g, g * dw};
-            ReduceScatter<4, 16>::run(sums, lane);
-            total = __shfl_sync(0xffffffffu, sums[0], 0);
+            ReduceScatter<4, G / 2>::run(sums, lane);
+            total = __shfl_sync(ALL, sums[0], 0, G);
             if (p.dloss) {
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                dot = __shfl_sync(0xffffffffu, sums[0], 8) * inv;
+                dot = __shfl_sync(ALL, sums[0], each, G) * inv;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) d[j] *= (slope[j] - dot) * inv;
             }
             if (p.dw) {
                 float val;
                 if (p.norm) {
-                    const float sum = __shfl_sync(0xffffffffu, sums[0], 16), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    val = p.scale * g * inv * r * (dw - __shfl_sync(0xffffffffu, sums[0], 24) * inv);
+                    const float sum = __shfl_sync(ALL, sums[0], 2 * each, G), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    val = p.scale * g * inv * r * (dw - __shfl_sync(ALL, sums[0], 3 * each, G) * inv);
                 } else {
                     const float q = __expf(-fabsf(mine)), one = rcp(1.0f + q);   // sig (1 - sig), the same for l and -l
                     val = p.scale * q * one * one * dw;
                 }
-                const unsigned same = __match_any_sync(0xffffffffu, on ? id : -1 - lane);
-                if (__all_sync(0xffffffffu, same == 1u << lane)) {
+                if (__all_sync(ALL, !on || mark[id] == lane)) {   // (a comparison of the lanes' ids takes twice the time of all this)
                     if (on) add[id] = val;
                 } else {   // an expert kept twice: in order of its places
                     for (int i = 0; i < p.K; ++i) {
@@ -577,7 +651,7 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < PER; j += VEC) {
-                    const int e = expert_of<VEC>(j, lane);   // (past E within the buffer, and zero)
+                    const int e = expert_of<VEC, G>(j, lane);   // (past E within the buffer, and zero)
                     if constexpr (VEC == 4) {
                         const float4 v = *reinterpret_cast<const float4 *>(add + e);
                         d[j] += v.x;
@@ -593,26 +667,32 @@ __global__ void __launch_bounds__(32 * kWarps, grad_ctas(PER)) balance_backward_
                 __syncwarp();
             }
         }
-        G *row = static_cast<G *>(p.dlogits) + (size_t)t * p.E;
+        if (R > 1) {   // rows that have no gradient, beside others that do
+            if (t >= end) continue;
+            if (!inside)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) d[j] = 0.0f;
+        }
+        D *row = static_cast<D *>(p.dlogits) + (size_t)t * p.E;
         if constexpr (VEC == 4) {
 #pragma unroll
             for (int j = 0; j < PER; j += 4) {
-                const int e = expert_of<4>(j, lane);
+                const int e = expert_of<4, G>(j, lane);
                 if (e >= p.E) continue;
                 union {
                     uint4 q;
                     uint2 h;
-                    G g[4];
+                    D d[4];
                 } u;
-                pair_from_f32(u.g, d[j], d[j + 1]);
-                pair_from_f32(u.g + 2, d[j + 2], d[j + 3]);
-                if constexpr (sizeof(G) == 4) *reinterpret_cast<uint4 *>(row + e) = u.q;
+                pair_from_f32(u.d, d[j], d[j + 1]);
+                pair_from_f32(u.d + 2, d[j + 2], d[j + 3]);
+                if constexpr (sizeof(D) == 4) *reinterpret_cast<uint4 *>(row + e) = u.q;
                 else *reinterpret_cast<uint2 *>(row + e) = u.h;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                const int e = expert_of<1>(j, lane);
+                const int e = expert_of<1, G>(j, lane);
                 if (e < p.E) from_f32(row[e], d[j]);
             }
         }
@@ -642,21 +722,26 @@ BalanceLayout balance_layout(int T, int E, int S)
     return L;
 }
 
-// f(logits that a lane holds, VEC) for rows of E
-template <typename F>
-cudaError_t with_row(int E, bool four, F &&f)
+// f(logits that a lane holds, VEC, lanes) for rows of E; K places fit the lanes too.  What a row costs beside its logits (the
+// sums over its lanes, the places' gradients) is shared by the rows that a warp takes at once, until the registers
+// leave too few warps.  Microseconds of 65536 tokens, both directions, by 32, 16 and 8 lanes a row: 30 experts 44, 34, 24;
+// 64 48, 33, 26; 128 50, 34, 33 (8192 tokens 16.9, 16.4, 17.6); 192 54, 42; 256 59, 51, of which forward 20.7, 21.9;
+// 384 73.4, 73.6.
+template <bool GRAD, typename F>
+cudaError_t with_row(int E, int K, bool four, F &&f)
 {
-    using std::integral_constant;
-    const int per = (E + 127) / 128 * 4;
-    const auto by_vec = [&](auto n) {
-        return four ? f(n, integral_constant<int, 4>()) : f(n, integral_constant<int, 1>());
+    const auto go = [&](auto per, auto lanes) {
+        return four ? f(per, std::integral_constant<int, 4>(), lanes) : f(per, std::integral_constant<int, 1>(), lanes);
     };
-    switch (per) {
-    case 4: return by_vec(integral_constant<int, 4>());
-    case 8: return by_vec(integral_constant<int, 8>());
-    case 12: return by_vec(integral_constant<int, 12>());
-    default: return by_vec(integral_constant<int, 16>());
-    }
+#define ROW(per, lanes) go(std::integral_constant<int, per>(), std::integral_constant<int, lanes>())
+    if (E <= 32 && K <= 8) return ROW(4, 8);
+    if (E <= 64 && K <= 8) return ROW(8, 8);
+    if (E <= 128) return ROW(8, 16);
+    if (E <= 192) return ROW(12, 16);
+    if (E <= 256) return ROW(GRAD ? 16 : 8, GRAD ? 16 : 32);
+    if (E <= 384) return ROW(12, 32);
+    return ROW(16, 32);
+#undef ROW
 }
 
 int elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
@@ -677,9 +762,9 @@ cudaError_t launch_forward(BalanceArgs a, int dtype, cudaStream_t st)
     a.finish = a.T > 0 && (chunks + a.S) * a.E <= kFinishSums;
     if (a.T > 0) {
         const cudaError_t e = with_dtype(dtype, [&](auto t) {
-            return with_row(a.E, by_four(a, dtype), [&](auto per, auto vec) {
-                return launch_kernel(balance_parts_kernel<decltype(t), decltype(per)::value, decltype(vec)::value>, dim3((unsigned)chunks),
-                                     dim3(32 * kWarps), 0, st, 1, a);
+            return with_row<false>(a.E, a.K, by_four(a, dtype), [&](auto per, auto vec, auto lanes) {
+                return launch_kernel(balance_parts_kernel<decltype(t), decltype(per)::value, decltype(vec)::value, decltype(lanes)::value>,
+                                     dim3((unsigned)chunks), dim3(32 * kWarps), 0, st, 1, a);
             });
         });
         if (e != cudaSuccess || a.finish) return e;
@@ -694,14 +779,14 @@ cudaError_t launch_backward(const BalanceArgs &a, int dtype, int gdtype, cudaStr
 {
     const bool four = by_four(a, dtype) && !off(a.dlogits, 4 * elem_bytes(gdtype));
     return with_dtype(dtype, [&](auto t) {
-        return with_row(a.E, four, [&](auto per, auto vec) {
+        return with_row<true>(a.E, a.K, four, [&](auto per, auto vec, auto lanes) {
             using T = decltype(t);
-            constexpr int PER = decltype(per)::value, VEC = decltype(vec)::value;
+            constexpr int PER = decltype(per)::value, VEC = decltype(vec)::value, G = decltype(lanes)::value;
             BalanceArgs b = a;
             b.chunk = chunk_tokens(a.T, 152 * grad_ctas(PER));
             const dim3 grid((a.T + b.chunk - 1) / b.chunk);
-            return gdtype == dtype ? launch_kernel(balance_backward_kernel<T, T, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, b)
-                                   : launch_kernel(balance_backward_kernel<T, float, PER, VEC>, grid, dim3(32 * kWarps), 0, st, 1, b);
+            return gdtype == dtype ? launch_kernel(balance_backward_kernel<T, T, PER, VEC, G>, grid, dim3(32 * kWarps), 0, st, 1, b)
+                                   : launch_kernel(balance_backward_kernel<T, float, PER, VEC, G>, grid, dim3(32 * kWarps), 0, st, 1, b);
         });
     });
 }

@@ -67,6 +67,20 @@ def test_sizes(T, E, K, S, varied, masked):
     check(o, dloss=-2.0, dw=True)
 
 
+@pytest.mark.parametrize("E,K", [(8, 8), (13, 2), (32, 8), (32, 9), (31, 16), (64, 16), (61, 3), (48, 1)])
+@pytest.mark.parametrize("T,S", [(3, 3), (45, 4), (2777, 60)])
+def test_narrow_rows(E, K, T, S):
+    """Several rows of a warp at once: cut by sequences, some of them padding, low or without an end beside others."""
+    o = make(T, E, K, S, varied=True, masked=True, seed=E * K)
+    o["logits"][1::5] -= 90
+    o["logits"][2::7, ::2] = -float("inf")
+    o["logits"][o["valid"] == 0] = float("nan")
+    check(o, dloss=0.7, dw=True)
+    check(o, dw=True, norm=False)
+    o["ids"][::3] = o["ids"][::3, :1]
+    check(o, dloss=0.7, dw=True)
+
+
 @pytest.mark.parametrize("dtype,gdtype", [(F32, F32), (BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
 def test_types(dtype, gdtype):
     for E in (60, 61):
