@@ -13,7 +13,8 @@ cudaError_t launch_forward(const NormArgs &p, int dtype, cudaStream_t st)
     return with_dtype(dtype, [&](auto yt) {
         using Y = decltype(yt);
         const int ring = kRowStages * p.H * (int)(sizeof(X) + (p.y ? sizeof(Y) : 0) + (p.kind == kGateFull ? sizeof(Y) : 0));
-        const int fit = std::min(2 * kMaxNormThreads / threads, kRingBytesSm / ring);   // CTAs of an SM
+        // CTAs of an SM, by the registers that each bound leaves a thread (72 and 64): a wave and a quarter of them takes two
+        const int fit = std::min((threads <= 448 ? 896 : 1024) / threads, kRingBytesSm / ring);
         // (three rows a CTA fill its ring; with fewer the kernel of one row a CTA begins sooner)
         if (fit >= 2 && p.T >= 3 * fit * num_sms())
             return launch_kernel(threads <= 448 ? norm_rows_kernel<X, Y, 448> : norm_rows_kernel<X, Y, 512>, dim3(fit * num_sms()),
