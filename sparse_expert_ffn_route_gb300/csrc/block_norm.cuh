@@ -334,17 +334,18 @@ struct RowBytes {
 // Beside the memory the issue slots are what is short (8192 rows of 6144, bf16, full gate; 805 MB): two vectors a
 // thread on half the warps 177 us (too few warps to fill the slots), the next row's sums beside this row's
 // results, formed twice, 211; one vector a thread, with the sums' exchange by its lanes and two conversions an
-// instruction 166; what is there known at compile time (KIND, a gate's kind with all operands and
-// gradients; -1: whatever is there) 147; the weights asked for ahead of the wait 142.
-template <typename X, typename Y, int THREADS, int KIND, bool POST>
+// instruction 166; what is there known at compile time (KIND, a gate's kind, with the gradients of all that is there;
+// -1: whatever is there) 147; the weights asked for ahead of the wait 142.  Without a pre norm 275, known at compile
+// time 135.
+template <typename X, typename Y, int THREADS, int KIND, bool POST, bool PRE>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormArgs p)
 {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t full[kMaxNormStages];
     __shared__ float s_sum[2][4 * 32];
     constexpr bool ALL = KIND >= 0;
-    const bool has_dout = ALL || p.dout, has_y = ALL || p.y, has_dn = ALL || p.dn, has_post = ALL ? POST : p.post != nullptr;
-    const bool want_dx = ALL || p.dx, want_dy = ALL || p.dy, want_post = ALL ? POST : p.want_post != 0, want_pre = ALL || p.want_pre;
+    const bool has_dout = ALL || p.dout, has_y = ALL || p.y, has_dn = ALL ? PRE : p.dn != nullptr, has_post = ALL ? POST : p.post != nullptr;
+    const bool want_dx = ALL || p.dx, want_dy = ALL || p.dy, want_post = ALL ? POST : p.want_post != 0, want_pre = ALL ? PRE : p.want_pre != 0;
     const int kind = ALL ? KIND : p.kind;
     const bool vector = kind & 1, want_channel = ALL ? KIND == kGateChannel : p.want_channel;
     const RowBytes rb(p, sizeof(X), sizeof(Y));
@@ -553,10 +554,20 @@ inline int norm_threads(int H, int vecs) { return ((H / 8 + vecs - 1) / vecs + 3
 // The backward kernel runs up to 768 threads an SM with 80 registers each: as many CTAs as whole rows fit.  (More of
 // them with 72 registers are slower, for what they spill: 6000 rows of 1792, full gate 93 us against 71, of 3336 154
 // against 142.)  Rows beyond 6144 take 896 threads with 72 registers or 1024 with 64.
-inline int ctas_per_sm(int H) { return std::max(1, std::min(8, 768 / norm_threads(H, 1))); }
+// Of one warp each, 24 (65536 rows of 256 both directions 92 us, with 8 of them 138); of more, 8 (65536 of 512 with 12: 155,
+// with 8 150).
+inline int ctas_per_sm(int H)
+{
+    const int threads = norm_threads(H, 1);
+    return std::max(1, std::min(threads == 32 ? 24 : 8, 768 / threads));
+}
 
-// Its CTAs: as many as stand on 152 SMs, and no more than there are rows for at two each
-inline int norm_parts(int T, int H) { return std::max(1, std::min((T + 1) / 2, 152 * ctas_per_sm(H))); }
+// Its CTAs: as many as stand on 152 SMs, and no more than there are rows for at two each, beyond eight an SM at four
+inline int norm_parts(int T, int H)
+{
+    const int ctas = ctas_per_sm(H), few = 152 * std::min(8, ctas);
+    return std::max(1, std::min((T + 1) / 2, std::max(few, std::min((T + 3) / 4, 152 * ctas))));
+}
 
 constexpr int kRingBytesSm = 216 * 1024;   // shared memory of an SM for rings
 

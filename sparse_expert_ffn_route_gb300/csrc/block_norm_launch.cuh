@@ -31,25 +31,28 @@ cudaError_t launch_backward(NormArgs p, int dtype, int parts, cudaStream_t st)
         using Y = decltype(yt);
         const int row = (int)RowBytes(p, sizeof(X), sizeof(Y)).total();
         p.stages = std::max(1, std::min(kMaxNormStages, kRingBytesSm / std::min((parts + 151) / 152, ctas_per_sm(p.H)) / row));
-        const auto go = [&](auto kind, auto post) {
+        const auto go = [&](auto kind, auto post, auto pre) {
             constexpr int KIND = decltype(kind)::value;
-            constexpr bool POST = decltype(post)::value;
-            return launch_kernel(threads <= 768   ? norm_backward_kernel<X, Y, 768, KIND, POST>
-                                 : threads <= 896 ? norm_backward_kernel<X, Y, 896, KIND, POST>
-                                                  : norm_backward_kernel<X, Y, 1024, KIND, POST>,
+            constexpr bool POST = decltype(post)::value, PRE = decltype(pre)::value;
+            return launch_kernel(threads <= 768   ? norm_backward_kernel<X, Y, 768, KIND, POST, PRE>
+                                 : threads <= 896 ? norm_backward_kernel<X, Y, 896, KIND, POST, PRE>
+                                                  : norm_backward_kernel<X, Y, 1024, KIND, POST, PRE>,
                                  dim3(parts), dim3(threads), (size_t)p.stages * row, st, 1, p);
         };
-        using std::bool_constant;
         using std::integral_constant;
+        constexpr std::true_type yes;
+        constexpr std::false_type no;
         const bool gate = p.kind == kGateChannel ? p.want_channel : p.kind == kGateNone || p.dgate;
-        if (!(p.dout && p.y && p.dn && p.dx && p.dy && p.want_pre && gate && p.want_post == (p.post != nullptr)))
-            return go(integral_constant<int, -1>(), bool_constant<false>());
-        const auto by_post = [&](auto kind) { return p.post ? go(kind, bool_constant<true>()) : go(kind, bool_constant<false>()); };
+        if (!(p.dout && p.y && p.dx && p.dy && gate && p.want_pre == (p.dn != nullptr) && p.want_post == (p.post != nullptr)))
+            return go(integral_constant<int, -1>(), no, no);
+        const auto with = [&](auto kind) {
+            return p.post ? p.dn ? go(kind, yes, yes) : go(kind, yes, no) : p.dn ? go(kind, no, yes) : go(kind, no, no);
+        };
         switch (p.kind) {
-        case kGateChannel: return by_post(integral_constant<int, kGateChannel>());
-        case kGateToken: return by_post(integral_constant<int, kGateToken>());
-        case kGateFull: return by_post(integral_constant<int, kGateFull>());
-        default: return by_post(integral_constant<int, kGateNone>());
+        case kGateChannel: return with(integral_constant<int, kGateChannel>());
+        case kGateToken: return with(integral_constant<int, kGateToken>());
+        case kGateFull: return with(integral_constant<int, kGateFull>());
+        default: return with(integral_constant<int, kGateNone>());
         }
     });
 }

@@ -90,6 +90,15 @@ def test_largest_rows_in_fp32():
     check(o, run(o))
 
 
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("T,H,stream,dt", [(1300, 128, F32, BF16), (9, 256, BF16, F16), (21, 6400, BF16, BF16), (13, 8192, F32, F32)])
+def test_no_norm_of_the_sum(T, H, stream, dt, gate, post):
+    """A block without a next one's norm, on one warp a row and on the widest."""
+    o = operands(T, H, stream, dt, gate, post, False)
+    check(o, run(o, a=0.5), a=0.5)
+
+
 @pytest.mark.parametrize("post,pre,gate", [(False, False, "none"), (True, False, "channel"), (False, True, "full"),
                                            (False, True, "token"), (True, False, "token")])
 def test_parts_left_out(post, pre, gate):
