@@ -43,7 +43,7 @@ cudaError_t forward(const NormArgs &p, int x_dtype, int dtype, cudaStream_t st)
 
 cudaError_t backward(const NormArgs &p, int x_dtype, int dtype, float *dpre, float *dpost, float *dchan, cudaStream_t st)
 {
-    const int parts = norm_parts(p.T, p.H);
+    const int parts = norm_parts(p.T, p.H, heavy_backward(p));
     const cudaError_t e = with_dtype(x_dtype, [&](auto x) { return norm::launch_backward<decltype(x)>(p, dtype, parts, st); });
     if (e != cudaSuccess || (!dpre && !dpost && !dchan)) return e;
     return launch_kernel(norm_parts_kernel, dim3((p.H + 31) / 32, 3), dim3(1024), 0, st, 1, (const float *)p.part, parts, p.H, dpre,
@@ -98,7 +98,7 @@ extern "C" {
 size_t moe_block_norm_workspace_size(int T, int H)
 {
     if (T < 0 || T > 1 << 24 || H < 8 || H > kMaxDim || H % 8) return 0;
-    return 256 + (size_t)norm_parts(T, H) * 3 * H * sizeof(float);
+    return 256 + (size_t)norm_parts(T, H, 0) * 3 * H * sizeof(float);
 }
 
 int moe_block_norm_forward(const void *x, long long ldx, int x_dtype, const void *y, long long ldy, const void *gate, int gate_kind,

@@ -552,22 +552,28 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormArgs p
 inline int norm_threads(int H, int vecs) { return ((H / 8 + vecs - 1) / vecs + 31) / 32 * 32; }
 
 // The backward kernel runs up to 768 threads an SM with 80 registers each: as many CTAs as whole rows fit.  (More of
-// them with 72 registers are slower, for what they spill: 6000 rows of 1792, full gate 93 us against 71, of 3336 154
-// against 142.)  Rows beyond 6144 take 896 threads with 72 registers or 1024 with 64.
-// Of one warp each, 24 (65536 rows of 256 both directions 92 us, with 8 of them 138); of more, 8 (65536 of 512 with 12: 155,
-// with 8 150).
-inline int ctas_per_sm(int H)
+// them with 72 registers are slower, for what they spill: 6000 rows of 1792, full gate 93 us against 71.)  Rows beyond
+// 6144 take 896 threads with 72 registers or 1024 with 64.  So do two rows of 3080 to 4096, which would stand alone,
+// where what a thread holds allows it (`heavy`, 0 to 2): both directions of 8192 rows in bf16, two and one, of 3584 without a
+// gate 114 us and 138, with a channel's 155 and 156 (fp32 stream 198 and 184), of 4096 without post 110 and 125, without pre
+// 101 and 119, with both 140 and 143 (fp32 stream 201 and 195), with a channel's gate too 231 and 164.
+// CTAs of one warp: 24 (65536 rows of 256 92 us, with 8 of them 138); of more, 8 (65536 of 512 with 12 155, with 8 150).
+inline int ctas_per_sm(int H, int heavy)
 {
     const int threads = norm_threads(H, 1);
+    if (threads > 384 && threads <= 512) return heavy < (threads <= 448 ? 2 : 1) ? 2 : 1;
     return std::max(1, std::min(threads == 32 ? 24 : 8, 768 / threads));
 }
 
 // Its CTAs: as many as stand on 152 SMs, and no more than there are rows for at two each, beyond eight an SM at four
-inline int norm_parts(int T, int H)
+inline int norm_parts(int T, int H, int heavy)
 {
-    const int ctas = ctas_per_sm(H), few = 152 * std::min(8, ctas);
+    const int ctas = ctas_per_sm(H, heavy), few = 152 * std::min(8, ctas);
     return std::max(1, std::min((T + 1) / 2, std::max(few, std::min((T + 3) / 4, 152 * ctas))));
 }
+
+// a post norm and a gate with columns, beside a pre norm
+inline int heavy_backward(const NormArgs &p) { return p.dn ? (p.post != nullptr) + (p.kind & 1) : 0; }
 
 constexpr int kRingBytesSm = 216 * 1024;   // shared memory of an SM for rings
 

@@ -30,13 +30,14 @@ cudaError_t launch_backward(NormArgs p, int dtype, int parts, cudaStream_t st)
     return with_dtype(dtype, [&](auto yt) {
         using Y = decltype(yt);
         const int row = (int)RowBytes(p, sizeof(X), sizeof(Y)).total();
-        p.stages = std::max(1, std::min(kMaxNormStages, kRingBytesSm / std::min((parts + 151) / 152, ctas_per_sm(p.H)) / row));
+        const int ctas = ctas_per_sm(p.H, heavy_backward(p));
+        p.stages = std::max(1, std::min(kMaxNormStages, kRingBytesSm / std::min((parts + 151) / 152, ctas) / row));
         const auto go = [&](auto kind, auto post, auto pre) {
             constexpr int KIND = decltype(kind)::value;
             constexpr bool POST = decltype(post)::value, PRE = decltype(pre)::value;
-            return launch_kernel(threads <= 768   ? norm_backward_kernel<X, Y, 768, KIND, POST, PRE>
-                                 : threads <= 896 ? norm_backward_kernel<X, Y, 896, KIND, POST, PRE>
-                                                  : norm_backward_kernel<X, Y, 1024, KIND, POST, PRE>,
+            return launch_kernel(ctas * threads <= 768   ? norm_backward_kernel<X, Y, 768, KIND, POST, PRE>
+                                 : ctas * threads <= 896 ? norm_backward_kernel<X, Y, 896, KIND, POST, PRE>
+                                                         : norm_backward_kernel<X, Y, 1024, KIND, POST, PRE>,
                                  dim3(parts), dim3(threads), (size_t)p.stages * row, st, 1, p);
         };
         using std::integral_constant;
