@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_forward_kernel(const Nor
     if (p.kept && threadIdx.x == 0) p.kept[t] = make_float2(iy, io);
 }
 
-// The same on many rows: rows blockIdx, blockIdx + grid, ... on two CTAs an SM, so that one works while the other
+// The same on many rows: rows blockIdx, blockIdx + grid, ... on two CTAs an SM or more, so that one works while another
 // waits for its warps, the next rows on their way into a ring in shared memory (asynchronous copies; a thread
 // reads back only what it copied).  8192 rows of 6144, bf16, full gate: 76 us with the weights in registers (99 with
 // them from L1, which the ring leaves too small for them), the kernel above 95.
@@ -336,7 +336,7 @@ struct RowBytes {
 // results, formed twice, 211; one vector a thread, with the sums' exchange by its lanes and two conversions an
 // instruction 166; what is there known at compile time (KIND, a gate's kind, with the gradients of all that is there;
 // -1: whatever is there) 147; the weights asked for ahead of the wait 142.  Without a pre norm 275, known at compile
-// time 135.
+// time 125.
 template <typename X, typename Y, int THREADS, int KIND, bool POST, bool PRE>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormArgs p)
 {
