@@ -232,15 +232,16 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
     const int rows = min(kTileRows / a.splits, t.hi - t.lo - rank * (kTileRows / a.splits));
     for (int i0 = warp; i0 < rows; i0 += kWarps * kAtOnce) {
         float4 w[kAtOnce][8];
-        if (4 * lane < p.R)
 #pragma unroll
-            for (int n = 0; n < kAtOnce; ++n) {
-                const int row = rank * (kTileRows / a.splits) + i0 + n * kWarps;
-                const uint32_t from = r0 + (uint32_t)(min(row, kTileRows - 1) * pitch + 4 * lane) * 4;
+        for (int n = 0; n < kAtOnce; ++n) {
+            if (i0 + n * kWarps >= rows) continue;   // nothing is read that is not used: the barrier at the end waits for no read
+            const int row = rank * (kTileRows / a.splits) + i0 + n * kWarps;
+            const uint32_t from = r0 + (uint32_t)(row * pitch + 4 * lane) * 4;
+            if (4 * lane < p.R)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     if (q < a.splits) w[n][q] = ld_cluster_v4(map_rank(from, q));
-            }
+        }
 #pragma unroll
         for (int n = 0; n < kAtOnce; ++n) {
             if (i0 + n * kWarps >= rows) continue;

@@ -37,8 +37,9 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// the same without an order of memory, for CTAs that only stay for one another's reads (a release waits for the
-// warp's global stores, 1500 cycles and more)
+// The same without an order of memory, for CTAs that only stay for one another's reads (a release waits for the
+// warp's global stores, 1500 cycles and more).  It does not wait for a read that is on its way: what a thread has
+// read of another CTA's shared memory has to be used, in something that it stores, before it comes here.
 __device__ __forceinline__ void cluster_sync_relaxed()
 {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

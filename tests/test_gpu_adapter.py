@@ -226,3 +226,14 @@ def test_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("R", [72, 128])
+@pytest.mark.parametrize("n", [5, 9, 15, 17, 33, 63, 65, 100, 127, 129, 137, 250])
+def test_short_tiles_of_a_cluster(n, R):
+    """The CTAs that share a tile's inputs have rows of their own to add up, some an odd number and some none."""
+    o = make([n], [0], 2048, 264, R, 1, out=F32)
+    check(o)
+    first = run(o)
+    for _ in range(5):
+        assert torch.equal(run(o), first)
