@@ -174,6 +174,11 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_forward_kernel(const Nor
     if (p.kept && threadIdx.x == 0) p.kept[t] = make_float2(iy, io);
 }
 
+struct RowsShared {
+    float sum[2][2][32];   // by turns: a row may exchange once only, and then no barrier stands between its sums' last
+                           // read and the next row's
+};
+
 // The same on many rows: rows blockIdx, blockIdx + grid, ... on two CTAs an SM or more, so that one works while another
 // waits for its warps, the next rows on their way into a ring in shared memory (asynchronous copies; a thread
 // reads back only what it copied).  8192 rows of 6144, bf16, full gate: 76 us with the weights in registers (99 with
@@ -183,8 +188,8 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rows_kernel(const NormArgs p)
 {
     constexpr bool HOLD = THREADS <= 448;   // the weights stay in registers
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float s_sum[2][2][32];   // by turns: a row may exchange once only, and then no barrier stands between its
-                                        // sums' last read and the next row's
+    __shared__ RowsShared sh;
+    auto &s_sum = sh.sum;
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t bx = p.H * sizeof(X), by = p.y ? p.H * sizeof(Y) : 0, bg = p.kind == kGateFull ? p.H * sizeof(Y) : 0;
@@ -327,6 +332,11 @@ struct RowBytes {
     __host__ __device__ uint32_t total() const { return x + dout + y + dn + gate; }
 };
 
+struct BackwardShared {
+    uint64_t full[kMaxNormStages];
+    float sum[2][4 * 32];
+};
+
 // Rows blockIdx, blockIdx + grid, ...; a thread keeps its 8 columns' sums over them.  The rows come through a
 // ring in shared memory (one bulk copy an operand), so that the next ones are on their way while one is worked
 // on; what is needed again after the row's one exchange between the warps stays in registers.
@@ -341,8 +351,9 @@ template <typename X, typename Y, int THREADS, int KIND, bool POST, bool PRE>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormArgs p)
 {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ uint64_t full[kMaxNormStages];
-    __shared__ float s_sum[2][4 * 32];
+    __shared__ BackwardShared sh;
+    auto &full = sh.full;
+    auto &s_sum = sh.sum;
     constexpr bool ALL = KIND >= 0;
     const bool has_dout = ALL || p.dout, has_y = ALL || p.y, has_dn = ALL ? PRE : p.dn != nullptr, has_post = ALL ? POST : p.post != nullptr;
     const bool want_dx = ALL || p.dx, want_dy = ALL || p.dy, want_post = ALL ? POST : p.want_post != 0, want_pre = ALL ? PRE : p.want_pre != 0;
@@ -575,7 +586,27 @@ inline int norm_parts(int T, int H, int heavy)
 // a post norm and a gate with columns, beside a pre norm
 inline int heavy_backward(const NormArgs &p) { return p.dn ? (p.post != nullptr) + (p.kind & 1) : 0; }
 
-constexpr int kRingBytesSm = 216 * 1024;   // shared memory of an SM for rings
+// Shared memory of an SM: what rings may take of it, all of it, and what each CTA takes beside its ring and static part
+constexpr int kRingBytesSm = 216 * 1024, kSharedBytesSm = 228 * 1024, kCtaBytes = 1024;
+
+// CTAs an SM of the forward kernel with rings of `ring` bytes, by the registers that each bound leaves a thread (72 and
+// 64) and by shared memory: a wave and a quarter of them takes two (16384 rows of 1024, fp32 stream, without a gate: 11 CTAs
+// 42 us, 12 and a second wave 48)
+inline int forward_ctas(int threads, int ring)
+{
+    const int bytes = (ring + (int)sizeof(RowsShared) + 127) / 128 * 128 + kCtaBytes;
+    return std::min((threads <= 448 ? 896 : 1024) / threads, std::min(kRingBytesSm / ring, kSharedBytesSm / bytes));
+}
+
+// Rows of `row` bytes in a ring of the backward kernel: what the CTAs of an SM share has to hold all of them, or the last
+// ones run as a second wave (65536 rows of 256, bf16, without a gate: rings of 3 rows 56 us, of 4 and a second wave 71;
+// 32768 of 768, fp32 stream: 2 rows 87, 3 rows 107).
+inline int backward_stages(int row, int parts, int ctas)
+{
+    const int share = std::min((parts + 151) / 152, ctas);
+    const int bytes = kSharedBytesSm / share / 128 * 128 - kCtaBytes - (int)sizeof(BackwardShared);
+    return std::max(1, std::min(kMaxNormStages, std::min(kRingBytesSm / share, bytes) / row));
+}
 
 // by the stream's type X, one translation unit each (block_norm_f32.cu and so on)
 template <typename X>

@@ -13,8 +13,7 @@ cudaError_t launch_forward(const NormArgs &p, int dtype, cudaStream_t st)
     return with_dtype(dtype, [&](auto yt) {
         using Y = decltype(yt);
         const int ring = kRowStages * p.H * (int)(sizeof(X) + (p.y ? sizeof(Y) : 0) + (p.kind == kGateFull ? sizeof(Y) : 0));
-        // CTAs of an SM, by the registers that each bound leaves a thread (72 and 64): a wave and a quarter of them takes two
-        const int fit = std::min((threads <= 448 ? 896 : 1024) / threads, kRingBytesSm / ring);
+        const int fit = forward_ctas(threads, ring);
         // (three rows a CTA fill its ring; with fewer the kernel of one row a CTA begins sooner)
         if (fit >= 2 && p.T >= 3 * fit * num_sms())
             return launch_kernel(threads <= 448 ? norm_rows_kernel<X, Y, 448> : norm_rows_kernel<X, Y, 512>, dim3(fit * num_sms()),
@@ -31,7 +30,7 @@ cudaError_t launch_backward(NormArgs p, int dtype, int parts, cudaStream_t st)
         using Y = decltype(yt);
         const int row = (int)RowBytes(p, sizeof(X), sizeof(Y)).total();
         const int ctas = ctas_per_sm(p.H, heavy_backward(p));
-        p.stages = std::max(1, std::min(kMaxNormStages, kRingBytesSm / std::min((parts + 151) / 152, ctas) / row));
+        p.stages = backward_stages(row, parts, ctas);
         const auto go = [&](auto kind, auto post, auto pre) {
             constexpr int KIND = decltype(kind)::value;
             constexpr bool POST = decltype(post)::value, PRE = decltype(pre)::value;
