@@ -348,8 +348,9 @@ size_t moe_block_norm_workspace_size(int T, int H);
  *   offsets [segments+1] int32 in order within [0, T] and ids [segments] int32, on the device: one
  *   segment a request, of any length, an adapter any number of times.  ids -1: no adapter,
  *   y = base.  Rows in no segment are left untouched.
- *   A segment whose offsets are out of order or past the rows is skipped, and recorded; one whose id is
- *   no adapter becomes NaN, and is recorded (moe_check_errors).
+ *   An offset out of order or outside [0, T] is recorded (moe_check_errors).  The segments that it begins or
+ *   ends are skipped, and so may be any others of a list that holds one: their rows, whole tiles of them, are left
+ *   as they were.  The rows of a segment whose id is no adapter become NaN, and that is recorded.
  *   K, N multiples of 8 in [8, 65536], rank a multiple of 8 in [8, 128] (smaller ones padded with
  *   zeros), adapters in [1, 2^16], adapters * N below 2^31, segments in [1, 2^20], T in [0, 2^24], rows of x 16-byte aligned.
  *   workspace: moe_adapter_workspace_size(T, rank) bytes, first 256 zeroed once.  With less, the

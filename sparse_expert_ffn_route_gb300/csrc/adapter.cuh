@@ -25,6 +25,8 @@ struct AdapterArgs {
 
 // Tiles of `rows` rows on a fixed grid over the batch, cut by the segments: the part of grid cell c that is
 // segment s's is tile c + s.  (A later part has a later cell or a later segment, so no two share a number.)
+// In a list whose offsets are not in order the search may miss a segment, whose tiles are then left out; a tile that is
+// found is a part of one segment within the rows, and no part has two numbers.
 struct Tile {
     int lo, hi;      // rows; empty where the number is not used
     int adapter;     // -1: none

@@ -237,3 +237,44 @@ def test_short_tiles_of_a_cluster(n, R):
     first = run(o)
     for _ in range(5):
         assert torch.equal(run(o), first)
+
+
+@pytest.mark.parametrize("n", [3, 200])
+@pytest.mark.parametrize("many", [False, True])
+def test_a_bad_offset_inside_a_list(n, many):
+    """What stands in no well-ordered segment stays as it was, and every other row has its result or what it held;
+    with runs of empty segments the search takes more than one step."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, down, up = (torch.randn(*s, generator=g, device="cuda").to(BF16) for s in ((4 * n, 64), (2, 8, 64), (2, 64, 8)))
+    base = torch.randn(4 * n, 64, generator=g, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def call(off):
+        y, ws = torch.full((4 * n, 64), 7.0, device="cuda"), moe.alloc_adapter_workspace(4 * n, 8)
+        moe.moe_adapter_matmul(x, down, up, None, i32(off), i32([i % 2 for i in range(len(off) - 1)]), y, ws, base=base)
+        return y, ws
+    for wrong in (5000000, -7, -2**31, 2**31 - 1, 4 * n + 1, 3 * n, 0):
+        off = [0, n, wrong, 2 * n, 3 * n]
+        if many:
+            off = [0] * 41 + off[:3] + [2 * n] * 50 + off[4:] + [3 * n] * 41
+        y, ws = call(off)
+        with pytest.raises(moe.MoeError):
+            moe.moe_check_errors(ws)
+        claims = [0] * (4 * n)
+        for a, b in zip(off, off[1:]):
+            if 0 <= a <= b <= 4 * n:
+                for r in range(a, b):
+                    claims[r] += 1
+        held = (y == 7).all(1).tolist()
+        assert all(h for h, c in zip(held, claims) if c == 0)
+        for i, (a, b) in enumerate(zip(off, off[1:])):
+            rows = [r for r in range(a, b) if claims[r] == 1 and not held[r]] if 0 <= a <= b <= 4 * n else []
+            if rows:
+                u = x[rows].double() @ down[i % 2].double().T
+                want = base[rows].double() + u @ up[i % 2].double().T
+                mag = (x[rows].double().abs() @ down[i % 2].double().abs().T) @ up[i % 2].double().abs().T
+                # sums of 64 and 8 terms, u as two 16-bit parts, the output's rounding
+                assert bool(((y[rows].double() - want).abs() <= (160 * pa.U + 2.0 ** -17) * mag + 4 * pa.U * want.abs()).all())
+    y, ws = call([0, n, n, 2 * n, 3 * n])      # the next call is right
+    moe.moe_check_errors(ws)
+    assert not (y[:3 * n] == 7).all(1).any() and (y[3 * n:] == 7).all()
