@@ -690,9 +690,9 @@ int moe_check_errors(void *workspace, size_t workspace_bytes, void *stream)
     if (flag & kErrBadExpertId) return fail(MOE_ERR_DEVICE, "an expert id outside [0, n_experts) was skipped");
     if (flag & kErrBadKeff) return fail(MOE_ERR_DEVICE, "a keff outside [0, top_k] was clamped");
     if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a bounded device-side wait gave up; the kernel stopped early and its outputs are incomplete");
-    if (flag & kErrBadOffsets) return fail(MOE_ERR_DEVICE, "a group whose offsets are out of order or past the rows was skipped");
+    if (flag & kErrBadOffsets) return fail(MOE_ERR_DEVICE, "offsets out of order or past the rows: what they bound was skipped (a balance loss is NaN)");
     if (flag & kErrBadToken) return fail(MOE_ERR_DEVICE, "a token index outside [0, T) was skipped");
-    if (flag & kErrBadAdapter) return fail(MOE_ERR_DEVICE, "an adapter index outside [-1, adapters) was skipped");
+    if (flag & kErrBadAdapter) return fail(MOE_ERR_DEVICE, "an adapter index outside [-1, adapters): its segment's rows are NaN");
     if (flag) return fail(MOE_ERR_DEVICE, "device error word 0x%x", flag);
     return ok();
 }

@@ -278,3 +278,12 @@ def test_a_bad_offset_inside_a_list(n, many):
     y, ws = call([0, n, n, 2 * n, 3 * n])      # the next call is right
     moe.moe_check_errors(ws)
     assert not (y[:3 * n] == 7).all(1).any() and (y[3 * n:] == 7).all()
+
+
+@pytest.mark.parametrize("n", [2, 200])
+def test_errors_say_what_became_of_the_rows(n):
+    o = make([n, n], [0, 5], 64, 64, 8, 2)
+    with pytest.raises(moe.MoeError, match="rows are NaN"):
+        run(o)
+    with pytest.raises(moe.MoeError, match="skipped"):
+        run(dict(o, offsets=[0, n, 2 * n + 1], ids=[0, 1]))

@@ -248,3 +248,9 @@ def test_the_same_again_and_in_a_graph():
         for a, b in zip(first, (loss, counts, tokens, d)):
             assert torch.equal(a, b.cpu())
     moe.moe_check_errors(ws)
+
+
+def test_the_error_of_wrong_offsets_names_the_loss():
+    o = make(40, 24, 3, 2)
+    with pytest.raises(moe.MoeError, match="loss is NaN"):
+        run(dict(o, offsets=[0, 30, 20]))
