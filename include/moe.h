@@ -307,7 +307,7 @@ size_t moe_gated_workspace_size(int T, int H, int F, int train);
  *   MOE_GATE_FULL [T][H].
  *   Without y (NULL; then no gate and no post_w) out = residual_scale * x: a first block's norm.
  *   out may be NULL (not written), pre_w and n both NULL (no norm), not all three.  post_w may be
- *   NULL.  out may be x itself and n may be y itself.
+ *   NULL.  out may be x itself and n may be y itself, where its rows are dense.
  *   kept [T][2] fp32 or NULL: the rows' two inverse norms, for moe_block_norm_backward.
  *   A row with mean square + eps = 0 normalises to zeros.  Sums and norms are in fp32.
  *   H a multiple of 8 in [8, 8192], T in [0, 2^24], eps finite and >= 0.

@@ -129,6 +129,8 @@ int moe_block_norm_forward(const void *x, long long ldx, int x_dtype, const void
     if (!n != !pre_w) return set_error(MOE_ERR_ARG, "n and pre_w go together");
     if (!n && !out) return set_error(MOE_ERR_ARG, "out and n are both NULL");
     NORM_PTR(x, 16);
+    if (T > 1 && ((out == x && ldx != H) || (n && n == y && ldy != H)))
+        return set_error(MOE_ERR_ARG, "out and n are dense: they cannot be an x or y of strided rows");
     if (off(out, 16) || off(n, 16)) return set_error(MOE_ERR_ALIGN, "out or n is not 16-byte aligned");
     if (off(kept, 8)) return set_error(MOE_ERR_ALIGN, "kept is not 8-byte aligned");
     if ((rc = require_device())) return rc;

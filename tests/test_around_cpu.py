@@ -262,3 +262,17 @@ def test_plain_balance_gradient(norm):
             weights = weights + (2.5 * (w / w.sum() if norm else w) * dw[t, :k]).sum()
     (0.7 * total + weights).backward()
     assert torch.allclose(d, x.grad, rtol=1e-10, atol=1e-13)
+
+
+def test_norm_in_place_needs_dense_rows(lib):
+    """out and n are dense: x or y with rows further apart cannot hold them."""
+    names = ("x", "ldx", "xd", "y", "ldy", "gate", "kind", "dt", "post", "pre", "eps", "a", "b", "T", "H", "out", "n", "kept", "st")
+    X, Y, O, N = (FAKE * i for i in (1, 2, 3, 4))
+    ok = [X, 64, 0, Y, 64, None, 0, 1, None, FAKE * 5, 1e-5, 1.0, 1.0, 4, 64, O, N, None, None]
+
+    def fwd(**kw):
+        return lib.moe_block_norm_forward(*[kw.get(k, v) for k, v in zip(names, ok)])
+    if not torch.cuda.is_available():
+        assert ready(fwd()) and ready(fwd(out=X, n=Y)) and ready(fwd(ldx=72, ldy=72))
+        assert ready(fwd(out=X, n=Y, T=1, ldx=72, ldy=72))
+    assert fwd(out=X, ldx=72) == moe.MOE_ERR_ARG and fwd(n=Y, ldy=72) == moe.MOE_ERR_ARG
