@@ -256,6 +256,7 @@ __device__ __forceinline__ void short_parts(const BalanceArgs &p, int first, int
 {
     const int warp = threadIdx.x / 32, wl = threadIdx.x % 32, lane = wl % G;
     const T *logits = static_cast<const T *>(p.logits);
+    int left = end - begin;   // sequences in order have no more tokens here; with others the loss is NaN, and this ends
     // (a lane looks at one of 32 sequences of the warp's, most of which may be empty)
     for (int s0 = first + warp; s0 <= last; s0 += 32 * kWarps) {
         const int my = s0 + wl * kWarps;
@@ -266,6 +267,7 @@ __device__ __forceinline__ void short_parts(const BalanceArgs &p, int first, int
         }
         for (unsigned some = __ballot_sync(0xffffffffu, my_lo < my_hi); some; some &= some - 1) {
             const int which = __ffs(some) - 1, lo = __shfl_sync(0xffffffffu, my_lo, which), hi = __shfl_sync(0xffffffffu, my_hi, which);
+            if ((left -= hi - lo) < 0) return;
             for (int e = wl; e < p.E; e += 32) count[e] = 0;
             __syncwarp();
             float sum[PER];

@@ -254,3 +254,35 @@ def test_the_error_of_wrong_offsets_names_the_loss():
     o = make(40, 24, 3, 2)
     with pytest.raises(moe.MoeError, match="loss is NaN"):
         run(dict(o, offsets=[0, 30, 20]))
+
+
+def test_sequences_over_one_another_end_soon():
+    """Every other one of 200000 sequences has all tokens: a wrong list, which costs no more than a walk over it."""
+    T, S, E = 100000, 200000, 64
+    cfg = moe.MoeConfig.make(64, E, 2, 64)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    l = torch.randn(T, E, generator=g, device="cuda")
+    ids, keff = l.topk(2, dim=1)[1].to(torch.int32), torch.full((T,), 2, dtype=torch.int32, device="cuda")
+    loss, tokens = torch.zeros(1, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda")
+    counts, ws = torch.empty(S, E, dtype=torch.int32, device="cuda"), moe.alloc_balance_workspace(cfg, T, S)
+    at = torch.arange(S + 1, device="cuda")
+
+    def time(off):
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            moe.moe_balance_forward(cfg, l, ids, keff, off, loss, counts, tokens, ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    good = time((at // 2).to(torch.int32))
+    moe.moe_check_errors(ws)
+    assert int(tokens.sum()) == T and float(loss) > 0
+    wrong = time((at % 2 * T).to(torch.int32))
+    assert loss.isnan().all()
+    with pytest.raises(moe.MoeError):
+        moe.moe_check_errors(ws)
+    # looking at all of its tokens for each sequence would be T / 2 times a row's work more
+    assert wrong <= 50 * good, (wrong, good)
