@@ -720,6 +720,7 @@ def alloc_adapter_workspace(T: int = 32768, rank: int = 64, device="cuda") -> to
     n = moe_adapter_workspace_size(T, rank)
     if n == 0:
         raise MoeError(MOE_ERR_SHAPE, "moe_adapter_workspace_size", "sizes outside the limits")
+    n = max(n, moe_adapter_workspace_size(128, 128))     # the least that the highest rank takes
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws

@@ -276,3 +276,11 @@ def test_norm_in_place_needs_dense_rows(lib):
         assert ready(fwd()) and ready(fwd(out=X, n=Y)) and ready(fwd(ldx=72, ldy=72))
         assert ready(fwd(out=X, n=Y, T=1, ldx=72, ldy=72))
     assert fwd(out=X, ldx=72) == moe.MOE_ERR_ARG and fwd(n=Y, ldy=72) == moe.MOE_ERR_ARG
+
+
+def test_an_adapter_workspace_serves_any_rank():
+    for T, R in ((0, 8), (1, 8), (128, 16), (4000, 64)):
+        n = moe.alloc_adapter_workspace(T, R, device="cpu").numel()
+        assert n >= moe.moe_adapter_workspace_size(T, R) and n >= moe.moe_adapter_workspace_size(128, 128)
+    with pytest.raises(moe.MoeError):
+        moe.alloc_adapter_workspace(4, 12, device="cpu")
