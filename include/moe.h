@@ -374,7 +374,8 @@ size_t moe_adapter_workspace_size(int T, int rank);
  *   logits [T][E] of dtype (fp32, bf16, fp16), ld elements between rows: the router's, before the
  *   bias.  -inf scores 0; a token of nothing but -inf adds nothing to P.
  *   ids [T][K], keff [T] as moe_route writes them.  valid [T] uint8 or NULL: tokens with 0 (padding)
- *   are not counted and their logits not read.  Tokens in no sequence are not counted.
+ *   are not counted: whatever their logits, ids and keff hold is not used (it is read, so it has to be there).  Tokens
+ *   in no sequence are not counted.
  *   cfg gives n_experts and top_k.  A kept id outside [0, E) is left out, a keff outside [0, K] clamped,
  *   and recorded.  Offsets out of order or outside [0, T] make the loss NaN, and are recorded.
  *   n_seq in [1, 2^20].  workspace: moe_balance_workspace_size(cfg, T, n_seq) bytes, first 256 zeroed
@@ -387,7 +388,7 @@ int moe_balance_forward(const moe_config *cfg, const void *logits, int dtype, lo
 /* Gradient of the logits from the balance loss and from the applied weights:
  *   dloss [1] fp32 (device) or NULL: the loss's gradient (its coefficient);
  *   dw [T][K] fp32 or NULL: the gradient of the weights w that moe_route writes, with
- *   cfg's norm_topk_prob and routed_scaling_factor; slots >= keff are not read.
+ *   cfg's norm_topk_prob and routed_scaling_factor; what slots >= keff hold is not used.
  *   The other operands as moe_balance_forward took them, counts and tokens as it wrote them (read with
  *   dloss).  The counts are constants and the choice has no gradient.
  *   dlogits [T][E] (dense) of grad_dtype, dtype or fp32, written in full: zero for tokens that are

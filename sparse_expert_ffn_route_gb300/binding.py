@@ -684,7 +684,7 @@ def moe_balance_forward(cfg, logits, ids, keff, seq_offsets, loss, counts, token
     """How evenly a routing loads the experts: counts [S][E] int32 (kept pairs of each sequence and expert),
     tokens [S] int32 (counted tokens) and loss [1] float32, from the router's logits [T][E] (float32, bfloat16 or
     float16; rows may be strided) and moe_route's ids [T][K], keff [T].  seq_offsets [S + 1] int32; valid [T] uint8
-    (None: all): tokens with 0 are left out."""
+    (None: all): tokens with 0 are left out, whatever their rows hold."""
     dev, T, S, operands = _routing(cfg, logits, ids, keff, seq_offsets, valid)
     rc = load_library().moe_balance_forward(
         *operands, _dense(loss, "loss", (1,), torch.float32, dev), _dense(counts, "counts", (S, cfg.n_experts), torch.int32, dev),

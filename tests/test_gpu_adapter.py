@@ -287,3 +287,20 @@ def test_errors_say_what_became_of_the_rows(n):
         run(o)
     with pytest.raises(moe.MoeError, match="skipped"):
         run(dict(o, offsets=[0, n, 2 * n + 1], ids=[0, 1]))
+
+
+@pytest.mark.parametrize("rows", [1, 128, 256])
+def test_the_least_workspace(rows):
+    """One or two tiles' rows a pass."""
+    o = make([100, 400, 3, 260], [1, 0, -1, 1], 264, 136, 24, 2, before=7, after=4)
+    want = run(o)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(moe.moe_adapter_workspace_size(rows, 24), dtype=torch.uint8, device="cuda")
+    for in_place in (False, True):
+        y = o["base"].clone() if in_place else torch.full_like(o["base"], 7.0)
+        moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y, ws,
+                               base=y if in_place else o["base"])
+        moe.moe_check_errors(ws)
+        assert torch.equal(y[7:-4], want[7:-4])
+    with pytest.raises(moe.MoeError):
+        moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y, ws[:-1])
