@@ -327,7 +327,8 @@ int moe_block_norm_forward(const void *x, long long ldx, int x_dtype, const void
  *   dx [T][H] x_dtype;  dy [T][H] dtype;  dpost, dpre [H] fp32, summed over the rows;
  *   dgate: [H] fp32 (MOE_GATE_CHANNEL), [T] fp32 (MOE_GATE_TOKEN), [T][H] dtype (MOE_GATE_FULL).
  * dx may be dout itself and dy may be dn itself.  T = 0 zeroes the sums over rows.
- *   workspace: moe_block_norm_workspace_size(T, H) bytes, first 256 zeroed once. */
+ *   workspace: moe_block_norm_workspace_size(T, H) bytes, first 256 zeroed once; for one call at a time
+ *   (the sums of dpost, dpre and dgate lie there between two kernels). */
 int moe_block_norm_backward(const void *x, long long ldx, int x_dtype, const void *y, long long ldy,
                             const void *gate, int gate_kind, int dtype, const float *post_w,
                             const float *pre_w, const float *kept, float residual_scale,

@@ -589,7 +589,7 @@ def moe_block_norm_workspace_size(T: int, H: int) -> int:
 
 
 def alloc_block_norm_workspace(T: int, H: int, device="cuda") -> torch.Tensor:
-    """Workspace of moe_block_norm_backward for T rows of H, its head zeroed."""
+    """Workspace of moe_block_norm_backward for T rows of H, its head zeroed; for one call at a time."""
     n = moe_block_norm_workspace_size(T, H)
     if n == 0:
         raise MoeError(MOE_ERR_SHAPE, "moe_block_norm_workspace_size", "sizes outside the limits")
