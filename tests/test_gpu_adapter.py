@@ -303,4 +303,5 @@ def test_the_least_workspace(rows):
         moe.moe_check_errors(ws)
         assert torch.equal(y[7:-4], want[7:-4])
     with pytest.raises(moe.MoeError):
-        moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y, ws[:-1])
+        moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y,
+                               ws[:moe.moe_adapter_workspace_size(128, 24) - 1])
