@@ -2,12 +2,13 @@
 //
 //   u = x down^T.  A cluster of up to 8 CTAs takes a tile (128 rows on the accumulator's lanes, the rank in its
 //   columns), each CTA a share of the inputs; the shares are added in rank order through distributed shared
-//   memory.  u goes to the workspace as two 16-bit numbers a value, a high and a low part, with the row's
-//   largest number brought to 2^13 (so that fp16 neither overflows nor loses the low part to its smallest
-//   numbers): 2^-17 of the row's largest is lost at most.
+//   memory.  u goes to the workspace in 16-bit parts, each what the ones before it leave, with the row's largest
+//   number brought to 2^13 (so that fp16 neither overflows nor loses the last part to its smallest numbers): three
+//   of bf16 where y is fp32, 2^-24 of the row's largest at most, and otherwise two, 2^-22 in fp16 and 2^-17 in bf16
+//   (for a y of 16 bits, whose own rounding takes 2^-9 or 2^-12 of it).
 //   y = base + scale u up^T.  A CTA takes a tile and a run of output columns, 128 bytes of a row at a time: u
 //   stays in its shared memory, up and base come by TMA, and a thread of the epilogue adds 64 consecutive bytes
-//   of a row and stores them.  The product of both parts costs nothing beside the memory.
+//   of a row and stores them.  The products of all parts cost nothing beside the memory.
 //
 // What they move is x once and base and y once: bound by memory.  Two CTAs stand on an SM (half of its shared
 // memory each) with a ring of copies in flight.  One kernel for both products, the clusters handing u on
@@ -39,6 +40,7 @@ constexpr int kMaxTileStages = 8;
 constexpr int kXBytes = kTileRows * 128;
 constexpr int kTmemCols = 128, kUpStep = 64;
 constexpr int kHalfSm = 112 * 1024;   // shared memory of a CTA where two stand on an SM
+constexpr int kMaxParts = 3;
 
 struct TileArgs {
     AdapterArgs p;
@@ -49,7 +51,8 @@ struct TileArgs {
     int chunks, slices;  // up: of the outputs' columns, CTAs of a tile
     int stages, stage_bytes;
     uint32_t idesc;      // without N
-    void *hi, *lo;       // [rows of the pass][r16]
+    int parts;           // of a value of u
+    void *u[kMaxParts];  // [rows of the pass][r16]
     float *back;         // what undoes a row's scaling
     int wide;            // y's rows lie on 32-byte boundaries
 };
@@ -58,7 +61,7 @@ struct TileArgs {
 // hold whatever was there; none of them is stored)
 constexpr int kShortRows = 32;
 struct TileMaps {
-    CUtensorMap a[2], b, c[2], d[2];   // x, down | base, up, hi, lo
+    CUtensorMap a[2], b, u[kMaxParts][2];   // x, down | base, up, u's parts
 };
 
 struct TileCtrl {
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
     }
     __syncwarp();
     cluster_sync();   // every CTA's sums are there
-    // this CTA's share of the rows: added over the cluster, two rows of a warp at a time, and cut into two 16-bit parts
+    // this CTA's share of the rows: added over the cluster, two rows of a warp at a time, and cut into 16-bit parts
     constexpr int kWarps = kDownThreads / 32, kAtOnce = 2;
     const int rows = min(kTileRows / a.splits, t.hi - t.lo - rank * (kTileRows / a.splits));
     for (int i0 = warp; i0 < rows; i0 += kWarps * kAtOnce) {
@@ -267,20 +270,23 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
             if (__any_sync(0xffffffffu, odd)) shift = 0;   // infinities and NaN stay what they are
             shift = max(-126, min(126, shift));
             const float by = __uint_as_float((uint32_t)(shift + 127) << 23);
-            union {
-                uint2 w;
-                T t[4];
-            } h, l;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                from_f32(h.t[j], v[j] * by);
-                const float had = to_f32(h.t[j]), rest = v[j] * by - had;
-                from_f32(l.t[j], fabsf(had) <= 3.4e38f ? rest : 0.0f);
-            }
             const size_t line = (size_t)(t.lo + rank * (kTileRows / a.splits) + i0 + n * kWarps - a.row0);
-            if (4 * lane < a.r16) {
-                *reinterpret_cast<uint2 *>(static_cast<T *>(a.hi) + line * a.r16 + 4 * lane) = h.w;
-                *reinterpret_cast<uint2 *>(static_cast<T *>(a.lo) + line * a.r16 + 4 * lane) = l.w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= by;
+#pragma unroll
+            for (int i = 0; i < kMaxParts; ++i) {
+                if (i == a.parts) break;
+                union {
+                    uint2 w;
+                    T t[4];
+                } part;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    from_f32(part.t[j], v[j]);
+                    const float had = to_f32(part.t[j]);
+                    v[j] = fabsf(had) <= 3.4e38f ? v[j] - had : 0.0f;
+                }
+                if (4 * lane < a.r16) *reinterpret_cast<uint2 *>(static_cast<T *>(a.u[i]) + line * a.r16 + 4 * lane) = part.w;
             }
             if (lane == 0) a.back[line] = __uint_as_float((uint32_t)(127 - shift) << 23);
         }
@@ -306,8 +312,8 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
     constexpr int NC = 2 * CW;           // of a chunk
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *ubuf = ring + a.stages * a.stage_bytes;   // hi, then lo
-    TileCtrl *c = reinterpret_cast<TileCtrl *>(ubuf + 2 * a.blocks * kXBytes);
+    uint8_t *ubuf = ring + a.stages * a.stage_bytes;   // part by part
+    TileCtrl *c = reinterpret_cast<TileCtrl *>(ubuf + a.parts * a.blocks * kXBytes);
     const AdapterArgs &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     const int slice = blockIdx.x % a.slices, index = blockIdx.x / a.slices;
@@ -356,11 +362,9 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
         pdl_wait();
         pdl_launch_dependents();
         const uint32_t bar = smem_u32(&c->ufull);
-        expect_tx(bar, 2 * a.blocks * row_bytes);
-        for (int b = 0; b < a.blocks; ++b) {
-            tma_2d(u0 + b * kXBytes, &maps.c[few], 64 * b, row0 - a.row0, bar);
-            tma_2d(u0 + (a.blocks + b) * kXBytes, &maps.d[few], 64 * b, row0 - a.row0, bar);
-        }
+        expect_tx(bar, a.parts * a.blocks * row_bytes);
+        for (int i = 0; i < a.parts; ++i)
+            for (int b = 0; b < a.blocks; ++b) tma_2d(u0 + (i * a.blocks + b) * kXBytes, &maps.u[i][few], 64 * b, row0 - a.row0, bar);
     } else if (warp == 2) {
         const uint32_t idesc = a.idesc | (uint32_t)(NC >> 3) << 17;
         pdl_wait();
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
             if (!(ok = wait(&c->full[at.s], at.phase))) break;
             tc::fence_after_sync();
             uint32_t first = 0;
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < a.parts; ++part)
                 for (int k = 0; k < a.r16; k += 16) {
                     const uint64_t ud = tc::sdesc_kmajor_sw128(u0 + (part * a.blocks + (k >> 6)) * kXBytes) + ((k & 63) >> 3);
                     const uint64_t wd = tc::sdesc_kmajor_sw128(r0 + at.s * a.stage_bytes + kXBytes + (k >> 6) * NC * 128) + ((k & 63) >> 3);
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
 }
 
 // bytes of the workspace for a row of a pass
-inline size_t row_bytes(int R) { return (size_t)(R + 15) / 16 * 16 * 4 + 4; }
+inline size_t row_bytes(int R) { return (size_t)(R + 15) / 16 * 16 * 2 * kMaxParts + 4; }
 
 // clusters of `size` CTAs of the first kernel that the current device runs at once, two CTAs an SM (the query counts one)
 template <typename T>
@@ -527,13 +531,12 @@ cudaError_t launch_pass(TileArgs a, int dtype, cudaStream_t st)
         }
     }
     a.stage_bytes = kXBytes + a.blocks * NC * 128;
-    const int ubytes = 2 * a.blocks * kXBytes;
+    const int ubytes = a.parts * a.blocks * kXBytes;
     a.stages = std::min(kMaxTileStages, ((a.blocks == 1 ? 1 : 2) * kHalfSm - 1024 - (int)sizeof(TileCtrl) - ubytes) / a.stage_bytes);
     a.wide = (((uintptr_t)p.N * sizeof(Y)) | (uintptr_t)p.y) % 32 == 0;
     if (p.base) both(m.a, p.base, (long long)p.N * sizeof(Y) / 2, (long long)p.N * sizeof(Y) / 2, p.T);
     if (e == cudaSuccess) e = rows_map(&m.b, p.up, 16, p.R, p.R, (long long)p.A * p.N, NC);
-    both(m.c, a.hi, a.r16, a.r16, rows);
-    both(m.d, a.lo, a.r16, a.r16, rows);
+    for (int i = 0; i < a.parts; ++i) both(m.u[i], a.u[i], a.r16, a.r16, rows);
     if (e != cudaSuccess) return e;
     return launch_kernel(adapter_up_kernel<T, Y>, dim3((unsigned)tiles * a.slices), dim3(kUpThreads),
                          1024 + (size_t)a.stages * a.stage_bytes + ubytes + sizeof(TileCtrl), st, 1, a, m);
@@ -554,9 +557,9 @@ cudaError_t launch_tiles(const AdapterArgs &p, int dtype, void *workspace, size_
         a.cell1 = (int)std::min(cells, c + each);
         a.row0 = (int)c * kTileRows;
         const size_t part = (size_t)each * kTileRows * ((p.R + 15) / 16 * 16) * 2;
-        a.hi = ws;
-        a.lo = ws + part;
-        a.back = reinterpret_cast<float *>(ws + 2 * part);
+        a.parts = sizeof(Y) == 4 && dtype == MOE_DTYPE_BF16 ? 3 : 2;
+        for (int i = 0; i < kMaxParts; ++i) a.u[i] = ws + i * part;
+        a.back = reinterpret_cast<float *>(ws + kMaxParts * part);
         const cudaError_t e = launch_pass<T, Y>(a, dtype, st);
         if (e != cudaSuccess) return e;
     }

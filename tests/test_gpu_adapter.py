@@ -305,3 +305,24 @@ def test_the_least_workspace(rows):
     with pytest.raises(moe.MoeError):
         moe.moe_adapter_matmul(o["x"], o["down"], o["up"], o["scale"], i32(o["offsets"]), i32(o["ids"]), y,
                                ws[:moe.moe_adapter_workspace_size(128, 24) - 1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lengths,R", [([300, 140], 24), ([500], 128), ([2, 1], 24)])
+def test_what_stands_between_the_products_keeps_its_digits(dtype, lengths, R):
+    """Sums of more digits than one or two 16-bit numbers of bf16 hold, each handed on to an fp32 output as it is.
+    All of them are whole numbers below 2^24, whatever order they are added in: exact."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+    T, S, K, N = sum(lengths), len(lengths), 1024, 264
+    draw = lambda *s: torch.randint(-100, 101, s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, down, base = draw(T, K), draw(S, R, K), draw(T, N).float()
+    up = torch.zeros(S, N, R, dtype=dtype, device="cuda")
+    n = torch.arange(N, device="cuda")
+    up[:, n, n % R] = (1 - 2 * (n // R % 2)).to(dtype)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    off = [sum(lengths[:i]) for i in range(S + 1)]
+    y, ws = torch.empty(T, N, device="cuda"), moe.alloc_adapter_workspace(T, R)
+    moe.moe_adapter_matmul(x, down, up, None, i32(off), i32(list(range(S))), y, ws, base=base)
+    moe.moe_check_errors(ws)
+    want, _ = pa.adapter(x.double(), down.double(), up.double(), None, off, range(S), torch.zeros_like(base, dtype=torch.float64), base.double())
+    assert float(want.abs().max()) > 2 ** 17 and torch.equal(y.double(), want)
