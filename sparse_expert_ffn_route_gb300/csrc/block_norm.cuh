@@ -568,7 +568,7 @@ inline int norm_threads(int H, int vecs) { return ((H / 8 + vecs - 1) / vecs + 3
 // where what a thread holds allows it (`heavy`, 0 to 2): both directions of 8192 rows in bf16, two and one, of 3584 without a
 // gate 114 us and 138, with a channel's 155 and 156 (fp32 stream 198 and 184), of 4096 without post 110 and 125, without pre
 // 101 and 119, with both 140 and 143 (fp32 stream 201 and 195), with a channel's gate too 231 and 164.
-// CTAs of one warp: 24 (65536 rows of 256 92 us, with 8 of them 138); of more, 8 (65536 of 512 with 12 155, with 8 150).
+// CTAs of one warp: 24 (65536 rows of 256 85 us, with 8 of them 138); of more, 8 (65536 of 512 with 12 155, with 8 150).
 inline int ctas_per_sm(int H, int heavy)
 {
     const int threads = norm_threads(H, 1);
