@@ -191,19 +191,22 @@ cudaError_t launch_few(const AdapterArgs &p, int dtype, int y_dtype, cudaStream_
 // and with a tile's products; a tile of 128 rows costs its copies whatever stands in it.  Measured, clusters and tiles
 // (rows, segments, K, N, rank): 1, 1, 2048, 6144, 16: 4.8, 6.9; 1, 1, 6144, 6144, 64: 10.3, 8.6; 64, 64, 6144, 2048, 16: 7.1,
 // 17.2; 64, 64, 6144, 6144, 64: 25.7, 31.8; 64, 16, 6144, 6144, 64: 24.9, 13.6; 128, 16, 6144, 2048, 16: 8.9, 10.6; 256, 64,
-// 6144, 2048, 16: 14.8, 16.9; 256, 64, 6144, 6144, 64: 58.1, 30.5; 256, 256, 6144, 6144, 16: 27.2, 86.1.
-bool few_rows(const AdapterArgs &p)
+// 6144, 2048, 16: 14.8, 16.9; 256, 64, 6144, 6144, 64: 58.1, 30.5; 256, 256, 6144, 6144, 16: 27.2, 86.1.  An fp32 y
+// costs the tiles more columns' chunks, and with bf16 operands a third part of u, the clusters nothing (bf16, fp32 y): 1, 1, 6144,
+// 6144, 64: 9.7, 11.2; 1, 1, 4096, 4096, 64: 7.5, 9.1; 1, 1, 6144, 6144, 128: 16.0, 13.3; 4, 1, 2048, 2048, 64: 8.8, 7.1.
+bool few_rows(const AdapterArgs &p, int dtype, int y_dtype)
 {
     const double each = std::max(1.0, (double)p.T / p.S), rows = std::min(each, (double)kFewRows);
     const double sms = p.S * std::ceil(each / kFewRows) * kFewCluster / num_sms(), work = (double)p.R * (p.K + p.N) / 1e5;
     const double few = 4 + 0.5 * sms + std::max(1.0, sms) * work * (0.45 + 0.35 * rows);
-    const double tiles = 6 + 2.1e-4 * (p.K + p.N) + (p.S + (double)p.T / adapter::kTileRows) * (0.02 + 2.2e-5 * (p.K + p.N));
+    const double wide = y_dtype == MOE_DTYPE_F32 ? 2.3e-4 + (dtype == MOE_DTYPE_BF16 ? 5e-5 + 2e-6 * p.R : 0) : 0;
+    const double tiles = 6 + 2.1e-4 * (p.K + p.N) + wide * p.N + (p.S + (double)p.T / adapter::kTileRows) * (0.02 + 2.2e-5 * (p.K + p.N));
     return few < tiles;
 }
 
 cudaError_t launch_adapter(const AdapterArgs &p, int dtype, int y_dtype, void *workspace, size_t bytes, cudaStream_t st)
 {
-    if (few_rows(p)) return launch_few(p, dtype, y_dtype, st);
+    if (few_rows(p, dtype, y_dtype)) return launch_few(p, dtype, y_dtype, st);
     return with_half(dtype, [&](auto t) {
         return with_dtype(y_dtype, [&](auto y) { return adapter::launch_tiles<decltype(t), decltype(y)>(p, dtype, workspace, bytes, st); });
     });
