@@ -345,7 +345,7 @@ size_t moe_block_norm_workspace_size(int T, int H);
  *   x [T][K] with ldx elements between rows, down [adapters][rank][K], up [adapters][N][rank], all
  *   bf16 or all fp16 (dtype); scale [adapters] fp32 or NULL (1); sums in fp32.
  *   What stands between the two products is fp32 where segments are short, and where they are long is held in
- *   16-bit parts: to 2^-24 of the row's largest (2^-22 in fp16), for bf16 and a y of 16 bits to 2^-17.
+ *   16-bit parts: bf16 to 2^-24 (with a y of 16 bits to 2^-17), fp16 to 2^-22 of the row's largest.
  *   base, y [T][N] of y_dtype (fp32, bf16 or fp16), rounded once.  base: the shared projection's
  *   output; y itself (added in place) or NULL (zero).
  *   offsets [segments+1] int32 in order within [0, T] and ids [segments] int32, on the device: one

@@ -2,10 +2,10 @@
 //
 //   u = x down^T.  A cluster of up to 8 CTAs takes a tile (128 rows on the accumulator's lanes, the rank in its
 //   columns), each CTA a share of the inputs; the shares are added in rank order through distributed shared
-//   memory.  u goes to the workspace in 16-bit parts, each what the ones before it leave, with the row's largest
-//   number brought to 2^13 (so that fp16 neither overflows nor loses the last part to its smallest numbers): three
-//   of bf16 where y is fp32, 2^-24 of the row's largest at most, and otherwise two, 2^-22 in fp16 and 2^-17 in bf16
-//   (for a y of 16 bits, whose own rounding takes 2^-9 or 2^-12 of it).
+//   memory.  u goes to the workspace in 16-bit parts, each what the ones before it leave: three of bf16 where y is
+//   fp32, 2^-24 of the number at most, and otherwise two, 2^-17 in bf16 (for a y of 16 bits, whose own rounding
+//   takes 2^-9 or 2^-12) and 2^-22 of the row's largest in fp16, which has it brought to 2^13 (so as neither to
+//   overflow nor to lose the last part to the smallest numbers) and its sums brought back before the adapter's factor.
 //   y = base + scale u up^T.  A CTA takes a tile and a run of output columns, 128 bytes of a row at a time: u
 //   stays in its shared memory, up and base come by TMA, and a thread of the epilogue adds 64 consecutive bytes
 //   of a row and stores them.  Two parts' products cost nothing beside the memory; a third takes 0 to 5 % at ranks up
@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "adapter.cuh"
 #include "gemm_tc.cuh"
@@ -43,6 +44,9 @@ constexpr int kXBytes = kTileRows * 128;
 constexpr int kTmemCols = 128, kUpStep = 64;
 constexpr int kHalfSm = 112 * 1024;   // shared memory of a CTA where two stand on an SM
 constexpr int kMaxParts = 3;
+// fp32's range is bf16's, but not fp16's
+template <typename T>
+constexpr bool kBroughtUp = std::is_same<T, __half>::value;
 
 struct TileArgs {
     AdapterArgs p;
@@ -55,7 +59,7 @@ struct TileArgs {
     uint32_t idesc;      // without N
     int parts;           // of a value of u
     void *u[kMaxParts];  // [rows of the pass][r16]
-    float *back;         // what undoes a row's scaling
+    float *back;         // fp16: what undoes a row's scaling
     int wide;            // y's rows lie on 32-byte boundaries
 };
 
@@ -96,9 +100,9 @@ __device__ __forceinline__ void store64(char *p, const uint32_t (&w)[16], int n,
     }
 }
 
-// had + scale * v of consecutive columns, in place
-template <typename Y>
-__device__ __forceinline__ void add_columns(uint32_t (&w)[sizeof(Y) * 4], const uint32_t (&v)[16], float scale)
+// had + scale * (back * v) of consecutive columns, in place
+template <typename Y, bool BACK>
+__device__ __forceinline__ void add_columns(uint32_t (&w)[sizeof(Y) * 4], const uint32_t (&v)[16], float scale, float back)
 {
     union {
         uint32_t w;
@@ -109,7 +113,10 @@ __device__ __forceinline__ void add_columns(uint32_t (&w)[sizeof(Y) * 4], const 
     for (int i = 0; i < 16 / N; ++i) {
         u.w = w[i];
 #pragma unroll
-        for (int j = 0; j < N; ++j) from_f32(u.y[j], fmaf(scale, __uint_as_float(v[i * N + j]), to_f32(u.y[j])));
+        for (int j = 0; j < N; ++j) {
+            const float sum = __uint_as_float(v[i * N + j]);
+            from_f32(u.y[j], fmaf(scale, BACK ? back * sum : sum, to_f32(u.y[j])));
+        }
         w[i] = u.w;
     }
 }
@@ -260,21 +267,24 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
                         v[2] += w[n][q].z;
                         v[3] += w[n][q].w;
                     }
-            float top = 0.0f;
-            bool odd = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                top = fmaxf(top, fabsf(v[j]));
-                odd |= !(fabsf(v[j]) <= 3.4e38f);
-            }
-            const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            int shift = bits == 0 ? 0 : 13 - ((int)(bits >> 23) - 127);
-            if (__any_sync(0xffffffffu, odd)) shift = 0;   // infinities and NaN stay what they are
-            shift = max(-126, min(126, shift));
-            const float by = __uint_as_float((uint32_t)(shift + 127) << 23);
             const size_t line = (size_t)(t.lo + rank * (kTileRows / a.splits) + i0 + n * kWarps - a.row0);
+            if constexpr (kBroughtUp<T>) {
+                float top = 0.0f;
+                bool odd = false;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] *= by;
+                for (int j = 0; j < 4; ++j) {
+                    top = fmaxf(top, fabsf(v[j]));
+                    odd |= !(fabsf(v[j]) <= 3.4e38f);
+                }
+                const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                int shift = bits == 0 ? 0 : 13 - ((int)(bits >> 23) - 127);
+                if (__any_sync(0xffffffffu, odd)) shift = 0;   // infinities and NaN stay what they are
+                shift = max(-126, min(126, shift));
+                const float by = __uint_as_float((uint32_t)(shift + 127) << 23);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] *= by;
+                if (lane == 0) a.back[line] = __uint_as_float((uint32_t)(127 - shift) << 23);
+            }
 #pragma unroll
             for (int i = 0; i < kMaxParts; ++i) {
                 if (i == a.parts) break;
@@ -290,7 +300,6 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_kernel(const __g
                 }
                 if (4 * lane < a.r16) *reinterpret_cast<uint2 *>(static_cast<T *>(a.u[i]) + line * a.r16 + 4 * lane) = part.w;
             }
-            if (lane == 0) a.back[line] = __uint_as_float((uint32_t)(127 - shift) << 23);
         }
     }
     __syncwarp();
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
         pdl_wait();
         const int part = (warp - kFirstEpi) >> 2, local = (warp & 3) * 32 + lane, row = t.lo + local;
         const bool on = row < t.hi;
-        const float scale = on ? (p.scale ? p.scale[adapter] : 1.0f) * a.back[row - a.row0] : 0.0f;
+        const float scale = p.scale ? p.scale[adapter] : 1.0f, back = kBroughtUp<T> && on ? a.back[row - a.row0] : 1.0f;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + part * CW;
         char *line = static_cast<char *>(p.y) + ((size_t)row * p.N + part * CW) * sizeof(Y);
         for (int j = 0; j < nchunks; ++j, at.next(a.stages)) {
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_kernel(const __grid_
                     if (lane == 0) mbar_arrive(&c->dempty[buf]);
                 }
                 constexpr int W = sizeof(Y) * 4;   // words of 16 columns
-                add_columns<Y>(*reinterpret_cast<uint32_t(*)[W]>(&w[h / 16 * W]), v, scale);
+                add_columns<Y, kBroughtUp<T>>(*reinterpret_cast<uint32_t(*)[W]>(&w[h / 16 * W]), v, scale, back);
             }
             const int n = (chunk0 + j) * NC;
             if (on) store64(line + (size_t)n * sizeof(Y), w, (p.N - n - part * CW) / (CW / 4), a.wide);

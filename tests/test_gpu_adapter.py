@@ -326,3 +326,18 @@ def test_what_stands_between_the_products_keeps_its_digits(dtype, lengths, R):
     moe.moe_check_errors(ws)
     want, _ = pa.adapter(x.double(), down.double(), up.double(), None, off, range(S), torch.zeros_like(base, dtype=torch.float64), base.double())
     assert float(want.abs().max()) > 2 ** 17 and torch.equal(y.double(), want)
+
+
+@pytest.mark.parametrize("n", [2, 300])
+@pytest.mark.parametrize("dtype,x,up,scale", [(BF16, 1e-20, 1e35, 1.0), (BF16, 1e25, 1e-25, 1e10), (BF16, 1e-25, 1e25, 1e-15),
+                                              (BF16, 1e30, 1e-30, 1e7), (F16, 1e3, 1e-3, 1e36), (F16, 1e-3, 1e3, 1e-36),
+                                              (F16, 1e5, 1e-6, 1e38)])
+def test_factors_far_from_one(n, dtype, x, up, scale):
+    """Sums, factors and results within fp32's range, the products of some of them beyond it."""
+    o = make([n, n], [0, 1], 256, 136, 16, 2, dtype, F32)
+    o["x"], o["up"] = (o["x"].double().abs() * x).to(dtype), (o["up"].double() * up).to(dtype)
+    o["down"].abs_()
+    o["scale"] = torch.full((2,), scale, device="cuda")
+    o["base"] *= 0
+    check(o)
+    check(o, base="none")
